@@ -14,6 +14,9 @@ Entry points (same names as the C ABI):
   sconv_paged_fused    -- paged sliding-window cache insert + conv
   sconv_paged_fused_multi -- several conv streams sharing one paged cache
   sconv_seq_metadata   -- per-token (request, first row) buffers
+  gdr_fwd_varlen       -- the gated delta rule over a packed varlen batch
+  gdr_update           -- its decode update, with the speculative options
+  sconv_verify_drafts  -- which drafted tokens stand (num_accepted_tokens)
 bind_fwd_varlen and bind_update_decode marshal a forward or a decode step
 once for repeated launches.
 """
@@ -26,7 +29,7 @@ import torch
 
 __all__ = ["conv1d_fwd_varlen", "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
            "sconv_paged_fused_multi", "sconv_seq_metadata", "new_output", "bind_fwd_varlen",
-           "bind_update_decode",
+           "bind_update_decode", "gdr_fwd_varlen", "gdr_update", "sconv_verify_drafts",
            "SconvError", "library_path", "load_library", "exported_symbols",
            "version", "status_string"]
 
@@ -83,8 +86,21 @@ def load_library(path: str | None = None):
     lib.sconv_paged_fused_multi.argtypes = [
         I32, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I32, I32, I32,
         P, P, P, I32, P, I64, I32, I64, I32, I32, I32, P]
+    F32 = ctypes.c_float
+    lib.gdr_fwd_varlen.argtypes = [
+        *([P, I64, I64, I64] * 3), *([P, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
+        P, P, P, I32, I64, I32, I32, I32, I32, F32, I32, I32, P, I64, I64, I64, P]
+    lib.gdr_update.argtypes = [
+        *([P, I64, I64, I64, I64] * 3), *([P, I64, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
+        P, I64, I64, I32, P, P, I64, I64, I32, I32, I32, I32, I32, I32, F32, I32, I32,
+        P, I64, I64, I64, I64, P]
+    lib.sconv_verify_drafts.argtypes = [
+        P, P, P, I64, P, I64, P, P, I32, I32, I32, I32, P, I64, P, P, I64, P]
+    lib.sconv_verify_workspace_bytes.argtypes = [I32, I32]
+    lib.sconv_verify_workspace_bytes.restype = I64
     for f in (lib.conv1d_fwd_varlen, lib.conv1d_update_decode, lib.conv1d_update,
-              lib.sconv_paged_fused, lib.sconv_paged_fused_multi, lib.sconv_seq_metadata):
+              lib.sconv_paged_fused, lib.sconv_paged_fused_multi, lib.sconv_seq_metadata,
+              lib.gdr_fwd_varlen, lib.gdr_update, lib.sconv_verify_drafts):
         f.restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -94,7 +110,8 @@ def load_library(path: str | None = None):
 def exported_symbols() -> list[str]:
     return ["sconv_status_string", "sconv_version", "conv1d_fwd_varlen",
             "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
-            "sconv_paged_fused_multi", "sconv_seq_metadata"]
+            "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen", "gdr_update",
+            "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
 
 
 def version() -> tuple[int, int]:
@@ -523,3 +540,186 @@ def sconv_paged_fused_multi(xs, weights, cache, positions, slot_mapping, query_s
     )
     _launch("sconv_paged_fused_multi", dev, args)
     return outs
+
+
+# ------------------------------------------------------- gated delta rule --
+
+def _gdr_gates(g, beta, A_log, dt_bias, lead, hv, dev):
+    """The two gate tensors and the layer's parameters, checked and marshalled."""
+    if (A_log is None) != (dt_bias is None):
+        raise ValueError("A_log and dt_bias go together")
+    dt = torch.float32 if A_log is None else torch.bfloat16
+    if g.shape != (*lead, hv) or beta.shape != (*lead, hv):
+        raise ValueError("g and beta need one value per token and value head")
+    for t in (A_log, dt_bias):
+        if t is not None and (t.shape != (hv,) or (hv > 1 and t.stride(0) != 1)):
+            raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
+    return (_dev(g, dt, "g", dev), *g.stride(), _dev(beta, dt, "beta", dev), *beta.stride(),
+            _dev(A_log, torch.float32, "A_log", dev), _dev(dt_bias, torch.float32, "dt_bias", dev))
+
+
+def _gdr_shapes(q, k, v, state, out):
+    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("q and k need one shape, and v the same tokens")
+    hk, dk = q.shape[-2:]
+    hv, dv = v.shape[-2:]
+    if hk < 1 or hv % hk:
+        raise ValueError("v's heads must be a multiple of q's")
+    if state is not None and (state.dim() != 4 or state.shape[1:] != (hv, dv, dk)):
+        raise ValueError("state must be (lines, num_v_heads, head_dim_v, head_dim_k)")
+    if out.shape != v.shape:
+        raise ValueError("out must have v's shape")
+    return hk, hv, dk, dv
+
+
+def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
+                   has_initial_state=None, A_log=None, dt_bias=None, scale: float | None = None,
+                   use_qk_l2norm: bool = False, pad_slot_id: int = -1, out=None):
+    """The gated delta rule over a packed varlen batch: per value head and
+    token, S <- e^g S; S <- S + beta (v - S k) k^T; out = S q * scale.
+
+    q, k (T, num_k_heads, head_dim_k) and v (T, num_v_heads, head_dim_v) bf16,
+    any strides (views of a convolution's (T, dim) output take the vector
+    loads); g, beta (T, num_v_heads) fp32 log decay and write strength, or,
+    with A_log and dt_bias (num_v_heads,) fp32, the layer's bf16 projections a
+    and b (g = -exp(A_log) softplus(a + dt_bias), beta = sigmoid(b)); state
+    (lines, num_v_heads, head_dim_v, head_dim_k) fp32 or None, updated in
+    place; query_start_loc int32 (batch+1,), cache_indices int32 (batch,) or
+    None, has_initial_state bool (batch,) or None: as for conv1d_fwd_varlen.
+    scale defaults to head_dim_k ** -0.5.  Returns out (T, num_v_heads,
+    head_dim_v); rows of padded sequences are left as they are."""
+    dev = q.device
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be (T, heads, head_dim)")
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    hk, hv, dk, dv = _gdr_shapes(q, k, v, state, out)
+    total = q.shape[0]
+    batch = query_start_loc.numel() - 1
+    bf = torch.bfloat16
+    args = (
+        _dev(q, bf, "q", dev), *q.stride(), _dev(k, bf, "k", dev), *k.stride(),
+        _dev(v, bf, "v", dev), *v.stride(),
+        *_gdr_gates(g, beta, A_log, dt_bias, (total,), hv, dev),
+        _dev(state, torch.float32, "state", dev),
+        *(state.stride() if state is not None else (0, 0, 0, 0)),
+        state.shape[0] if state is not None else 0,
+        _index(cache_indices, torch.int32, "cache_indices", dev, batch),
+        _index(has_initial_state, torch.bool, "has_initial_state", dev, batch),
+        _index(query_start_loc, torch.int32, "query_start_loc", dev),
+        batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
+        1 if use_qk_l2norm else 0, pad_slot_id, _dev(out, bf, "out", dev), *out.stride(),
+    )
+    _launch("gdr_fwd_varlen", dev, args)
+    return out
+
+
+def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=None,
+               output_state_indices=None, A_log=None, dt_bias=None, scale: float | None = None,
+               use_qk_l2norm: bool = False, pad_slot_id: int = -1, out=None):
+    """Decode update of the gated delta rule: q, k (batch, num_k_heads,
+    head_dim_k) or (batch, seqlen, num_k_heads, head_dim_k), v and the gates
+    likewise (types as for gdr_fwd_varlen), state updated in place.
+
+    cache_indices int32 (batch,), or (batch, steps) with num_accepted_tokens
+    (batch,) int32: entry b then reads line cache_indices[b,
+    num_accepted_tokens[b] - 1].  output_state_indices int32 (batch, seqlen):
+    the lines that receive the state after each step, in place of the update
+    of the line that was read; the lines of one call are the next call's
+    cache_indices.  Returns out, shaped like v."""
+    dev = q.device
+    single = q.dim() == 3
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    ov = out
+    if single:
+        if v.dim() != 3 or g.dim() != 2 or beta.dim() != 2 or out.dim() != 3:
+            raise ValueError("q, k, v, g, beta and out must all be without a token dimension, or none")
+        q, k, v, g, beta, ov = (t.unsqueeze(1) for t in (q, k, v, g, beta, out))
+    elif q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be (batch, [seqlen,] heads, head_dim)")
+    if state is None:
+        raise ValueError("state is required")
+    hk, hv, dk, dv = _gdr_shapes(q, k, v, state, ov)
+    batch, seqlen = q.shape[:2]
+    ci, ci_st, steps = cache_indices, (0, 0), 1
+    if ci is not None:
+        if ci.dim() not in (1, 2) or ci.shape[0] < batch:
+            raise ValueError("cache_indices must be (batch,) or (batch, steps)")
+        if ci.dim() == 2:
+            ci_st, steps = ci.stride(), ci.shape[1]
+        else:
+            ci_st = (ci.stride(0), 0)
+    if num_accepted_tokens is not None and (ci is None or ci.dim() != 2):
+        raise ValueError("num_accepted_tokens needs cache_indices of (batch, steps)")
+    osi = output_state_indices
+    if osi is not None and (osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen):
+        raise ValueError("output_state_indices must be (batch, >= seqlen)")
+    bf, i32 = torch.bfloat16, torch.int32
+    args = (
+        _dev(q, bf, "q", dev), *q.stride(), _dev(k, bf, "k", dev), *k.stride(),
+        _dev(v, bf, "v", dev), *v.stride(),
+        *_gdr_gates(g, beta, A_log, dt_bias, (batch, seqlen), hv, dev),
+        _dev(state, torch.float32, "state", dev), *state.stride(), state.shape[0],
+        _dev(ci, i32, "cache_indices", dev), *ci_st, steps,
+        _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
+        _dev(osi, i32, "output_state_indices", dev), *(osi.stride() if osi is not None else (0, 0)),
+        batch, seqlen, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
+        1 if use_qk_l2norm else 0, pad_slot_id, _dev(ov, bf, "out", dev), *ov.stride(),
+    )
+    _launch("gdr_update", dev, args)
+    return out
+
+
+# ----------------------------------------------------- draft verification --
+
+def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs,
+                        accept_uniform, sample_uniform, max_drafts: int, tokens=None,
+                        num_accepted_tokens=None):
+    """Which drafted tokens stand, and the token drawn after them.
+
+    draft_tokens int32 (num_drafts,), request i's at draft_start_loc[i] ..
+    draft_start_loc[i+1] (int32 (batch+1,)), at most max_drafts each;
+    target_probs fp32 (num_drafts + batch, vocab), request i's rows at
+    draft_start_loc[i] + i; draft_probs fp32 (num_drafts, vocab), or None for
+    deterministic drafts; accept_uniform fp32 (num_drafts,) and sample_uniform
+    fp32 (batch,) in [0, 1).  Returns (tokens, num_accepted_tokens): int32
+    (batch, max_drafts + 1) with the standing drafts, the drawn token, then -1;
+    int32 (batch,) with standing drafts + 1, as conv1d_update and gdr_update
+    take it."""
+    dev = target_probs.device
+    batch = draft_start_loc.numel() - 1
+    nd = draft_tokens.numel()
+    if target_probs.dim() != 2 or target_probs.shape[0] < nd + batch:
+        raise ValueError("target_probs must be (num_drafts + batch, vocab)")
+    vocab = target_probs.shape[1]
+    if draft_probs is not None and (draft_probs.dim() != 2 or draft_probs.shape[0] < nd or
+                                    draft_probs.shape[1] != vocab):
+        raise ValueError("draft_probs must be (num_drafts, vocab)")
+    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
+        if t is not None and vocab > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have a unit vocabulary stride")
+    i32, f32 = torch.int32, torch.float32
+    if tokens is None:
+        tokens = torch.empty((max(batch, 0), max_drafts + 1), dtype=i32, device=dev)
+    if tokens.shape != (batch, max_drafts + 1) or tokens.stride(1) != 1:
+        raise ValueError("tokens must be (batch, max_drafts + 1) with a unit inner stride")
+    if num_accepted_tokens is None:
+        num_accepted_tokens = torch.empty((batch,), dtype=i32, device=dev)
+    ws_bytes = load_library().sconv_verify_workspace_bytes(batch, vocab)
+    ws = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+    args = (
+        _index(draft_tokens, i32, "draft_tokens", dev),
+        _index(draft_start_loc, i32, "draft_start_loc", dev),
+        _dev(target_probs, f32, "target_probs", dev), target_probs.stride(0),
+        _dev(draft_probs, f32, "draft_probs", dev),
+        draft_probs.stride(0) if draft_probs is not None else 0,
+        _index(accept_uniform, f32, "accept_uniform", dev, nd),
+        _index(sample_uniform, f32, "sample_uniform", dev, batch),
+        batch, nd, vocab, max_drafts,
+        _dev(tokens, i32, "tokens", dev), tokens.stride(0),
+        _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
+        _dev(ws, torch.uint8, "workspace", dev), ws_bytes,
+    )
+    _launch("sconv_verify_drafts", dev, args)
+    return tokens, num_accepted_tokens

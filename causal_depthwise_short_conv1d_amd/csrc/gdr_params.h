@@ -1,0 +1,70 @@
+// Kernel parameters of the gated delta rule and of draft verification, shared
+// by the host checks and the kernels.
+#pragma once
+
+#include <stdint.h>
+#include <hip/hip_runtime_api.h>
+
+namespace sconv {
+
+// One strided (sequence, token, head, channel) tensor.
+struct GdrTensor {
+    int64_t sb, st, sh, sd;    // element strides; sb is 0 for packed tokens
+};
+
+struct GdrParams {
+    const uint16_t *q, *k, *v;
+    uint16_t *out;
+    GdrTensor qs, ks, vs, os;
+    const void *gate, *beta;   // fp32, or bf16 when raw
+    GdrTensor gs, bs;          // (sd unused)
+    const float *a_log, *dt_bias;   // [Hv] when raw
+    float *state;              // [lines][Hv][Dv][Dk] or null
+    int64_t s_sl, s_sh, s_sv, s_sk;
+    int64_t num_lines;
+    int32_t batch;
+    int32_t Hk, Hv, Dk, Dv;
+    int32_t group;             // value heads per key head
+    int32_t raw, l2norm;
+    int32_t pad_slot_id;
+    float scale;
+    // packed prefill (qsl) or fixed-length entries (seqlen)
+    const int32_t *qsl;
+    const uint8_t *has_init;
+    int64_t total_T;
+    int32_t seqlen;
+    // decode: the line that an entry reads, and those that its steps write
+    const int32_t *ci;
+    int64_t ci_sb, ci_ss;
+    int32_t ci_steps;
+    const int32_t *accepted;
+    const int32_t *osi;
+    int64_t osi_sb, osi_ss;
+};
+
+struct VerifyParams {
+    const int32_t *draft_tokens;    // [num_drafts]
+    const int32_t *start;           // [batch + 1]
+    const float *p;                 // [num_drafts + batch][vocab]
+    int64_t p_sr;
+    const float *q;                 // [num_drafts][vocab] or null
+    int64_t q_sr;
+    const float *u_acc;             // [num_drafts]
+    const float *u_smp;             // [batch]
+    int32_t batch, num_drafts, vocab, max_drafts;
+    int32_t slice, slices;          // vocabulary entries per workgroup, workgroups per request
+    double *sums_ws;                // [batch][slices][2]
+    int32_t *tokens;                // [batch][max_drafts + 1]
+    int64_t t_sr;
+    int32_t *num_accepted;          // [batch]
+};
+
+// Launchers: each enqueues its kernels and returns hipGetLastError().
+// `vec`: unit channel strides, and every base and stride keeps four elements
+// together (8-byte bf16, 16-byte fp32 accesses).
+hipError_t launch_gdr_recurrent(const GdrParams &p, bool vec, hipStream_t s);
+hipError_t launch_verify_drafts(const VerifyParams &p, hipStream_t s);
+
+constexpr int kGdrMaxHeadK = 256;      // key channels a head of the recurrent kernel
+
+}  // namespace sconv

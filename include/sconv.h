@@ -1,7 +1,9 @@
 /*
  * sconv.h -- C ABI of libsconv, a gfx950 (MI355X) library for the causal
  * depthwise short convolution (width 2..5) used by hybrid / linear-attention
- * language models.
+ * language models, for the gated delta rule that such a layer feeds with the
+ * convolution's output, and for the verification of drafted tokens that
+ * yields the convolution's and the delta rule's num_accepted_tokens.
  *
  * The operation, in the notation of the pages it comes from:
  *
@@ -398,6 +400,143 @@ int sconv_paged_fused_multi(int32_t num_streams,
                             int32_t max_blocks, int64_t num_tokens, int32_t width,
                             int32_t activation, int32_t use_residual,
                             hipStream_t stream);
+
+/*
+ * The gated delta rule -- gdr_fwd_varlen (prefill) and gdr_update (decode).
+ *
+ * For value head h (key head h / (num_v_heads / num_k_heads)) with a state
+ * S[head_dim_v][head_dim_k] in fp32, per token:
+ *     S <- e^g S;   u = beta (v - S k);   S <- S + u k^T;   o = S q
+ * where q and k are first divided by sqrt(sum of squares + 1e-6) when
+ * qk_l2norm is non-zero, and q is multiplied by `scale`.  The state, all sums
+ * and the gates are in fp32 or more; o is rounded once to bf16.
+ *
+ * q, k         logical [.. tokens][num_k_heads][head_dim_k] bf16.
+ * v, out       logical [.. tokens][num_v_heads][head_dim_v] bf16.  q, k and v
+ *              may be views of one buffer, e.g. the rows of a convolution's
+ *              (T, dim) output.  out may overlap no input.
+ * gate, beta   logical [.. tokens][num_v_heads].  With a_log and dt_bias NULL:
+ *              fp32, the log decay g and the write strength beta.  With both
+ *              given (fp32 [num_v_heads]): bf16, the layer's two projections
+ *              a and b, and g = -exp(a_log) softplus(a + dt_bias),
+ *              beta = sigmoid(b).  g is at most 0; a larger value counts as 0.
+ * state        logical [num_cache_lines][num_v_heads][head_dim_v][head_dim_k]
+ *              fp32, any strides without two elements at one address.
+ * num_v_heads must be a multiple of num_k_heads and head_dim_k at most 256
+ *   (else SCONV_ERR_SHAPE).
+ * Layouts and speed (results agree to rounding): unit channel strides with
+ *   head_dim_k a multiple of 4 (decode) or of 8 (prefill) and rows aligned to
+ *   16 bytes take the vector loads; every other layout loads by elements.
+ * Errors: a NULL tensor, or one of a_log / dt_bias without the other ->
+ *   SCONV_ERR_NULL; bad sizes -> SCONV_ERR_SHAPE; a negative stride, or out /
+ *   state with two elements at one address -> SCONV_ERR_STRIDE; a pointer not
+ *   aligned to its elements -> SCONV_ERR_ALIGN; a scale that is not finite ->
+ *   SCONV_ERR_ARG; out or state overlapping an input or each other ->
+ *   SCONV_ERR_ALIAS.
+ */
+
+/*
+ * gdr_fwd_varlen -- the rule over a packed batch of variable-length sequences.
+ * cache_indices, has_initial_state, query_start_loc, pad_slot_id and
+ * total_tokens: as for conv1d_fwd_varlen.  The state of a sequence starts from
+ * its line when has_initial_state is set, else from zero, and is written back
+ * to its line (a sequence of no tokens writes nothing).  state may be NULL:
+ * zero states, none written.  Rows of skipped sequences and rows behind the
+ * last sequence are left untouched.
+ */
+int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, int64_t q_stride_dim,
+                   const void *k, int64_t k_stride_tok, int64_t k_stride_head, int64_t k_stride_dim,
+                   const void *v, int64_t v_stride_tok, int64_t v_stride_head, int64_t v_stride_dim,
+                   const void *gate, int64_t g_stride_tok, int64_t g_stride_head,
+                   const void *beta, int64_t b_stride_tok, int64_t b_stride_head,
+                   const float *a_log, const float *dt_bias,
+                   float *state, int64_t s_stride_line, int64_t s_stride_head,
+                   int64_t s_stride_v, int64_t s_stride_k, int64_t num_cache_lines,
+                   const int32_t *cache_indices, const uint8_t *has_initial_state,
+                   const int32_t *query_start_loc, int32_t batch, int64_t total_tokens,
+                   int32_t num_k_heads, int32_t num_v_heads, int32_t head_dim_k,
+                   int32_t head_dim_v, float scale, int32_t qk_l2norm, int32_t pad_slot_id,
+                   void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
+                   hipStream_t stream);
+
+/*
+ * gdr_update -- decode: each of `batch` entries feeds `seqlen` tokens, from the
+ * state of its line.
+ * cache_indices  int32, element (b, s) at cache_indices[b*ci_stride_seq +
+ *              s*ci_stride_step], ci_steps steps an entry.  Entry b reads the
+ *              line of step 0, or of step num_accepted_tokens[b] - 1 when that
+ *              array is given (so the lines to which the last call saved its
+ *              steps' states can be passed as they are).  NULL: line b.  An
+ *              entry whose line is pad_slot_id or outside [0,
+ *              num_cache_lines), or whose num_accepted_tokens is below 1 or
+ *              above ci_steps, is skipped (no output, no state).
+ * output_state_indices  [batch][seqlen] int32 or NULL, element (b, t) at
+ *              [b*osi_stride_seq + t*osi_stride_step]: a line in [0,
+ *              num_cache_lines) receives the state after step t; other values
+ *              write nothing.  When given, the line that was read keeps its
+ *              state unless it is named here; otherwise it receives the last
+ *              state.  A destination must not be a line that another entry of
+ *              the call reads or writes (the entry's own are fine: it reads
+ *              before it writes).
+ */
+int gdr_update(const void *q, int64_t q_stride_seq, int64_t q_stride_tok, int64_t q_stride_head,
+               int64_t q_stride_dim,
+               const void *k, int64_t k_stride_seq, int64_t k_stride_tok, int64_t k_stride_head,
+               int64_t k_stride_dim,
+               const void *v, int64_t v_stride_seq, int64_t v_stride_tok, int64_t v_stride_head,
+               int64_t v_stride_dim,
+               const void *gate, int64_t g_stride_seq, int64_t g_stride_tok, int64_t g_stride_head,
+               const void *beta, int64_t b_stride_seq, int64_t b_stride_tok, int64_t b_stride_head,
+               const float *a_log, const float *dt_bias,
+               float *state, int64_t s_stride_line, int64_t s_stride_head, int64_t s_stride_v,
+               int64_t s_stride_k, int64_t num_cache_lines,
+               const int32_t *cache_indices, int64_t ci_stride_seq, int64_t ci_stride_step,
+               int32_t ci_steps, const int32_t *num_accepted_tokens,
+               const int32_t *output_state_indices, int64_t osi_stride_seq,
+               int64_t osi_stride_step, int32_t batch, int32_t seqlen,
+               int32_t num_k_heads, int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v,
+               float scale, int32_t qk_l2norm, int32_t pad_slot_id,
+               void *out, int64_t o_stride_seq, int64_t o_stride_tok, int64_t o_stride_head,
+               int64_t o_stride_dim, hipStream_t stream);
+
+/*
+ * sconv_verify_drafts -- which drafted tokens stand, and the token after them,
+ * by rejection sampling from given uniform numbers in [0, 1).  Two kernels.
+ *
+ * Request i's drafts are draft_tokens[draft_start_loc[i] ..
+ * draft_start_loc[i+1]); n_i of them, at most max_drafts (more are not looked
+ * at).  Its target rows are target_probs[draft_start_loc[i] + i + j], j = 0 ..
+ * n_i: the target's distribution for draft j, and for the token after the
+ * last one.  Draft j stands while
+ *     accept_uniform * q(x) < p(x)      (p: its target row, q: its draft row,
+ *                                        x: the token; exact in fp64)
+ * and drafts after the first that does not are dropped.  A token outside
+ * [0, vocab) does not stand.  The token after them is drawn from
+ *     max(p - q, 0) of the refused draft's rows (from p when that is all 0), or
+ *     p of the row after the last draft when all stand:
+ * the smallest index whose running sum exceeds sample_uniform[i] times the
+ * total (fp64), at most the last index of positive mass; 0 when the row has no
+ * mass.  Entries that are not above zero (NaN included) have none.
+ * target_probs [num_drafts + batch][vocab] fp32, unit vocabulary stride.
+ * draft_probs  [num_drafts][vocab] fp32, or NULL: the drafts are deterministic,
+ *              q is 1 at the drafted token and 0 elsewhere.
+ * tokens       [batch][max_drafts + 1] int32: the standing drafts, the drawn
+ *              token, then -1.
+ * num_accepted_tokens  [batch] int32: standing drafts + 1, as conv1d_update
+ *              and gdr_update take it.
+ * workspace    device memory of sconv_verify_workspace_bytes(batch, vocab)
+ *              bytes, 8-byte aligned, in use until the call's work is done:
+ *              calls that may run at once need one each.
+ */
+int64_t sconv_verify_workspace_bytes(int32_t batch, int32_t vocab);
+
+int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_loc,
+                        const float *target_probs, int64_t p_stride_row,
+                        const float *draft_probs, int64_t q_stride_row,
+                        const float *accept_uniform, const float *sample_uniform,
+                        int32_t batch, int32_t num_drafts, int32_t vocab, int32_t max_drafts,
+                        int32_t *tokens, int64_t t_stride_row, int32_t *num_accepted_tokens,
+                        void *workspace, int64_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
