@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsconv.so")
 SOURCES = ["sconv_api.hip", "fwd_tokmajor.hip", "fwd_chanlast.hip", "general.hip",
            "update_decode.hip", "paged_fused.hip", "seq_metadata.hip", "gdr_api.hip",
-           "gdr_recurrent.hip", "verify_drafts.hip"]
+           "gdr_recurrent.hip", "gdr_chunk.hip", "verify_drafts.hip"]
 ARCH = os.environ.get("SCONV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

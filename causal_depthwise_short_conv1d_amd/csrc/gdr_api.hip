@@ -152,6 +152,15 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
     const int rc = check_gdr(p, 1, total_tokens, &vec);
     if (rc != SCONV_OK) return rc;
     p.group = p.Hv / p.Hk;
+    const int64_t T = total_tokens;
+    if (p.Dk <= kGdrMaxChunkK) {
+        const bool vec8 = p.Dk % 8 == 0 && p.qs.sd == 1 && p.ks.sd == 1 &&
+                          groups_of(q, 8, 2, {T, p.Hk}, {p.qs.st, p.qs.sh}) &&
+                          groups_of(k, 8, 2, {T, p.Hk}, {p.ks.st, p.ks.sh});
+        const bool svec = state && p.Dk % 4 == 0 && p.s_sk == 1 &&
+                          groups_of(state, 4, 4, {p.num_lines, p.Hv, p.Dv}, {p.s_sl, p.s_sh, p.s_sv});
+        return launch_status(launch_gdr_chunk(p, vec8, svec, stream));
+    }
     return launch_status(launch_gdr_recurrent(p, vec, stream));
 }
 

@@ -63,8 +63,12 @@ struct VerifyParams {
 // `vec`: unit channel strides, and every base and stride keeps four elements
 // together (8-byte bf16, 16-byte fp32 accesses).
 hipError_t launch_gdr_recurrent(const GdrParams &p, bool vec, hipStream_t s);
+// `vec`: unit channel strides of q and k, every base and stride a multiple of 8
+// elements; `svec`: the state's rows in 16-byte pieces.  Dk at most kGdrMaxChunkK.
+hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, hipStream_t s);
 hipError_t launch_verify_drafts(const VerifyParams &p, hipStream_t s);
 
 constexpr int kGdrMaxHeadK = 256;      // key channels a head of the recurrent kernel
+constexpr int kGdrMaxChunkK = 128;     // ... of the chunked kernel
 
 }  // namespace sconv
