@@ -15,6 +15,12 @@ import numpy as np
 import torch
 
 F64 = torch.float64
+# Chunks: a column's values of one 64-token chunk share power-of-two scales.
+# X, z and S lie below 2^15, their bounds above 2^14, and the bounds are at most
+# 128 times the chunk's largest (|v| + |u| |k| + 64 |S row|); an fp16 part is
+# rounded at 2^-25 at the least, so nothing is off by more than
+# 128 * 2^-25 / 2^14 = 2^-32 of that largest value, per token: E takes it in at
+# every token, an output 64 times.
 # one token at a time in fp32: 16..32 terms a lane and 3 exchanges in a sum,
 # twice in u, 3 for the update, the gate's e^g (|g| + 4 steps, |g| counted for
 # what is left of the state after it) and the norms' roots and quotients
@@ -49,7 +55,7 @@ class Row:
         self.E = torch.zeros(S.shape[:2], dtype=F64)
         self.W = torch.zeros(S.shape[:2], dtype=F64)
 
-    def step(self, q, k, v, g, beta):
+    def step(self, q, k, v, g, beta, floor=None):
         e = torch.exp(g)[:, None]
         before = self.S.norm(dim=-1)
         S = self.S * e[..., None]
@@ -57,10 +63,15 @@ class Row:
         self.S = S + u[..., None] * k[:, None]
         kn = k.norm(dim=-1)[:, None]
         self.E = e * self.E + self.c * 2.0 ** -24 * (v.abs() + 2 * e * before + 2 * u.abs() * kn)
+        if floor is not None:
+            self.E = self.E + floor
         self.W = e * self.W + u.abs() * kn
+        self.M = v.abs() + u.abs() * kn + 64 * before
         o = (self.S * q[:, None]).sum(-1)
         qn = q.norm(dim=-1)[:, None]
         tol = 2.0 ** -8 * o.abs() + qn * (self.E + self.f * (before + self.W)) * (1 + 2.0 ** -7) + 1e-38
+        if floor is not None:
+            tol = tol + 64 * qn * floor
         return o, tol
 
 
@@ -86,9 +97,15 @@ def fwd(q, k, v, g, beta, state, qsl, cache_indices, has_init, A_log, dt_bias, s
         S = torch.zeros(hv, dv, dk, dtype=F64)
         if st is not None and has_init is not None and bool(has_init[i]):
             S = state[line].to(F64)
-        r = Row(S, c, f)
+        r, look = Row(S, c, f), Row(S, c, f)
         for t in range(a, b):
-            out[t], otol[t] = r.step(qq[t], kk[t], vv[t], gg[t], bb[t])
+            if (t - a) % 64 == 0 and c == C_CHUNK:     # the chunk's largest values, for the floor of its scales
+                floor = torch.zeros(r.E.shape, dtype=F64)
+                for x in range(t, min(t + 64, b)):
+                    look.step(qq[x], kk[x], vv[x], gg[x], bb[x])
+                    floor = torch.maximum(floor, look.M)
+                floor = floor * 2.0 ** -32
+            out[t], otol[t] = r.step(qq[t], kk[t], vv[t], gg[t], bb[t], floor if c == C_CHUNK else None)
             live[t] = True
         if st is not None:
             st[line], stol[line] = r.S, r.E
