@@ -154,9 +154,11 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
     p.group = p.Hv / p.Hk;
     const int64_t T = total_tokens;
     if (p.Dk <= kGdrMaxChunkK) {
-        // 16-byte rows of q and k; a chunk's rows within the 31 bits of a descriptor's offsets
-        const auto near = [](const GdrTensor &t, int64_t d) { return 63 * t.st + (d - 1) * t.sd < (int64_t(1) << 29); };
-        const bool vec8 = near(p.qs, p.Dk) && near(p.ks, p.Dk) && near(p.vs, p.Dv) && near(p.os, p.Dv) && p.Dk % 8 == 0 && p.qs.sd == 1 && p.ks.sd == 1 &&
+        // 16-byte rows of q and k; rows longer than a head, a chunk's within the 31 bits of a descriptor's offsets
+        const auto rows = [](const GdrTensor &t, int64_t d) {
+            return t.sd < (1 << 24) && d * t.sd <= t.st && t.st < (1 << 23);
+        };
+        const bool vec8 = rows(p.qs, p.Dk) && rows(p.ks, p.Dk) && rows(p.vs, p.Dv) && rows(p.os, p.Dv) && p.Dk % 8 == 0 && p.qs.sd == 1 && p.ks.sd == 1 &&
                           groups_of(q, 8, 2, {T, p.Hk}, {p.qs.st, p.qs.sh}) &&
                           groups_of(k, 8, 2, {T, p.Hk}, {p.ks.st, p.ks.sh});
         const bool svec = state && p.Dk % 4 == 0 && p.s_sk == 1 &&
