@@ -131,7 +131,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], f16x8 &hi, f16x8 &lo
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const f16x2 h = cvt2(x[i], x[i + 1]);
-        const f16x2 l = cvt2(x[i] - float(h.x), x[i + 1] - float(h.y));
+        const f16x2 l = cvt2(fmaf(float(h.x), -1.0f, x[i]), fmaf(float(h.y), -1.0f, x[i + 1]));
         hi[i] = h.x; hi[i + 1] = h.y;
         lo[i] = l.x; lo[i + 1] = l.y;
     }
@@ -271,7 +271,7 @@ __device__ __forceinline__ void split4(const f32x4 &x, f16x4 &hi, f16x4 &lo) {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         const f16x2 h = cvt2(x[i], x[i + 1]);
-        const f16x2 l = cvt2(x[i] - float(h.x), x[i + 1] - float(h.y));
+        const f16x2 l = cvt2(fmaf(float(h.x), -1.0f, x[i]), fmaf(float(h.y), -1.0f, x[i + 1]));
         hi[i] = h.x; hi[i + 1] = h.y;
         lo[i] = l.x; lo[i + 1] = l.y;
     }
@@ -284,27 +284,39 @@ struct Prepare {
     const Span64 sp;
     const int lane0, w, h;
     const uint16_t *qh, *kh;
-    Quad next;                         // rows of the chunk to come
 
     // The first waves stage the keys, as many after them the queries: 4 KT threads a row, four rows a thread.
     static constexpr int kStage = KT;  // waves
     __device__ __forceinline__ int quad_of(int lane) const { return (64 * (w & (kStage - 1)) + lane) / (4 * KT); }
 
-    __device__ __forceinline__ void fetch(int64_t c0) {
+    __device__ __forceinline__ void stage(int64_t c0) {
         const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
-        if (w < kStage) next = load_quad<VEC>(kh, p.ks, sp, c0, quad, kc, p.Dk);
-        else if (w < 2 * kStage) next = load_quad<VEC>(qh, p.qs, sp, c0, quad, kc, p.Dk);
-    }
-    __device__ __forceinline__ void stage() {
-        const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
-        if (w < kStage) stage_quad<KT, true>(next, sh.t.k, sh.t.kt, sh.kf, quad, kc, 1.0f, p.l2norm);
-        else if (w < 2 * kStage) stage_quad<KT, false>(next, sh.t.q, nullptr, sh.t.qf, quad, kc, p.scale, p.l2norm);
+        if (w < kStage)
+            stage_quad<KT, true>(load_quad<VEC>(kh, p.ks, sp, c0, quad, kc, p.Dk), sh.t.k, sh.t.kt, sh.kf, quad, kc, 1.0f,
+                                 p.l2norm);
+        else if (w < 2 * kStage)
+            stage_quad<KT, false>(load_quad<VEC>(qh, p.qs, sp, c0, quad, kc, p.Dk), sh.t.q, nullptr, sh.t.qf, quad, kc,
+                                  p.scale, p.l2norm);
     }
 
-    // From the chunk's staged rows and its gates in LDS to its tiles; leaves the next chunk's gates there.
-    // `loads` starts what the passage through the chunk reads from memory, once the registers are free.
-    template <class F>
-    __device__ __forceinline__ void chunk(int64_t c0, bool more, F loads) {
+    // Reads one word of each 128-byte line that the chunk's rows will be read from: the lines wait in L2 and the
+    // registers stay free.  The caller keeps the word until the reads have had their time.
+    __device__ __forceinline__ uint32_t touch(int64_t c0, const uint16_t *vh, int32_t v0) {
+        uint32_t word = 0;
+        if constexpr (VEC) {
+            const int lane = fresh(lane0), i = 64 * (w & 1) + lane, r = i >> 1;
+            const int64_t left = sp.n - c0 < kC ? sp.n - c0 : kC;
+            const GdrTensor &ts = w < 2 ? p.ks : w < 4 ? p.qs : p.vs;
+            const uint16_t *base = (w < 2 ? kh : w < 4 ? qh : vh) + (sp.t0 + c0) * ts.st;
+            const int32_t first = w < 4 ? 0 : v0, end = w < 4 ? p.Dk : p.Dv, c = first + 64 * (i & 1);
+            if (w < 6 && c < end) word = buf_ld16(make_rsrc(base, left * ts.st * 2), uint32_t(r * ts.st + c * ts.sd) * 2);
+        }
+        return word;
+    }
+
+    // From the chunk's rows and its gates (in LDS) to its tiles; leaves the next chunk's gates there.
+    __device__ __forceinline__ void chunk(int64_t c0, bool more) {
+        stage(c0);
         __syncthreads();
         if (w < 4) key_products();
         else query_products();
@@ -314,7 +326,6 @@ struct Prepare {
         if (w == 7 && more) gates(c0 + kC);
         __syncthreads();
         if (w < 4) invert_rest();
-        loads();
         __syncthreads();
     }
 
@@ -510,7 +521,6 @@ struct Consumer {
     int32_t col;                       // this lane's channel
     f32x4 S[2 * KT];                   // the state times 2^un
     int un;
-    uint16_t v[16];                    // the chunk's values: [4 mt + i]
 
     // The state's rows in memory: this lane has channels 8 g + 4 t .. of each 32 of its value channel's row.
     template <class F>
@@ -575,7 +585,8 @@ struct Consumer {
         for (int r = 0; r < 16; ++r) f(r, at + uint32_t(tok_of(r >> 2, r & 3)) * row);
     }
 
-    __device__ __forceinline__ void fetch(int64_t t0) {
+    // The chunk's values: [4 mt + i].
+    __device__ __forceinline__ void fetch(int64_t t0, uint16_t (&v)[16]) {
         const int g = lane0 >> 4;
         if constexpr (VEC) {
             const Rsrc rs = rows(vh, t0, p.vs);
@@ -603,12 +614,8 @@ struct Consumer {
         }
     }
 
-    template <class F>
-    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b, F more) {
+    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b) {
         const int lane = fresh(lane0), g = lane >> 4;
-        uint32_t vp[8];                                // v in pairs: registers are what bounds this phase
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vp[i] = v[2 * i] | uint32_t(v[2 * i + 1]) << 16;
         // K S and Q S, the state split on the way (its largest element is below 2^15)
         f32x4 ak[4], aq[4];
 #pragma unroll
@@ -634,6 +641,8 @@ struct Consumer {
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+        uint16_t v[16];
+        fetch(t0, v);                                  // (from L2; registers are what bounds the products above)
         // X, scaled to 2^12
         float x[16], xm = 0.0f;
         const float unit = pow2(un);
@@ -643,11 +652,10 @@ struct Consumer {
             const f32x4 ka = *reinterpret_cast<const f32x4 *>(b.ka + t), kb = *reinterpret_cast<const f32x4 *>(b.kb + t);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * ((i & 1) ? bf_hi(vp[2 * mt + i / 2]) : bf_lo(vp[2 * mt + i / 2])));
+                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * bf_one(v[4 * mt + i]));
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
-        more();                                        // the next chunk's rows, into the registers of v
         const int ex = exp_of(max_groups(xm));
         const float xs = pow2(12 - ex);
 
@@ -779,7 +787,6 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     }
     const int hk = pl.h / p.group;
     Prepare<KT, VEC> pr{p, sh, sp, lane, wave, pl.h, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
-    pr.fetch(0);
     if (wave == 7) pr.gates(0);
 
     Consumer<KT, VEC> st{p, sp, lane};
@@ -792,12 +799,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     else st.clear();
 
     for (int64_t c = 0; c < nc; ++c) {
-        const bool more = c + 1 < nc;
-        pr.stage();
-        pr.chunk(c * kC, more, [&]() { if (work) st.fetch(c * kC); });
-        const auto ahead = [&]() { if (more) pr.fetch((c + 1) * kC); };
-        if (work) st.chunk(c * kC, sh.t, ahead);
-        else ahead();
+        pr.chunk(c * kC, c + 1 < nc);
+        uint32_t word = 0;
+        if (c + 1 < nc) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
+        if (work) st.chunk(c * kC, sh.t);
+        asm volatile("" : : "v"(word));
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
