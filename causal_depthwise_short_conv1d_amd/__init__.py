@@ -89,7 +89,9 @@ def load_library(path: str | None = None):
     F32 = ctypes.c_float
     lib.gdr_fwd_varlen.argtypes = [
         *([P, I64, I64, I64] * 3), *([P, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
-        P, P, P, I32, I64, I32, I32, I32, I32, F32, I32, I32, P, I64, I64, I64, P]
+        P, P, P, I32, I64, I32, I32, I32, I32, F32, I32, I32, P, I64, I64, I64, P, I64, P]
+    lib.gdr_fwd_workspace_bytes.argtypes = [I32, I64, I32, I32, I32, I32, I32]
+    lib.gdr_fwd_workspace_bytes.restype = I64
     lib.gdr_update.argtypes = [
         *([P, I64, I64, I64, I64] * 3), *([P, I64, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
         P, I64, I64, I32, P, P, I64, I64, I32, I32, I32, I32, I32, I32, F32, I32, I32,
@@ -110,8 +112,8 @@ def load_library(path: str | None = None):
 def exported_symbols() -> list[str]:
     return ["sconv_status_string", "sconv_version", "conv1d_fwd_varlen",
             "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
-            "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen", "gdr_update",
-            "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
+            "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen",
+            "gdr_fwd_workspace_bytes", "gdr_update", "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
 
 
 def version() -> tuple[int, int]:
@@ -610,6 +612,12 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
         batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
         1 if use_qk_l2norm else 0, pad_slot_id, _dev(out, bf, "out", dev), *out.stride(),
     )
+    vector = dk % 8 == 0 and q.stride(2) == 1 and k.stride(2) == 1 and all(
+        t.data_ptr() % 16 == 0 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 for t in (q, k)) and all(
+        t.stride(0) >= t.shape[2] * t.stride(2) for t in (q, k, v, out))
+    need = load_library().gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    args += (_dev(ws, torch.uint8, "workspace", dev), need)
     _launch("gdr_fwd_varlen", dev, args)
     return out
 

@@ -29,6 +29,29 @@ bool groups_of(const void *p, int n, int elem, std::initializer_list<int64_t> si
     return aligned(p, uintptr_t(n) * uintptr_t(elem));
 }
 
+Span span_of_out(const GdrParams &p, int64_t B, int64_t T) {
+    return span_of(p.out, {B, T, p.Hv, p.Dv}, {p.os.sb, p.os.st, p.os.sh, p.os.sd});
+}
+Span span_of_state(const GdrParams &p) {
+    return span_of(p.state, {p.num_lines, p.Hv, p.Dv, p.Dk}, {p.s_sl, p.s_sh, p.s_sv, p.s_sk}, 4);
+}
+// Whether what is written at `w` overlaps a tensor that the kernels read.
+bool overlaps_input(const GdrParams &p, int64_t B, int64_t T, const Span &w) {
+    const int gate_bytes = p.raw ? 2 : 4;
+    const Span in[] = {
+        span_of(p.q, {B, T, p.Hk, p.Dk}, {p.qs.sb, p.qs.st, p.qs.sh, p.qs.sd}),
+        span_of(p.k, {B, T, p.Hk, p.Dk}, {p.ks.sb, p.ks.st, p.ks.sh, p.ks.sd}),
+        span_of(p.v, {B, T, p.Hv, p.Dv}, {p.vs.sb, p.vs.st, p.vs.sh, p.vs.sd}),
+        span_of(p.gate, {B, T, p.Hv}, {p.gs.sb, p.gs.st, p.gs.sh}, gate_bytes),
+        span_of(p.beta, {B, T, p.Hv}, {p.bs.sb, p.bs.st, p.bs.sh}, gate_bytes),
+        span_of(p.a_log, {p.Hv}, {1}, 4),
+        span_of(p.dt_bias, {p.Hv}, {1}, 4),
+    };
+    for (const Span &s : in)
+        if (overlap(w, s)) return true;
+    return false;
+}
+
 // The checks that prefill and decode share; B and T are the sizes of the
 // sequence and token dimensions.
 int check_gdr(const GdrParams &p, int64_t B, int64_t T, bool *vec) {
@@ -55,20 +78,8 @@ int check_gdr(const GdrParams &p, int64_t B, int64_t T, bool *vec) {
         !aligned(p.accepted, 4) || !aligned(p.osi, 4))
         return SCONV_ERR_ALIGN;
 
-    const Span so = span_of(p.out, {B, T, p.Hv, p.Dv}, {p.os.sb, p.os.st, p.os.sh, p.os.sd});
-    const Span ss = span_of(p.state, {p.num_lines, p.Hv, p.Dv, p.Dk}, {p.s_sl, p.s_sh, p.s_sv, p.s_sk}, 4);
-    const Span in[] = {
-        span_of(p.q, {B, T, p.Hk, p.Dk}, {p.qs.sb, p.qs.st, p.qs.sh, p.qs.sd}),
-        span_of(p.k, {B, T, p.Hk, p.Dk}, {p.ks.sb, p.ks.st, p.ks.sh, p.ks.sd}),
-        span_of(p.v, {B, T, p.Hv, p.Dv}, {p.vs.sb, p.vs.st, p.vs.sh, p.vs.sd}),
-        span_of(p.gate, {B, T, p.Hv}, {p.gs.sb, p.gs.st, p.gs.sh}, gate_bytes),
-        span_of(p.beta, {B, T, p.Hv}, {p.bs.sb, p.bs.st, p.bs.sh}, gate_bytes),
-        span_of(p.a_log, {p.Hv}, {1}, 4),
-        span_of(p.dt_bias, {p.Hv}, {1}, 4),
-    };
-    if (overlap(so, ss)) return SCONV_ERR_ALIAS;
-    for (const Span &s : in)
-        if (overlap(so, s) || overlap(ss, s)) return SCONV_ERR_ALIAS;
+    const Span so = span_of_out(p, B, T), ss = span_of_state(p);
+    if (overlap(so, ss) || overlaps_input(p, B, T, so) || overlaps_input(p, B, T, ss)) return SCONV_ERR_ALIAS;
 
     // four elements at a time: 8-byte rows of q and k, 16-byte state rows
     *vec = p.Dk % 4 == 0 && p.qs.sd == 1 && p.ks.sd == 1 &&
@@ -107,7 +118,7 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
                    int32_t num_k_heads, int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v,
                    float scale, int32_t qk_l2norm, int32_t pad_slot_id,
                    void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
-                   hipStream_t stream) {
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (batch < 0 || total_tokens < 0 || total_tokens > INT32_MAX || num_cache_lines < 0)
         return SCONV_ERR_SHAPE;
     if (batch == 0 || total_tokens == 0) return SCONV_OK;
@@ -158,14 +169,35 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
         const auto rows = [](const GdrTensor &t, int64_t d) {
             return t.sd < (1 << 24) && d * t.sd <= t.st && t.st < (1 << 23);
         };
-        const bool vec8 = rows(p.qs, p.Dk) && rows(p.ks, p.Dk) && rows(p.vs, p.Dv) && rows(p.os, p.Dv) && p.Dk % 8 == 0 && p.qs.sd == 1 && p.ks.sd == 1 &&
+        const bool vec8 = rows(p.qs, p.Dk) && rows(p.ks, p.Dk) && rows(p.vs, p.Dv) && rows(p.os, p.Dv) && p.Dk % 8 == 0 &&
+                          p.qs.sd == 1 && p.ks.sd == 1 &&
                           groups_of(q, 8, 2, {T, p.Hk}, {p.qs.st, p.qs.sh}) &&
                           groups_of(k, 8, 2, {T, p.Hk}, {p.ks.st, p.ks.sh});
         const bool svec = state && p.Dk % 4 == 0 && p.s_sk == 1 &&
                           groups_of(state, 4, 4, {p.num_lines, p.Hv, p.Dv}, {p.s_sl, p.s_sh, p.s_sv});
-        return launch_status(launch_gdr_chunk(p, vec8, svec, stream));
+        const int64_t need = gdr_fwd_workspace_bytes(batch, T, p.Hk, p.Hv, p.Dk, p.Dv, vec8);
+        if (workspace && need > 0) {
+            if (!aligned(workspace, 16)) return SCONV_ERR_ALIGN;
+            if (workspace_bytes < need) return SCONV_ERR_SHAPE;
+            const Span sw = span_of(workspace, {need}, {1}, 1);
+            if (overlap(sw, span_of_out(p, 1, T)) || overlap(sw, span_of_state(p)) || overlaps_input(p, 1, T, sw))
+                return SCONV_ERR_ALIAS;
+            return launch_status(launch_gdr_chunk(p, vec8, svec, workspace, stream));
+        }
+        if (vec8) return launch_status(launch_gdr_chunk(p, vec8, svec, nullptr, stream));
     }
     return launch_status(launch_gdr_recurrent(p, vec, stream));
+}
+
+int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num_k_heads, int32_t num_v_heads,
+                                int32_t head_dim_k, int32_t head_dim_v, int32_t vector_layout) {
+    if (batch < 1 || total_tokens < 1 || num_k_heads < 1 || num_v_heads < 1 || head_dim_k < 1 || head_dim_v < 1 ||
+        head_dim_k > kGdrMaxChunkK)
+        return 0;
+    if (vector_layout && !gdr_few_heads(batch, num_v_heads, head_dim_v)) return 0;
+    const int64_t slots = gdr_slots(total_tokens, batch);
+    if (slots * num_k_heads >= (int64_t(1) << 31)) return 0;
+    return gdr_workspace_bytes(total_tokens, batch, num_k_heads, num_v_heads, head_dim_k);
 }
 
 int gdr_update(const void *q, int64_t q_stride_seq, int64_t q_stride_tok, int64_t q_stride_head,

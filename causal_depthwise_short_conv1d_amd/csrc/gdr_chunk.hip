@@ -54,10 +54,13 @@ __device__ __forceinline__ constexpr int tri_tile(int mt, int tt) { return mt < 
 constexpr int kTriTiles = 6;
 
 template <int KT>
-struct alignas(16) Tiles {
+struct alignas(16) KeyTiles {          // of a chunk's keys and queries
     _Float16 k[4 * KT * kTile];        // [mt][kt] rows tokens
     _Float16 q[4 * KT * kTile];
     _Float16 kt[4 * KT * kTile];       // [2 KT channel tiles][2] rows key channels, columns tokens
+    float qf[kC];
+};
+struct alignas(16) HeadTiles {         // ... with a value head's gates
     _Float16 th[kTriTiles * kTile];    // T, high and low parts
     _Float16 tl[kTriTiles * kTile];
     _Float16 p[kTriTiles * kTile];     // e^(Gi - Gj) q16.k16
@@ -65,9 +68,10 @@ struct alignas(16) Tiles {
     float ka[kC];                      // kf beta e^G kf
     float eg[kC];                      // e^(G_last - G)
     float qe[kC];                      // qf e^G
-    float qf[kC];
     float last;                        // e^G_last
 };
+template <int KT>
+struct Tiles : KeyTiles<KT>, HeadTiles {};
 
 template <int KT>
 struct alignas(16) Shared {
@@ -282,11 +286,20 @@ struct Prepare {
     const GdrParams &p;
     Shared<KT> &sh;
     const Span64 sp;
-    const int lane0, w, h;
+    const int lane0, w;
+    int h;                             // value head
     const uint16_t *qh, *kh;
 
     // The first waves stage the keys, as many after them the queries: 4 KT threads a row, four rows a thread.
     static constexpr int kStage = KT;  // waves
+    // What lies above T's diagonal blocks in its tiles is zero and stays so.
+    __device__ __forceinline__ void clear() {
+        for (int i = 64 * w + lane0; i < kTriTiles * kTile / 2; i += 64 * kWaves) {
+            reinterpret_cast<uint32_t *>(sh.t.th)[i] = 0u;
+            reinterpret_cast<uint32_t *>(sh.t.tl)[i] = 0u;
+        }
+    }
+
     __device__ __forceinline__ int quad_of(int lane) const { return (64 * (w & (kStage - 1)) + lane) / (4 * KT); }
 
     __device__ __forceinline__ void stage(int64_t c0) {
@@ -314,16 +327,16 @@ struct Prepare {
         return word;
     }
 
-    // From the chunk's rows and its gates (in LDS) to its tiles; leaves the next chunk's gates there.
-    __device__ __forceinline__ void chunk(int64_t c0, bool more) {
-        stage(c0);
+    // From the chunk's staged rows and its gates in LDS to its tiles.  `ahead` runs in wave 7 once the gates' place is free.
+    template <class F>
+    __device__ __forceinline__ void tiles(F ahead) {
         __syncthreads();
         if (w < 4) key_products();
         else query_products();
         if (w == 7) factors();
         __syncthreads();
         if (w == 0) invert_diagonal();
-        if (w == 7 && more) gates(c0 + kC);
+        if (w == 7) ahead();
         __syncthreads();
         if (w < 4) invert_rest();
         __syncthreads();
@@ -531,13 +544,13 @@ struct Consumer {
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d) f(d, row, 32 * (d >> 1) + 8 * g + 4 * (d & 1), c < p.Dv);
     }
-    __device__ __forceinline__ void clear() {
+    __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d) S[d] = f32x4{0, 0, 0, 0};
         un = 0;
     }
     __device__ __forceinline__ void load(float *rows, bool svec) {
-        clear();
+        zero();
         float m = 0.0f;
         rows_of(rows, [&](int d, const float *row, int k, bool ok) {
             if (svec) {
@@ -614,7 +627,10 @@ struct Consumer {
         }
     }
 
-    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b) {
+    // LEAN: few registers (the values are read inside, the products held apart); else v comes in and goes out with the
+    // next chunk's.
+    template <bool LEAN>
+    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16]) {
         const int lane = fresh(lane0), g = lane >> 4;
         // K S and Q S, the state split on the way (its largest element is below 2^15)
         f32x4 ak[4], aq[4];
@@ -637,12 +653,11 @@ struct Consumer {
                 ak[mt] = mfma(kf, sh, ak[mt]);
                 aq[mt] = mfma(qf, sh, aq[mt]);
                 ak[mt] = mfma(kf, sl, ak[mt]);
-                if (mt == 1) __builtin_amdgcn_sched_barrier(0);
+                if (LEAN && mt == 1) __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
         }
-        uint16_t v[16];
-        fetch(t0, v);                                  // (from L2; registers are what bounds the products above)
+        if constexpr (LEAN) fetch(t0, v);              // (from L2; registers are what bounds the products above)
         // X, scaled to 2^12
         float x[16], xm = 0.0f;
         const float unit = pow2(un);
@@ -656,6 +671,7 @@ struct Consumer {
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
+        if constexpr (!LEAN) fetch(t0 + kC, v);        // (rows behind the end read as zero)
         const int ex = exp_of(max_groups(xm));
         const float xs = pow2(12 - ex);
 
@@ -676,7 +692,7 @@ struct Consumer {
                 z[mt] = mfma(h, xl, z[mt]);
                 z[mt] = mfma(l, xh, z[mt]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
         }
         // the next unit: from a bound of the next state (64 tokens, |k16| < 1.5, so it adds at most 2^7 max |z|),
         // brought below 2^15
@@ -722,7 +738,7 @@ struct Consumer {
                 S[d] = mfma(k, yh, S[d]);
                 S[d] = mfma(k, yl, S[d]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
         }
 
         // o
@@ -757,72 +773,232 @@ __device__ __forceinline__ Place place_of(const GdrParams &p, int32_t groups) {
     return pl;
 }
 
+// Sequence b's rows and line; false when nothing is to be done for it.
+__device__ __forceinline__ bool sequence(const GdrParams &p, int32_t b, Span64 &sp, int64_t &line) {
+    int64_t a = p.qsl[b], e = p.qsl[b + 1];
+    a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
+    e = e < a ? a : (e > p.total_T ? p.total_T : e);
+    sp.t0 = a;
+    sp.n = e - a;
+    if (sp.n == 0) return false;
+    line = b;
+    if (p.ci) {
+        line = p.ci[b];
+        if (line == p.pad_slot_id) return false;
+    }
+    return !(p.state && (line < 0 || line >= p.num_lines));
+}
+
+template <int KT, bool VEC>
+__device__ __forceinline__ Consumer<KT, VEC> consumer(const GdrParams &p, const Span64 &sp, int lane, int32_t h, int32_t tile) {
+    Consumer<KT, VEC> st{p, sp, lane};
+    st.col = tile * 16 + (lane & 15);
+    st.vh = p.v + sp.t0 * p.vs.st + h * p.vs.sh;
+    st.oh = p.out + sp.t0 * p.os.st + h * p.os.sh;
+    return st;
+}
+
 template <int KT, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, int32_t groups, bool svec) {
     __shared__ Shared<KT> sh;
     const Place pl = place_of(p, groups);
     if (!pl.ok) return;
     Span64 sp;
-    {
-        int64_t a = p.qsl[pl.b], e = p.qsl[pl.b + 1];
-        a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
-        e = e < a ? a : (e > p.total_T ? p.total_T : e);
-        sp.t0 = a;
-        sp.n = e - a;
-    }
-    if (sp.n == 0) return;
-    int64_t line = pl.b;
-    if (p.ci) {
-        line = p.ci[pl.b];
-        if (line == p.pad_slot_id) return;
-    }
-    if (p.state && (line < 0 || line >= p.num_lines)) return;
+    int64_t line;
+    if (!sequence(p, pl.b, sp, line)) return;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t nc = (sp.n + kC - 1) / kC;
-    // what lies above T's diagonal blocks in its tiles is zero and stays so
-    for (int i = threadIdx.x; i < kTriTiles * kTile / 2; i += 64 * kWaves) {
-        reinterpret_cast<uint32_t *>(sh.t.th)[i] = 0u;
-        reinterpret_cast<uint32_t *>(sh.t.tl)[i] = 0u;
-    }
     const int hk = pl.h / p.group;
     Prepare<KT, VEC> pr{p, sh, sp, lane, wave, pl.h, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
+    pr.clear();
     if (wave == 7) pr.gates(0);
 
-    Consumer<KT, VEC> st{p, sp, lane};
-    st.col = (pl.cg * kWaves + wave) * 16 + (lane & 15);
-    st.vh = p.v + sp.t0 * p.vs.st + pl.h * p.vs.sh;
-    st.oh = p.out + sp.t0 * p.os.st + pl.h * p.os.sh;
-    const bool work = (pl.cg * kWaves + wave) * 16 < p.Dv;         // this wave has channels
+    const int32_t tile = pl.cg * kWaves + wave;
+    auto st = consumer<KT, VEC>(p, sp, lane, pl.h, tile);
+    const bool work = tile * 16 < p.Dv;                            // this wave has channels
     float *rows = p.state ? p.state + line * p.s_sl + pl.h * p.s_sh : nullptr;
     if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
-    else st.clear();
+    else st.zero();
 
     for (int64_t c = 0; c < nc; ++c) {
-        pr.chunk(c * kC, c + 1 < nc);
+        const bool more = c + 1 < nc;
+        pr.stage(c * kC);
+        pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
         uint32_t word = 0;
-        if (c + 1 < nc) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
-        if (work) st.chunk(c * kC, sh.t);
+        if (more) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
+        if (work) {
+            uint16_t v[16];
+            st.template chunk<true>(c * kC, sh.t, v);
+        }
         asm volatile("" : : "v"(word));
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
 }
 
+// ------------------------------------------------------------ two kernels --
+//
+// Where a call has few heads to walk, the walk's length is what counts, and the tiles of all chunks are prepared
+// beforehand by every CU into a workspace: [slots][Hk] KeyTiles, then [slots][Hv] HeadTiles.  Chunk j of sequence i has
+// slot floor(start_i / 64) + i + j: no two chunks share one, and floor(T / 64) + batch + 2 of them are enough for any
+// offsets, so no kernel has to count chunks.
+
+__device__ __forceinline__ int64_t first_slot(const GdrParams &p, int32_t b) {
+    int64_t a = p.qsl[b];
+    a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
+    return (a >> 6) + b;
+}
+
+template <class D, class S>
+__device__ __forceinline__ void copy_out(D *dst, const S *src, int thread) {
+    u32x4 *d = reinterpret_cast<u32x4 *>(dst);
+    const u32x4 *f = reinterpret_cast<const u32x4 *>(src);
+    for (int i = thread; i < int(sizeof(D) / 16); i += 64 * kWaves) d[i] = f[i];
+}
+
+// A workgroup prepares one chunk of one key head, for all the value heads that share it.
 template <int KT, bool VEC>
-hipError_t launch_kt(const GdrParams &p, bool svec, hipStream_t s) {
+__global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, KeyTiles<KT> *keys, HeadTiles *heads) {
+    __shared__ Shared<KT> sh;
+    const int64_t slot = blockIdx.x / uint32_t(p.Hk);
+    const int32_t hk = int32_t(blockIdx.x - uint32_t(slot) * uint32_t(p.Hk));
+    int32_t lo = 0, hi = p.batch - 1;                              // the last sequence whose slots start at or before
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (first_slot(p, mid) <= slot) lo = mid; else hi = mid - 1;
+    }
+    Span64 sp;
+    int64_t line;
+    if (!sequence(p, lo, sp, line)) return;
+    const int64_t c = slot - first_slot(p, lo);
+    if (c < 0 || c * kC >= sp.n) return;
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    Prepare<KT, VEC> pr{p, sh, sp, lane, wave, hk * p.group, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
+    pr.clear();
+    if (wave == 7) pr.gates(c * kC);
+    pr.stage(c * kC);
+    for (int32_t x = 0; x < p.group; ++x) {
+        pr.tiles([&]() {
+            if (x + 1 < p.group) {
+                ++pr.h;
+                pr.gates(c * kC);
+            }
+        });
+        if (x == 0) copy_out(keys + slot * p.Hk + hk, static_cast<const KeyTiles<KT> *>(&sh.t), threadIdx.x);
+        copy_out(heads + slot * p.Hv + hk * p.group + x, static_cast<const HeadTiles *>(&sh.t), threadIdx.x);
+        __syncthreads();
+    }
+}
+
+constexpr int kWalkers = 4;            // state waves of a walking workgroup
+constexpr int kLoaders = 4;
+
+// Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers,
+// four take their 16 channels through the present one.
+template <int KT, bool VEC>
+__global__ __launch_bounds__(64 * (kWalkers + kLoaders), 2) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
+                                                                                 const HeadTiles *heads, int32_t groups,
+                                                                                 bool svec) {
+    __shared__ Tiles<KT> buf[2];
+    const Place pl = place_of(p, groups);
+    if (!pl.ok) return;
+    Span64 sp;
+    int64_t line;
+    if (!sequence(p, pl.b, sp, line)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t nc = (sp.n + kC - 1) / kC, slot = first_slot(p, pl.b);
+
+    if (wave >= kWalkers) {
+        constexpr int kN = 64 * kLoaders;
+        constexpr int kKey = sizeof(KeyTiles<KT>) / 16, kHead = sizeof(HeadTiles) / 16;
+        constexpr int kKeyPer = (kKey + kN - 1) / kN, kHeadPer = (kHead + kN - 1) / kN;
+        const int t = (wave - kWalkers) * 64 + lane;
+        u32x4 rk[kKeyPer], rh[kHeadPer];
+        const auto load = [&](int64_t c) {
+            const u32x4 *k = reinterpret_cast<const u32x4 *>(keys + (slot + c) * p.Hk + pl.h / p.group);
+            const u32x4 *h = reinterpret_cast<const u32x4 *>(heads + (slot + c) * p.Hv + pl.h);
+#pragma unroll
+            for (int i = 0; i < kKeyPer; ++i) rk[i] = k[t + i * kN < kKey ? t + i * kN : 0];
+#pragma unroll
+            for (int i = 0; i < kHeadPer; ++i) rh[i] = h[t + i * kN < kHead ? t + i * kN : 0];
+        };
+        const auto put = [&](Tiles<KT> &b) {
+            u32x4 *k = reinterpret_cast<u32x4 *>(static_cast<KeyTiles<KT> *>(&b));
+            u32x4 *h = reinterpret_cast<u32x4 *>(static_cast<HeadTiles *>(&b));
+#pragma unroll
+            for (int i = 0; i < kKeyPer; ++i)
+                if (t + i * kN < kKey) k[t + i * kN] = rk[i];
+#pragma unroll
+            for (int i = 0; i < kHeadPer; ++i)
+                if (t + i * kN < kHead) h[t + i * kN] = rh[i];
+        };
+        load(0);
+        put(buf[0]);
+        load(nc > 1 ? 1 : 0);
+        __syncthreads();
+        for (int64_t c = 0; c < nc; ++c) {
+            put(buf[(c + 1) & 1]);
+            load(c + 2 < nc ? c + 2 : nc - 1);
+            __syncthreads();
+        }
+        return;
+    }
+
+    const int32_t tile = pl.cg * kWalkers + wave;
+    auto st = consumer<KT, VEC>(p, sp, lane, pl.h, tile);
+    const bool work = tile * 16 < p.Dv;
+    float *rows = p.state ? p.state + line * p.s_sl + pl.h * p.s_sh : nullptr;
+    if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
+    else st.zero();
+    uint16_t v[16];
+    st.fetch(0, v);
+    __syncthreads();
+    for (int64_t c = 0; c < nc; ++c) {
+        if (work) st.template chunk<false>(c * kC, buf[c & 1], v);
+        __syncthreads();
+    }
+    if (p.state) st.save(rows, svec);
+}
+
+// Workgroups of a kernel that walks sequences, `groups` a head (see place_of).
+int64_t walk_grid(const GdrParams &p, int32_t groups) {
+    return (int64_t(p.batch) * p.Hk + 7) / 8 * 8 * p.group * groups;
+}
+
+template <int KT>
+hipError_t launch_one(const GdrParams &p, bool svec, hipStream_t s) {
     const int32_t groups = (p.Dv + 16 * kWaves - 1) / (16 * kWaves);
-    const int64_t units = (int64_t(p.batch) * p.Hk + 7) / 8 * 8;
-    const dim3 grid(uint32_t(units * p.group * groups)), block(64 * kWaves);
-    gdr_chunk_kernel<KT, VEC><<<grid, block, 0, s>>>(p, groups, svec);
+    gdr_chunk_kernel<KT, true><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * kWaves), 0, s>>>(p, groups, svec);
+    return hipGetLastError();
+}
+
+template <int KT, bool VEC>
+hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream_t s) {
+    const int64_t slots = gdr_slots(p.total_T, p.batch);
+    KeyTiles<KT> *keys = static_cast<KeyTiles<KT> *>(workspace);
+    HeadTiles *heads = reinterpret_cast<HeadTiles *>(keys + slots * p.Hk);
+    gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, keys, heads);
+    const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
+    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * (kWalkers + kLoaders)), 0, s>>>(
+        p, keys, heads, groups, svec);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, hipStream_t s) {
-    if (p.Dk <= 64) return vec ? launch_kt<2, true>(p, svec, s) : launch_kt<2, false>(p, svec, s);
-    return vec ? launch_kt<4, true>(p, svec, s) : launch_kt<4, false>(p, svec, s);
+int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hk, int32_t Hv, int32_t Dk) {
+    const int64_t key = Dk <= 64 ? sizeof(KeyTiles<2>) : sizeof(KeyTiles<4>);
+    return gdr_slots(T, batch) * (Hk * key + Hv * int64_t(sizeof(HeadTiles)));
+}
+
+hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, void *workspace, hipStream_t s) {
+    if (workspace) {
+        if (p.Dk <= 64) return vec ? launch_walk<2, true>(p, svec, workspace, s) : launch_walk<2, false>(p, svec, workspace, s);
+        return vec ? launch_walk<4, true>(p, svec, workspace, s) : launch_walk<4, false>(p, svec, workspace, s);
+    }
+    return p.Dk <= 64 ? launch_one<2>(p, svec, s) : launch_one<4>(p, svec, s);
 }
 
 }  // namespace sconv

@@ -65,8 +65,17 @@ struct VerifyParams {
 hipError_t launch_gdr_recurrent(const GdrParams &p, bool vec, hipStream_t s);
 // `vec`: unit channel strides of q and k, every base and stride a multiple of 8
 // elements; `svec`: the state's rows in 16-byte pieces.  Dk at most kGdrMaxChunkK.
-hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, hipStream_t s);
+// With a workspace of gdr_workspace_bytes(), 16-byte aligned: two kernels, the
+// tiles of all chunks first; without (vec only): one kernel.
+int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hk, int32_t Hv, int32_t Dk);
+hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, void *workspace, hipStream_t s);
 hipError_t launch_verify_drafts(const VerifyParams &p, hipStream_t s);
+
+// Slots for the 64-token chunks of any packing of T tokens into `batch` sequences.
+inline int64_t gdr_slots(int64_t T, int64_t batch) { return T / 64 + batch + 2; }
+
+// Whether a call's heads are so few that walking prepared chunks in two kernels is faster than one kernel.
+inline bool gdr_few_heads(int64_t batch, int64_t Hv, int64_t Dv) { return batch * Hv * ((Dv + 63) / 64) <= 256; }
 
 constexpr int kGdrMaxHeadK = 256;      // key channels a head of the recurrent kernel
 constexpr int kGdrMaxChunkK = 128;     // ... of the chunked kernel

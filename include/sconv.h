@@ -443,6 +443,20 @@ int sconv_paged_fused_multi(int32_t num_streams,
  * to its line (a sequence of no tokens writes nothing).  state may be NULL:
  * zero states, none written.  Rows of skipped sequences and rows behind the
  * last sequence are left untouched.
+ * Heads of up to 128 key channels are processed in chunks of 64 tokens on the
+ * matrix cores, longer ones a token at a time.  In a chunk
+ *   - beta |k|^2 must stay at or below 2 (k after its norm), as it must for the
+ *     rule to be stable at all; the inverse below it leaves fp16 far above;
+ *   - an infinity or NaN in a token may reach the other tokens of its chunk,
+ *     sequence and head, earlier ones too;
+ *   - a value channel is held to about 2^-26 of its largest value in the chunk.
+ * workspace    device memory, 16-byte aligned, in use until the call's work is
+ *              done, or NULL.  With gdr_fwd_workspace_bytes() bytes of it, calls
+ *              of few heads take two kernels (all chunks are prepared at once,
+ *              then walked), which is up to three times as fast for them, and
+ *              layouts without vector loads can be processed in chunks; without
+ *              it these go a token at a time.  Smaller than asked for ->
+ *              SCONV_ERR_SHAPE.
  */
 int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, int64_t q_stride_dim,
                    const void *k, int64_t k_stride_tok, int64_t k_stride_head, int64_t k_stride_dim,
@@ -457,7 +471,13 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
                    int32_t num_k_heads, int32_t num_v_heads, int32_t head_dim_k,
                    int32_t head_dim_v, float scale, int32_t qk_l2norm, int32_t pad_slot_id,
                    void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
-                   hipStream_t stream);
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that gdr_fwd_varlen makes use of (0: none).  vector_layout:
+ * q, k, v and out are in the layout of the vector loads (above). */
+int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num_k_heads,
+                                int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                int32_t vector_layout);
 
 /*
  * gdr_update -- decode: each of `batch` entries feeds `seqlen` tokens, from the

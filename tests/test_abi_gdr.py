@@ -20,12 +20,27 @@ def fwd(lib, **kw):
     a = dict(q=addr(1), qs=(256, 64, 1), k=addr(2), ks=(256, 64, 1), v=addr(3), vs=(512, 64, 1),
              g=addr(4), gs=(8, 1), b=addr(5), bs=(8, 1), al=None, dt=None, st=addr(6),
              ss=(8 * 64 * 64, 64 * 64, 64, 1), lines=4, ci=addr(7), hi=addr(8), qsl=addr(9), batch=2, T=10, hk=4,
-             hv=8, dk=64, dv=64, scale=1.0, l2=1, pad=-1, o=addr(10), os=(512, 64, 1))
+             hv=8, dk=64, dv=64, scale=1.0, l2=1, pad=-1, o=addr(10), os=(512, 64, 1), ws=None, wb=0)
     a.update(kw)
     return lib.gdr_fwd_varlen(a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["g"], *a["gs"], a["b"],
                               *a["bs"], a["al"], a["dt"], a["st"], *a["ss"], a["lines"], a["ci"], a["hi"], a["qsl"],
                               a["batch"], a["T"], a["hk"], a["hv"], a["dk"], a["dv"], a["scale"], a["l2"], a["pad"],
-                              a["o"], *a["os"], None)
+                              a["o"], *a["os"], a["ws"], a["wb"], None)
+
+
+def test_fwd_workspace(lib):
+    need = lib.gdr_fwd_workspace_bytes(2, 10, 4, 8, 64, 64, 1)
+    assert need > 0
+    assert fwd(lib, ws=addr(11), wb=need) == ELAUNCH
+    assert fwd(lib, ws=addr(11), wb=need - 1) == ESHAPE
+    assert fwd(lib, ws=ctypes.c_void_p(BASE + 11 * GB + 8), wb=need) == EALIGN
+    for x in (1, 2, 3, 4, 5, 6, 10):
+        assert fwd(lib, ws=addr(x), wb=need) == EALIAS, x
+    assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 1) == 0          # many heads: one kernel
+    assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 0) > 0
+    for bad in ((0, 10, 4, 8, 64, 64, 1), (2, 0, 4, 8, 64, 64, 1), (2, 10, 0, 8, 64, 64, 1), (2, 10, 4, 8, 129, 64, 1),
+                (2, 10, 4, 8, 64, 0, 1)):
+        assert lib.gdr_fwd_workspace_bytes(*bad) == 0
 
 
 def test_fwd_accepted(lib):

@@ -75,6 +75,24 @@ def test_prefill_ragged_batch_with_empty_and_padded_sequences():
     prefill([0, 1, 64, 0, 3, 129, 2, 63, 65, 1, 0, 7], 2, 4, 64, 64, seed=3, pads=(2, 6), tail=9)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (96, 80), (128, 200), (8, 16), (36, 24)])
+def test_prefill_many_heads(dk, dv):
+    """Batches whose heads fill the chip by themselves: one kernel (two for 36 channels, which have no vector loads)."""
+    lens = [1 + (37 * i) % 90 for i in range(44)]
+    lens[7], lens[9], lens[30] = 0, 200, 64
+    prefill(lens, 2, 6, dk, dv, seed=dk + dv, pads=(3, 40))
+
+
+def test_prefill_without_workspace(monkeypatch):
+    """The C entry with no workspace: one kernel for layouts with vector loads, a token at a time for others."""
+    import ctypes
+    real = S._launch
+    monkeypatch.setattr(S, "_launch", lambda fn, dev, args: real(fn, dev, (*args[:-2], ctypes.c_void_p(None), 0)))
+    prefill([70, 5, 130], 2, 4, 128, 128, seed=1)
+    prefill([70, 5, 130], 2, 4, 64, 100, seed=2)
+    prefill([70, 5, 130], 2, 4, 36, 24, seed=3)
+
+
 def test_prefill_no_decay_and_full_decay():
     def edit(d):
         d["g"][:20] = 0.0                              # nothing is forgotten
