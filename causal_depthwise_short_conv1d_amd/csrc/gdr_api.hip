@@ -98,7 +98,7 @@ int check_gdr(const GdrParams &p, int64_t B, int64_t T, bool *vec) {
 int32_t verify_slice(int64_t batch, int64_t vocab) {
     int64_t s = (batch * vocab + 2047) / 2048;
     s = (s + 255) / 256 * 256;
-    return int32_t(s < 1024 ? 1024 : (s > 8192 ? 8192 : s));
+    return int32_t(s < 1024 ? 1024 : (s > kVfMaxSlice ? kVfMaxSlice : s));
 }
 
 }  // namespace

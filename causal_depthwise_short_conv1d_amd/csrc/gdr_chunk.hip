@@ -73,16 +73,14 @@ struct alignas(16) HeadTiles {         // ... with a value head's gates
 template <int KT>
 struct Tiles : KeyTiles<KT>, HeadTiles {};
 
-template <int KT>
-struct alignas(16) Shared {
-    Tiles<KT> t;
+struct alignas(16) Scratch {           // of the preparation
     _Float16 off[6 * kTile];           // A's blocks below the diagonal: [4 rows / 4][column]: 4 high, 4 low parts
     float diag[4 * 256];               // A's diagonal blocks by columns, then T's
     float dump[4];                     // for what lies in neither
     float Gh[kC], Gl[kC];              // running log decay, in powers of 2: high and low parts
-    float beta[kC], eG[kC], eg[kC], kf[kC];
+    float beta[kC], eG[kC], eg[kC], kf[kC], qf[kC];
 };
-static_assert(sizeof(Shared<4>) <= 80 * 1024, "two workgroups per CU");
+static_assert(sizeof(Tiles<4>) + sizeof(Scratch) <= 80 * 1024, "two workgroups of the one-kernel form per CU");
 
 // Token t of a chunk as a row: tile 2 (t / 32) + (t / 4) % 2, row 4 ((t % 32) / 8) + t % 4.
 __device__ __forceinline__ int row_tile(int t) { return 2 * (t >> 5) + ((t >> 2) & 1); }
@@ -208,9 +206,10 @@ __device__ __forceinline__ Quad load_quad(const uint16_t *head, const GdrTensor 
 
 // Scales a row by a power of two (to a norm of 2^-0.5 .. 2^0.5), writes it as a row of the operand tiles (and, for
 // keys, transposed), and its factor: the power, times the norm's inverse and `scale`.
+// `copy`: the same rows again (in memory), or null.
 template <int KT, bool KEYS>
-__device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Float16 *cols, float *factor, int quad,
-                                           int kc, float scale, bool l2norm) {
+__device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Float16 *copy, _Float16 *cols, float *factor,
+                                           int quad, int kc, float scale, bool l2norm) {
     f16x8 h[4];
     const int kt = kc >> 2, g = kc & 3;
 #pragma unroll
@@ -234,8 +233,9 @@ __device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Floa
         if (kc == i)
             factor[t] = scale * (l2norm ? __builtin_amdgcn_rsqf(ss + kL2Eps) : 1.0f) * __uint_as_float((64u + e) << 23);
         // (row, columns 8 kc ..) of tile (row tile, kt)
-        *reinterpret_cast<f16x8 *>(rows + (row_tile(t) * KT + kt) * kTile + (swz_rows(row_in(t), g, kt) + 16 * g) * 8) =
-            h[i];
+        const int at = (row_tile(t) * KT + kt) * kTile + (swz_rows(row_in(t), g, kt) + 16 * g) * 8;
+        *reinterpret_cast<f16x8 *>(rows + at) = h[i];
+        if (copy) *reinterpret_cast<f16x8 *>(copy + at) = h[i];
     }
     if constexpr (KEYS) {
         // channel 8 kc + j: result tile d = 2 kt + j / 4, row 4 g + j % 4; tokens 4 quad ..
@@ -284,7 +284,10 @@ __device__ __forceinline__ void split4(const f32x4 &x, f16x4 &hi, f16x4 &lo) {
 template <int KT, bool VEC>
 struct Prepare {
     const GdrParams &p;
-    Shared<KT> &sh;
+    Scratch &sh;
+    _Float16 *k, *q;                   // the chunk's rows as tiles, in LDS
+    KeyTiles<KT> *kt;                  // where the tiles go: LDS (k and q are its own) or memory
+    HeadTiles *ht;
     const Span64 sp;
     const int lane0, w;
     int h;                             // value head
@@ -292,24 +295,16 @@ struct Prepare {
 
     // The first waves stage the keys, as many after them the queries: 4 KT threads a row, four rows a thread.
     static constexpr int kStage = KT;  // waves
-    // What lies above T's diagonal blocks in its tiles is zero and stays so.
-    __device__ __forceinline__ void clear() {
-        for (int i = 64 * w + lane0; i < kTriTiles * kTile / 2; i += 64 * kWaves) {
-            reinterpret_cast<uint32_t *>(sh.t.th)[i] = 0u;
-            reinterpret_cast<uint32_t *>(sh.t.tl)[i] = 0u;
-        }
-    }
-
     __device__ __forceinline__ int quad_of(int lane) const { return (64 * (w & (kStage - 1)) + lane) / (4 * KT); }
 
     __device__ __forceinline__ void stage(int64_t c0) {
         const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
         if (w < kStage)
-            stage_quad<KT, true>(load_quad<VEC>(kh, p.ks, sp, c0, quad, kc, p.Dk), sh.t.k, sh.t.kt, sh.kf, quad, kc, 1.0f,
-                                 p.l2norm);
+            stage_quad<KT, true>(load_quad<VEC>(kh, p.ks, sp, c0, quad, kc, p.Dk), k, kt->k == k ? nullptr : kt->k, kt->kt,
+                                 sh.kf, quad, kc, 1.0f, p.l2norm);
         else if (w < 2 * kStage)
-            stage_quad<KT, false>(load_quad<VEC>(qh, p.qs, sp, c0, quad, kc, p.Dk), sh.t.q, nullptr, sh.t.qf, quad, kc,
-                                  p.scale, p.l2norm);
+            stage_quad<KT, false>(load_quad<VEC>(qh, p.qs, sp, c0, quad, kc, p.Dk), q, kt->q == q ? nullptr : kt->q, nullptr,
+                                  sh.qf, quad, kc, p.scale, p.l2norm);
     }
 
     // Reads one word of each 128-byte line that the chunk's rows will be read from: the lines wait in L2 and the
@@ -372,12 +367,13 @@ struct Prepare {
     // The row factors of the chunk.
     __device__ __forceinline__ void factors() {
         const int lane = fresh(lane0);
-        const float kf = sh.kf[lane], eG = sh.eG[lane], kb = kf * sh.beta[lane];
-        sh.t.kb[lane] = kb;
-        sh.t.ka[lane] = kb * eG * kf;
-        sh.t.eg[lane] = sh.eg[lane];
-        sh.t.qe[lane] = sh.t.qf[lane] * eG;
-        if (lane == 63) sh.t.last = eG;
+        const float kf = sh.kf[lane], qf = sh.qf[lane], eG = sh.eG[lane], kb = kf * sh.beta[lane];
+        kt->qf[lane] = qf;
+        ht->kb[lane] = kb;
+        ht->ka[lane] = kb * eG * kf;
+        ht->eg[lane] = sh.eg[lane];
+        ht->qe[lane] = qf * eG;
+        if (lane == 63) ht->last = eG;
     }
 
     // 2^(running decays of four tokens less that of one, or the reverse).
@@ -407,8 +403,8 @@ struct Prepare {
             pair(3 * w + x, mt, nt);
             kk[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                kk[x] = mfma(row_tile_of(sh.t.k, mt * KT + kt, kt, lane), row_tile_of(sh.t.k, nt * KT + kt, kt, lane), kk[x]);
+            for (int i = 0; i < KT; ++i)
+                kk[x] = mfma(row_tile_of(k, mt * KT + i, i, lane), row_tile_of(k, nt * KT + i, i, lane), kk[x]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -437,8 +433,8 @@ struct Prepare {
             pair(3 * (w - 4) + x, mt, nt);
             qk[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                qk[x] = mfma(row_tile_of(sh.t.k, nt * KT + kt, kt, lane), row_tile_of(sh.t.q, mt * KT + kt, kt, lane), qk[x]);
+            for (int i = 0; i < KT; ++i)
+                qk[x] = mfma(row_tile_of(k, nt * KT + i, i, lane), row_tile_of(q, mt * KT + i, i, lane), qk[x]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -451,7 +447,7 @@ struct Prepare {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = tj + i <= ti ? d[i] * qk[x][i] : 0.0f;
             const f16x2 lo = cvt2(v[0], v[1]), hi = cvt2(v[2], v[3]);
-            *reinterpret_cast<f16x4 *>(sh.t.p + tri_tile(mt, nt >> 1) * kTile + in_tile(n, tj & 31)) =
+            *reinterpret_cast<f16x4 *>(ht->p + tri_tile(mt, nt >> 1) * kTile + in_tile(n, tj & 31)) =
                 f16x4{lo.x, lo.y, hi.x, hi.y};
         }
     }
@@ -516,13 +512,37 @@ struct Prepare {
             split4(t, hi[j], lo[j]);
             const int tj = 16 * j + 4 * g;
             const int o = tri_tile(row_tile(ti), tj >> 5) * kTile + in_tile(row_in(ti), tj & 31);
-            *reinterpret_cast<f16x4 *>(sh.t.th + o) = hi[j];
-            *reinterpret_cast<f16x4 *>(sh.t.tl + o) = lo[j];
+            *reinterpret_cast<f16x4 *>(ht->th + o) = hi[j];
+            *reinterpret_cast<f16x4 *>(ht->tl + o) = lo[j];
+        }
+        if (!(w & 1)) {                                // the block to the right shares the tile: zero
+            const int o = tri_tile(row_tile(ti), ti >> 5) * kTile + in_tile(row_in(ti), (16 * (w + 1) + 4 * g) & 31);
+            *reinterpret_cast<f16x4 *>(ht->th + o) = f16x4{0, 0, 0, 0};
+            *reinterpret_cast<f16x4 *>(ht->tl + o) = f16x4{0, 0, 0, 0};
         }
     }
 };
 
 // ---------------------------------------------------- the state's passage --
+
+// What a state wave hands to the wave that computes its channels' output: the state before the chunk and z as fp16
+// operands, and 2^-unit of both.  `ready` counts the halves handed over, two a chunk.
+template <int KT>
+struct alignas(16) Exchange {
+    f16x8 s[KT * 64];
+    f16x8 z[2 * 64];
+    float oinv[16], ninv[16];
+};
+
+__device__ __forceinline__ void hand_over(int *ready) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    if ((threadIdx.x & 63) == 0) __hip_atomic_fetch_add(ready, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+// Both waves are of one workgroup, so both are resident, and the state wave waits for no one between two barriers.
+__device__ __forceinline__ void await(int *ready, int count) {
+    while (__hip_atomic_load(ready, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) < count) __builtin_amdgcn_s_sleep(1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
 
 template <int KT, bool VEC>
 struct Consumer {
@@ -627,37 +647,59 @@ struct Consumer {
         }
     }
 
-    // LEAN: few registers (the values are read inside, the products held apart); else v comes in and goes out with the
-    // next chunk's.
-    template <bool LEAN>
-    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16]) {
+    // The state through one chunk.  WHOLE: the output too, with few registers (the values are read inside, the products
+    // held apart); else v comes in and goes out with the next chunk's, and the output is another wave's.
+    template <bool WHOLE>
+    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16], Exchange<KT> *ex, int *ready) {
         const int lane = fresh(lane0), g = lane >> 4;
-        // K S and Q S, the state split on the way (its largest element is below 2^15)
         f32x4 ak[4], aq[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) { ak[mt] = f32x4{0, 0, 0, 0}; aq[mt] = f32x4{0, 0, 0, 0}; }
         float ms = 0.0f;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
+        const float oinv = pow2(-un);
+        // the state in high and low parts (its largest element is below 2^15)
+        f16x8 sh[WHOLE ? 1 : KT], sl[WHOLE ? 1 : KT];
+        const auto part = [&](int kt, f16x8 &hi, f16x8 &lo) {
             float f[8];
-            f16x8 sh, sl;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 f[j] = S[2 * kt + (j >> 2)][j & 3];
                 ms = fmaxf(ms, fabsf(f[j]));
             }
-            split8(f, sh, sl);
+            split8(f, hi, lo);
+        };
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                part(kt, sh[kt], sl[kt]);
+                ex->s[kt * 64 + lane] = sh[kt];
+            }
+            if (lane < 16) ex->oinv[lane] = oinv;
+            hand_over(ready);
+        }
+        // K S and Q S
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            if constexpr (WHOLE) part(kt, sh[0], sl[0]);
+            const f16x8 &hi = sh[WHOLE ? 0 : kt], &lo = sl[WHOLE ? 0 : kt];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const f16x8 kf = row_tile_of(b.k, mt * KT + kt, kt, lane), qf = row_tile_of(b.q, mt * KT + kt, kt, lane);
-                ak[mt] = mfma(kf, sh, ak[mt]);
-                aq[mt] = mfma(qf, sh, aq[mt]);
-                ak[mt] = mfma(kf, sl, ak[mt]);
-                if (LEAN && mt == 1) __builtin_amdgcn_sched_barrier(0);
+                const f16x8 kf = row_tile_of(b.k, mt * KT + kt, kt, lane);
+                ak[mt] = mfma(kf, hi, ak[mt]);
+                if constexpr (WHOLE) {
+                    aq[mt] = mfma(row_tile_of(b.q, mt * KT + kt, kt, lane), hi, aq[mt]);
+                    ak[mt] = mfma(kf, lo, ak[mt]);
+                    if (mt == 1) __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (WHOLE) {
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(row_tile_of(b.k, mt * KT + kt, kt, lane), lo, ak[mt]);
+            }
         }
-        if constexpr (LEAN) fetch(t0, v);              // (from L2; registers are what bounds the products above)
+        if constexpr (WHOLE) fetch(t0, v);             // (from L2; registers are what bounds the products above)
         // X, scaled to 2^12
         float x[16], xm = 0.0f;
         const float unit = pow2(un);
@@ -671,9 +713,9 @@ struct Consumer {
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
-        if constexpr (!LEAN) fetch(t0 + kC, v);        // (rows behind the end read as zero)
-        const int ex = exp_of(max_groups(xm));
-        const float xs = pow2(12 - ex);
+        if constexpr (!WHOLE) fetch(t0 + kC, v);       // (rows behind the end read as zero)
+        const int xe = exp_of(max_groups(xm));
+        const float xs = pow2(12 - xe);
 
         // z = T X
         f32x4 z[4];
@@ -692,7 +734,7 @@ struct Consumer {
                 z[mt] = mfma(h, xl, z[mt]);
                 z[mt] = mfma(l, xh, z[mt]);
             }
-            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (WHOLE) __builtin_amdgcn_sched_barrier(0);
         }
         // the next unit: from a bound of the next state (64 tokens, |k16| < 1.5, so it adds at most 2^7 max |z|),
         // brought below 2^15
@@ -702,46 +744,64 @@ struct Consumer {
 #pragma unroll
             for (int i = 0; i < 4; ++i) zm = fmaxf(zm, fabsf(z[mt][i]));
         const float last = b.last;
-        // in the present unit z is z * 2^(ex - 12)
-        const float bound = max_groups(fmaf(zm * pow2(ex - 12), 128.0f, ms * last));
+        // in the present unit z is z * 2^(xe - 12)
+        const float bound = max_groups(fmaf(zm * pow2(xe - 12), 128.0f, ms * last));
         int up = 14 - exp_of(bound);
         up = up < -126 - un ? -126 - un : (up > 126 - un ? 126 - un : up);
         up = up < -114 ? -114 : up;
-        int zu = ex - 12 + up;
+        int zu = xe - 12 + up;
         zu = zu < -126 ? -126 : (zu > 126 ? 126 : zu);
-        const float zs = pow2(zu), sc = last * pow2(up), oinv = pow2(-un);
+        const float zs = pow2(zu), sc = last * pow2(up);
         un += up;
         const float ninv = pow2(-un);
-#pragma unroll
-        for (int d = 0; d < 2 * KT; ++d) S[d] *= sc;
 
-        // S += K^T y
         f16x8 zh[2];
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            float f[8], y[8];
-            f16x8 yh, yl;
+        float y[WHOLE ? 1 : 2][8];
+        const auto scaled = [&](int tt, float (&to)[8]) {
+            float f[8];
 #pragma unroll
             for (int t2 = 0; t2 < 2; ++t2) {
                 const f32x4 eg = *reinterpret_cast<const f32x4 *>(b.eg + tok_of(2 * tt + t2, 4 * g));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     f[4 * t2 + i] = z[2 * tt + t2][i] * zs;
-                    y[4 * t2 + i] = f[4 * t2 + i] * eg[i];
+                    to[4 * t2 + i] = f[4 * t2 + i] * eg[i];
                 }
             }
             zh[tt] = half8(f);
-            split8(y, yh, yl);
+        };
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                scaled(tt, y[tt]);
+                ex->z[tt * 64 + lane] = zh[tt];
+            }
+            if (lane < 16) ex->ninv[lane] = ninv;
+            hand_over(ready);
+        }
+        // S += K^T y
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d) S[d] *= sc;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            f16x8 yh, yl;
+            if constexpr (WHOLE) scaled(tt, y[0]);
+            split8(y[WHOLE ? 0 : tt], yh, yl);
 #pragma unroll
             for (int d = 0; d < 2 * KT; ++d) {
                 const f16x8 k = col_tile_of(b.kt, d, tt, lane);
                 S[d] = mfma(k, yh, S[d]);
                 S[d] = mfma(k, yl, S[d]);
             }
-            if constexpr (LEAN) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (WHOLE) __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (WHOLE) output(t0, b, lane, aq, zh, oinv, ninv);
+    }
 
-        // o
+    // o from Q S and z.
+    __device__ __forceinline__ void output(int64_t t0, const Tiles<KT> &b, int lane, const f32x4 (&aq)[4], const f16x8 (&zh)[2],
+                                           float oinv, float ninv) {
+        const int g = lane >> 4;
         float o[16];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
@@ -754,6 +814,24 @@ struct Consumer {
             for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[i] * ninv, pz[i], qe[i] * oinv * aq[mt][i]);
         }
         store(t0, o);
+    }
+
+    // The output of one chunk from what the state wave hands over; `done` halves came before.
+    __device__ __forceinline__ void emit(int64_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
+        const int lane = fresh(lane0), n = lane & 15;
+        f32x4 aq[4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) aq[mt] = f32x4{0, 0, 0, 0};
+        await(ready, done + 1);
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            const f16x8 s = ex->s[kt * 64 + lane];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) aq[mt] = mfma(row_tile_of(b.q, mt * KT + kt, kt, lane), s, aq[mt]);
+        }
+        await(ready, done + 2);
+        const f16x8 zh[2] = {ex->z[lane], ex->z[64 + lane]};
+        output(t0, b, lane, aq, zh, ex->oinv[n], ex->ninv[n]);
     }
 };
 
@@ -800,7 +878,8 @@ __device__ __forceinline__ Consumer<KT, VEC> consumer(const GdrParams &p, const 
 
 template <int KT, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, int32_t groups, bool svec) {
-    __shared__ Shared<KT> sh;
+    __shared__ Tiles<KT> tiles;
+    __shared__ Scratch sh;
     const Place pl = place_of(p, groups);
     if (!pl.ok) return;
     Span64 sp;
@@ -810,8 +889,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t nc = (sp.n + kC - 1) / kC;
     const int hk = pl.h / p.group;
-    Prepare<KT, VEC> pr{p, sh, sp, lane, wave, pl.h, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
-    pr.clear();
+    Prepare<KT, VEC> pr{p, sh, tiles.k, tiles.q, &tiles, &tiles, sp, lane, wave, pl.h, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
     if (wave == 7) pr.gates(0);
 
     const int32_t tile = pl.cg * kWaves + wave;
@@ -829,7 +907,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
         if (more) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
         if (work) {
             uint16_t v[16];
-            st.template chunk<true>(c * kC, sh.t, v);
+            st.template chunk<true>(c * kC, tiles, v, nullptr, nullptr);
         }
         asm volatile("" : : "v"(word));
         __syncthreads();
@@ -850,17 +928,11 @@ __device__ __forceinline__ int64_t first_slot(const GdrParams &p, int32_t b) {
     return (a >> 6) + b;
 }
 
-template <class D, class S>
-__device__ __forceinline__ void copy_out(D *dst, const S *src, int thread) {
-    u32x4 *d = reinterpret_cast<u32x4 *>(dst);
-    const u32x4 *f = reinterpret_cast<const u32x4 *>(src);
-    for (int i = thread; i < int(sizeof(D) / 16); i += 64 * kWaves) d[i] = f[i];
-}
-
 // A workgroup prepares one chunk of one key head, for all the value heads that share it.
 template <int KT, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, KeyTiles<KT> *keys, HeadTiles *heads) {
-    __shared__ Shared<KT> sh;
+    __shared__ _Float16 k[4 * KT * kTile], q[4 * KT * kTile];
+    __shared__ Scratch sh;
     const int64_t slot = blockIdx.x / uint32_t(p.Hk);
     const int32_t hk = int32_t(blockIdx.x - uint32_t(slot) * uint32_t(p.Hk));
     int32_t lo = 0, hi = p.batch - 1;                              // the last sequence whose slots start at or before
@@ -875,8 +947,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
     if (c < 0 || c * kC >= sp.n) return;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    Prepare<KT, VEC> pr{p, sh, sp, lane, wave, hk * p.group, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
-    pr.clear();
+    HeadTiles *ht = heads + slot * p.Hv + hk * p.group;
+    Prepare<KT, VEC> pr{p, sh, k, q, keys + slot * p.Hk + hk, ht, sp, lane, wave, hk * p.group, p.q + hk * p.qs.sh,
+                        p.k + hk * p.ks.sh};
     if (wave == 7) pr.gates(c * kC);
     pr.stage(c * kC);
     for (int32_t x = 0; x < p.group; ++x) {
@@ -886,9 +959,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
                 pr.gates(c * kC);
             }
         });
-        if (x == 0) copy_out(keys + slot * p.Hk + hk, static_cast<const KeyTiles<KT> *>(&sh.t), threadIdx.x);
-        copy_out(heads + slot * p.Hv + hk * p.group + x, static_cast<const HeadTiles *>(&sh.t), threadIdx.x);
-        __syncthreads();
+        pr.h = hk * p.group + x + 1;
+        ++pr.ht;
     }
 }
 
@@ -896,12 +968,14 @@ constexpr int kWalkers = 4;            // state waves of a walking workgroup
 constexpr int kLoaders = 4;
 
 // Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers,
-// four take their 16 channels through the present one.
+// four take the state of 16 channels each through the present one, four compute those channels' output beside them.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * (kWalkers + kLoaders), 2) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
+__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
                                                                                  const HeadTiles *heads, int32_t groups,
                                                                                  bool svec) {
     __shared__ Tiles<KT> buf[2];
+    __shared__ Exchange<KT> exchange[kWalkers];
+    __shared__ int ready[kWalkers];
     const Place pl = place_of(p, groups);
     if (!pl.ok) return;
     Span64 sp;
@@ -909,12 +983,13 @@ __global__ __launch_bounds__(64 * (kWalkers + kLoaders), 2) void gdr_walk_kernel
     if (!sequence(p, pl.b, sp, line)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t nc = (sp.n + kC - 1) / kC, slot = first_slot(p, pl.b);
+    if (threadIdx.x < kWalkers) ready[threadIdx.x] = 0;
 
-    if (wave >= kWalkers) {
+    if (wave >= 2 * kWalkers) {
         constexpr int kN = 64 * kLoaders;
         constexpr int kKey = sizeof(KeyTiles<KT>) / 16, kHead = sizeof(HeadTiles) / 16;
         constexpr int kKeyPer = (kKey + kN - 1) / kN, kHeadPer = (kHead + kN - 1) / kN;
-        const int t = (wave - kWalkers) * 64 + lane;
+        const int t = (wave - 2 * kWalkers) * 64 + lane;
         u32x4 rk[kKeyPer], rh[kHeadPer];
         const auto load = [&](int64_t c) {
             const u32x4 *k = reinterpret_cast<const u32x4 *>(keys + (slot + c) * p.Hk + pl.h / p.group);
@@ -946,9 +1021,18 @@ __global__ __launch_bounds__(64 * (kWalkers + kLoaders), 2) void gdr_walk_kernel
         return;
     }
 
-    const int32_t tile = pl.cg * kWalkers + wave;
+    const int unit = wave & (kWalkers - 1);
+    const int32_t tile = pl.cg * kWalkers + unit;
     auto st = consumer<KT, VEC>(p, sp, lane, pl.h, tile);
     const bool work = tile * 16 < p.Dv;
+    if (wave >= kWalkers) {
+        __syncthreads();
+        for (int64_t c = 0; c < nc; ++c) {
+            if (work) st.emit(c * kC, buf[c & 1], &exchange[unit], &ready[unit], int(2 * c));
+            __syncthreads();
+        }
+        return;
+    }
     float *rows = p.state ? p.state + line * p.s_sl + pl.h * p.s_sh : nullptr;
     if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
     else st.zero();
@@ -956,7 +1040,7 @@ __global__ __launch_bounds__(64 * (kWalkers + kLoaders), 2) void gdr_walk_kernel
     st.fetch(0, v);
     __syncthreads();
     for (int64_t c = 0; c < nc; ++c) {
-        if (work) st.template chunk<false>(c * kC, buf[c & 1], v);
+        if (work) st.template chunk<false>(c * kC, buf[c & 1], v, &exchange[unit], &ready[unit]);
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
@@ -981,7 +1065,7 @@ hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream
     HeadTiles *heads = reinterpret_cast<HeadTiles *>(keys + slots * p.Hk);
     gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, keys, heads);
     const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
-    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * (kWalkers + kLoaders)), 0, s>>>(
+    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
         p, keys, heads, groups, svec);
     return hipGetLastError();
 }

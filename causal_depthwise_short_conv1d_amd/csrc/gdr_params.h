@@ -77,6 +77,8 @@ inline int64_t gdr_slots(int64_t T, int64_t batch) { return T / 64 + batch + 2; 
 // Whether a call's heads are so few that walking prepared chunks in two kernels is faster than one kernel.
 inline bool gdr_few_heads(int64_t batch, int64_t Hv, int64_t Dv) { return batch * Hv * ((Dv + 63) / 64) <= 256; }
 
+constexpr int kVfMaxSlice = 8192;      // vocabulary entries of a slice, a multiple of 1024
+
 constexpr int kGdrMaxHeadK = 256;      // key channels a head of the recurrent kernel
 constexpr int kGdrMaxChunkK = 128;     // ... of the chunked kernel
 

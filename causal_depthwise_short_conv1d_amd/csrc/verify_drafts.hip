@@ -10,7 +10,7 @@
 // wrong by some 1e-14, so the choice does not depend on the slicing.
 // verify_sums_kernel streams the deciding row(s) once, a slice a workgroup,
 // and is bound by those reads; verify_pick_kernel (a workgroup a request)
-// scans the slice sums and reads one slice again.
+// scans the slice sums and reads one slice again, into registers).
 #include "gdr_params.h"
 #include "sconv_device.h"
 
@@ -109,89 +109,137 @@ __global__ __launch_bounds__(kVfBlock) void verify_sums_kernel(VerifyParams p) {
     }
 }
 
-// Inclusive running sum over the workgroup's threads, in thread order.
-__device__ __forceinline__ double block_scan(double v, double *part) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// Inclusive running sum over a wave's lanes.
+__device__ __forceinline__ double wave_scan(double v) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
         const double o = __shfl_up(v, m);
         if (lane >= m) v += o;
     }
-    __syncthreads();
-    if (lane == 63) part[w] = v;
-    __syncthreads();
-    for (int i = 0; i < w; ++i) v += part[i];
     return v;
 }
 
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+constexpr int kWaveSlice = kVfMaxSlice / (kVfBlock / 64);      // entries a wave scans
+constexpr int kRounds = kWaveSlice / 256;                      // of four consecutive entries a lane
+
 __global__ __launch_bounds__(kVfBlock) void verify_pick_kernel(VerifyParams p) {
-    const int32_t b = int32_t(blockIdx.x), tid = int32_t(threadIdx.x);
+    const int32_t b = int32_t(blockIdx.x), tid = int32_t(threadIdx.x), w = tid >> 6, lane = tid & 63;
     __shared__ double part[kVfBlock / 64];
-    __shared__ int32_t hit, last;
-    __shared__ double before;
-    Decision d = decide(p, b);
+    __shared__ int32_t found[kVfBlock / 64], last[kVfBlock / 64];
     const double *sums = p.sums_ws + int64_t(b) * p.slices * 2;
+    Decision d = decide(p, b);
 
-    // which sums count: of the residual, or of p when nothing is left of it
-    const int32_t per = (p.slices + kVfBlock - 1) / kVfBlock;
-    const int32_t s0 = tid * per, s1 = s0 + per < p.slices ? s0 + per : p.slices;
-    double t[2] = {0.0, 0.0};
-    for (int32_t s = s0; s < s1; ++s) { t[0] += sums[2 * s]; t[1] += sums[2 * s + 1]; }
-    const double c0 = block_scan(t[0], part);
-    __shared__ double total;
-    if (tid == kVfBlock - 1) total = c0;
-    __syncthreads();
-    const int which = total > 0.0 ? 0 : 1;
-    __syncthreads();
-    const double cum = which == 0 ? c0 : block_scan(t[1], part);
-    if (which == 1) { d.q = nullptr; d.out_token = -1; }
-    if (tid == 0) { hit = INT32_MAX; last = -1; }
-    if (tid == kVfBlock - 1) total = cum;
-    __syncthreads();
-    const double goal = double(p.u_smp[b]) * total;
-
-    // the first slice whose running sum exceeds the goal, else the last one with any mass
-    {
-        double c = cum - t[which];
-        if (t[which] > 0.0) {
-            for (int32_t s = s0; s < s1; ++s) {
-                const double m = sums[2 * s + which];
-                if (m > 0.0) atomicMax(&last, s);
-                if (m > 0.0 && c + m > goal) { atomicMin(&hit, s); break; }
-                c += m;
+    // Every wave by itself: which slice.  A lane takes `per` consecutive slice sums.
+    const int32_t per = (p.slices + 63) / 64;
+    const int32_t s0 = lane * per, s1 = s0 + per < p.slices ? s0 + per : p.slices;
+    double t0 = 0.0, t1 = 0.0;
+    for (int32_t s = s0; s < s1; ++s) { t0 += sums[2 * s]; t1 += sums[2 * s + 1]; }
+    double cum = wave_scan(t0), own = t0;
+    int which = 0;
+    if (!(__shfl(cum, 63) > 0.0)) {                    // nothing is left of p - q: by p itself
+        cum = wave_scan(t1);
+        own = t1;
+        which = 1;
+        d.q = nullptr;
+        d.out_token = -1;
+    }
+    const double goal = double(p.u_smp[b]) * __shfl(cum, 63);
+    const uint64_t some = __ballot(own > 0.0), over = __ballot(own > 0.0 && cum > goal);
+    // the first lane whose running sum exceeds the goal, else the last one with any mass
+    const int at = over ? __builtin_ctzll(over) : (some ? 63 - __builtin_clzll(some) : 0);
+    int32_t slice = -1;
+    double before = cum - own;
+    if (lane == at && some) {
+        double run = before;                           // before the slice at hand; `before`: before the chosen one
+        for (int32_t s = s0; s < s1; ++s) {
+            const double m = sums[2 * s + which];
+            if (m > 0.0) {
+                slice = s;
+                before = run;
+                if (run + m > goal) break;
             }
+            run += m;
         }
     }
-    __syncthreads();
-    const bool found = hit != INT32_MAX;
-    const int32_t slice = found ? hit : last;
-    if (slice >= s0 && slice < s1) {
-        double c = cum - t[which];
-        for (int32_t s = s0; s < slice; ++s) c += sums[2 * s + which];
-        before = c;
-    }
-    __syncthreads();
-    if (tid == 0) { hit = INT32_MAX; last = -1; }
-    __syncthreads();
+    slice = __shfl(slice, at);
+    before = __shfl(before, at);
+
+    // The slice again, a quarter a wave, four consecutive entries a lane and round: (wave, round, lane) is index order.
+    int32_t hit = INT32_MAX, top = -1;
     if (slice >= 0) {
-        // a thread takes consecutive entries, so thread order is index order
         const int32_t lo = slice * p.slice, hi = lo + p.slice < p.vocab ? lo + p.slice : p.vocab;
-        const int32_t w = (p.slice + kVfBlock - 1) / kVfBlock;
-        const int32_t i0 = lo + tid * w, i1 = i0 + w < hi ? i0 + w : hi;
-        double m = 0.0;
-        for (int32_t i = i0; i < i1; ++i) m += left_of(d, i, d.p[i], d.q ? d.q[i] : 0.0f);
-        double c = before + (block_scan(m, part) - m);
-        if (m > 0.0) {
-            for (int32_t i = i0; i < i1; ++i) {
-                const double x = left_of(d, i, d.p[i], d.q ? d.q[i] : 0.0f);
-                if (x > 0.0) atomicMax(&last, i);
-                c += x;
-                if (x > 0.0 && c > goal) { atomicMin(&hit, i); break; }
+        const int32_t quarter = (p.slice + kVfBlock / 64 - 1) / (kVfBlock / 64);
+        const int32_t w0 = lo + w * quarter, w1 = w0 + quarter < hi ? w0 + quarter : hi;
+        float x[kRounds][4];                           // fp32 suffices for p and q; masses are formed in fp64
+        float y[kRounds][4];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int32_t i = w0 + 256 * r + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[r][e] = y[r][e] = 0.0f;
+            if (i + 4 <= w1) {
+                const f32x4u v = *reinterpret_cast<const f32x4u *>(d.p + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[r][e] = v[e];
+                if (d.q) {
+                    const f32x4u q = *reinterpret_cast<const f32x4u *>(d.q + i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[r][e] = q[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i + e < w1) {
+                        x[r][e] = d.p[i + e];
+                        if (d.q) y[r][e] = d.q[i + e];
+                    }
             }
         }
+        double round[kRounds], all = 0.0;
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            round[r] = 0.0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) round[r] += left_of(d, w0 + 256 * r + 4 * lane + e, x[r][e], y[r][e]);
+            all += round[r];
+        }
+        all = wave_sum(all);
+        if (lane == 0) part[w] = all;
         __syncthreads();
+        double c = before;
+        for (int i = 0; i < w; ++i) c += part[i];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (hit != INT32_MAX) break;
+            const double end = wave_scan(round[r]);
+            double run = c + (end - round[r]);
+            int32_t h = INT32_MAX, l = -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int32_t i = w0 + 256 * r + 4 * lane + e;
+                const double m = left_of(d, i, x[r][e], y[r][e]);
+                run += m;
+                if (m > 0.0) {
+                    l = i;
+                    if (h == INT32_MAX && run > goal) h = i;
+                }
+            }
+            const uint64_t hs = __ballot(h != INT32_MAX), ls = __ballot(l >= 0);
+            if (hs) hit = __shfl(h, __builtin_ctzll(hs));
+            if (ls) top = __shfl(l, 63 - __builtin_clzll(ls));
+            c += __shfl(end, 63);
+        }
+        if (lane == 0) { found[w] = hit; last[w] = top; }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kVfBlock / 64; ++i) {
+            hit = found[i] < hit ? found[i] : hit;
+            top = last[i] > top ? last[i] : top;
+        }
     }
-    const int32_t token = slice < 0 ? 0 : (hit != INT32_MAX ? hit : last);
+    const int32_t token = slice < 0 ? 0 : (hit != INT32_MAX ? hit : top);
     for (int32_t i = tid; i <= p.max_drafts; i += kVfBlock)
         p.tokens[b * p.t_sr + i] = i < d.count ? p.draft_tokens[d.d0 + i] : (i == d.count ? token : -1);
     if (tid == 0) p.num_accepted[b] = d.count + 1;
