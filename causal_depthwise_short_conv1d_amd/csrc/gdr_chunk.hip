@@ -647,76 +647,87 @@ struct Consumer {
         }
     }
 
-    // The state through one chunk.  WHOLE: the output too, with few registers (the values are read inside, the products
-    // held apart); else v comes in and goes out with the next chunk's, and the output is another wave's.
-    template <bool WHOLE>
-    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16], Exchange<KT> *ex, int *ready) {
+    // The units of the next state: 2^14 above a bound of it (64 tokens, |k16| < 1.5, so the chunk adds at most 2^7 max |z|
+    // to what is left of the last one).  z comes in its own unit, 2^(xe - 12) of the state's.
+    struct Units { float zs, sc, ninv; };
+    __device__ __forceinline__ Units next_unit(const f32x4 (&z)[4], float ms, float last, int xe) {
+        float zm = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) zm = fmaxf(zm, fabsf(z[mt][i]));
+        const float bound = max_groups(fmaf(zm * pow2(xe - 12), 128.0f, ms * last));
+        int up = 14 - exp_of(bound);
+        up = up < -126 - un ? -126 - un : (up > 126 - un ? 126 - un : up);
+        up = up < -114 ? -114 : up;
+        int zu = xe - 12 + up;
+        zu = zu < -126 ? -126 : (zu > 126 ? 126 : zu);
+        un += up;
+        return {pow2(zu), last * pow2(up), pow2(-un)};
+    }
+    __device__ __forceinline__ void split_state(int kt, f16x8 &hi, f16x8 &lo) const {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = S[2 * kt + (j >> 2)][j & 3];
+        split8(f, hi, lo);
+    }
+    __device__ __forceinline__ float largest() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[d][i]));
+        return m;
+    }
+    // z of tiles 2 tt and 2 tt + 1 as an fp16 operand, and y = e^(G_last - G) z.
+    static __device__ __forceinline__ f16x8 scaled(const f32x4 (&z)[4], int tt, float zs, const f32x4 (&eg)[2], float (&y)[8]) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = z[2 * tt + (j >> 2)][j & 3] * zs;
+            y[j] = f[j] * eg[j >> 2][j & 3];
+        }
+        return half8(f);
+    }
+    static __device__ __forceinline__ f32x4 row4(const float *v, int t) { return *reinterpret_cast<const f32x4 *>(v + t); }
+
+    // The state and the output through one chunk, in as few registers as go: four waves a SIMD hide what each waits for.
+    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b) {
         const int lane = fresh(lane0), g = lane >> 4;
         f32x4 ak[4], aq[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) { ak[mt] = f32x4{0, 0, 0, 0}; aq[mt] = f32x4{0, 0, 0, 0}; }
-        float ms = 0.0f;
-        const float oinv = pow2(-un);
-        // the state in high and low parts (its largest element is below 2^15)
-        f16x8 sh[WHOLE ? 1 : KT], sl[WHOLE ? 1 : KT];
-        const auto part = [&](int kt, f16x8 &hi, f16x8 &lo) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[j] = S[2 * kt + (j >> 2)][j & 3];
-                ms = fmaxf(ms, fabsf(f[j]));
-            }
-            split8(f, hi, lo);
-        };
-        if constexpr (!WHOLE) {
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                part(kt, sh[kt], sl[kt]);
-                ex->s[kt * 64 + lane] = sh[kt];
-            }
-            if (lane < 16) ex->oinv[lane] = oinv;
-            hand_over(ready);
-        }
-        // K S and Q S
+        const float ms = largest(), oinv = pow2(-un), unit = pow2(un);
+        // K S and Q S, the state split on the way (its largest element is below 2^15)
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-            if constexpr (WHOLE) part(kt, sh[0], sl[0]);
-            const f16x8 &hi = sh[WHOLE ? 0 : kt], &lo = sl[WHOLE ? 0 : kt];
+            f16x8 hi, lo;
+            split_state(kt, hi, lo);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const f16x8 kf = row_tile_of(b.k, mt * KT + kt, kt, lane);
+                const f16x8 kf = row_tile_of(b.k, mt * KT + kt, kt, lane), qf = row_tile_of(b.q, mt * KT + kt, kt, lane);
                 ak[mt] = mfma(kf, hi, ak[mt]);
-                if constexpr (WHOLE) {
-                    aq[mt] = mfma(row_tile_of(b.q, mt * KT + kt, kt, lane), hi, aq[mt]);
-                    ak[mt] = mfma(kf, lo, ak[mt]);
-                    if (mt == 1) __builtin_amdgcn_sched_barrier(0);
-                }
+                aq[mt] = mfma(qf, hi, aq[mt]);
+                ak[mt] = mfma(kf, lo, ak[mt]);
+                if (mt == 1) __builtin_amdgcn_sched_barrier(0);
             }
-            if constexpr (WHOLE) {
-                __builtin_amdgcn_sched_barrier(0);
-            } else {
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(row_tile_of(b.k, mt * KT + kt, kt, lane), lo, ak[mt]);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (WHOLE) fetch(t0, v);             // (from L2; registers are what bounds the products above)
         // X, scaled to 2^12
+        uint16_t v[16];
+        fetch(t0, v);                                  // (from L2; registers are what bounds the products above)
         float x[16], xm = 0.0f;
-        const float unit = pow2(un);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const int t = tok_of(mt, 4 * g);
-            const f32x4 ka = *reinterpret_cast<const f32x4 *>(b.ka + t), kb = *reinterpret_cast<const f32x4 *>(b.kb + t);
+            const f32x4 ka = row4(b.ka, tok_of(mt, 4 * g)), kb = row4(b.kb, tok_of(mt, 4 * g));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * bf_one(v[4 * mt + i]));
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
-        if constexpr (!WHOLE) fetch(t0 + kC, v);       // (rows behind the end read as zero)
         const int xe = exp_of(max_groups(xm));
         const float xs = pow2(12 - xe);
-
         // z = T X
         f32x4 z[4];
 #pragma unroll
@@ -734,104 +745,182 @@ struct Consumer {
                 z[mt] = mfma(h, xl, z[mt]);
                 z[mt] = mfma(l, xh, z[mt]);
             }
-            if constexpr (WHOLE) __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // the next unit: from a bound of the next state (64 tokens, |k16| < 1.5, so it adds at most 2^7 max |z|),
-        // brought below 2^15
-        float zm = 0.0f;
+        const Units u = next_unit(z, ms, b.last, xe);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) zm = fmaxf(zm, fabsf(z[mt][i]));
-        const float last = b.last;
-        // in the present unit z is z * 2^(xe - 12)
-        const float bound = max_groups(fmaf(zm * pow2(xe - 12), 128.0f, ms * last));
-        int up = 14 - exp_of(bound);
-        up = up < -126 - un ? -126 - un : (up > 126 - un ? 126 - un : up);
-        up = up < -114 ? -114 : up;
-        int zu = xe - 12 + up;
-        zu = zu < -126 ? -126 : (zu > 126 ? 126 : zu);
-        const float zs = pow2(zu), sc = last * pow2(up);
-        un += up;
-        const float ninv = pow2(-un);
-
-        f16x8 zh[2];
-        float y[WHOLE ? 1 : 2][8];
-        const auto scaled = [&](int tt, float (&to)[8]) {
-            float f[8];
-#pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2) {
-                const f32x4 eg = *reinterpret_cast<const f32x4 *>(b.eg + tok_of(2 * tt + t2, 4 * g));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[4 * t2 + i] = z[2 * tt + t2][i] * zs;
-                    to[4 * t2 + i] = f[4 * t2 + i] * eg[i];
-                }
-            }
-            zh[tt] = half8(f);
-        };
-        if constexpr (!WHOLE) {
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                scaled(tt, y[tt]);
-                ex->z[tt * 64 + lane] = zh[tt];
-            }
-            if (lane < 16) ex->ninv[lane] = ninv;
-            hand_over(ready);
-        }
+        for (int d = 0; d < 2 * KT; ++d) S[d] *= u.sc;
         // S += K^T y
-#pragma unroll
-        for (int d = 0; d < 2 * KT; ++d) S[d] *= sc;
+        f16x8 zh[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
+            const f32x4 eg[2] = {row4(b.eg, tok_of(2 * tt, 4 * g)), row4(b.eg, tok_of(2 * tt + 1, 4 * g))};
+            float y[8];
             f16x8 yh, yl;
-            if constexpr (WHOLE) scaled(tt, y[0]);
-            split8(y[WHOLE ? 0 : tt], yh, yl);
+            zh[tt] = scaled(z, tt, u.zs, eg, y);
+            split8(y, yh, yl);
 #pragma unroll
             for (int d = 0; d < 2 * KT; ++d) {
                 const f16x8 k = col_tile_of(b.kt, d, tt, lane);
                 S[d] = mfma(k, yh, S[d]);
                 S[d] = mfma(k, yl, S[d]);
             }
-            if constexpr (WHOLE) __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (WHOLE) output(t0, b, lane, aq, zh, oinv, ninv);
-    }
-
-    // o from Q S and z.
-    __device__ __forceinline__ void output(int64_t t0, const Tiles<KT> &b, int lane, const f32x4 (&aq)[4], const f16x8 (&zh)[2],
-                                           float oinv, float ninv) {
-        const int g = lane >> 4;
+        // o
         float o[16];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             f32x4 pz = {0, 0, 0, 0};
 #pragma unroll
             for (int tt = 0; tt <= mt / 2; ++tt) pz = mfma(tile_of(b.p, tri_tile(mt, tt), lane), zh[tt], pz);
-            const f32x4 qf = *reinterpret_cast<const f32x4 *>(b.qf + tok_of(mt, 4 * g));
-            const f32x4 qe = *reinterpret_cast<const f32x4 *>(b.qe + tok_of(mt, 4 * g));
+            const f32x4 qf = row4(b.qf, tok_of(mt, 4 * g)), qe = row4(b.qe, tok_of(mt, 4 * g));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[i] * ninv, pz[i], qe[i] * oinv * aq[mt][i]);
+            for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[i] * u.ninv, pz[i], qe[i] * oinv * aq[mt][i]);
         }
         store(t0, o);
     }
 
-    // The output of one chunk from what the state wave hands over; `done` halves came before.
-    __device__ __forceinline__ void emit(int64_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
-        const int lane = fresh(lane0), n = lane & 15;
-        f32x4 aq[4];
+    // The state alone through one chunk, one wave a SIMD: what a product needs beside the last one's result is read and
+    // computed before that result is there.  v comes in and goes out with the next chunk's.
+    __device__ __forceinline__ void advance(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16], Exchange<KT> *ex, int *ready) {
+        const int lane = fresh(lane0), g = lane >> 4;
+        f16x8 sh[KT], sl[KT];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) aq[mt] = f32x4{0, 0, 0, 0};
+        for (int kt = 0; kt < KT; ++kt) {
+            split_state(kt, sh[kt], sl[kt]);
+            ex->s[kt * 64 + lane] = sh[kt];
+        }
+        if (lane < 16) ex->oinv[lane] = pow2(-un);
+        hand_over(ready);
+        // K S
+        f32x4 ak[4];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            f16x8 k[4];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) k[mt] = row_tile_of(b.k, mt * KT + kt, kt, lane);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(k[mt], sh[kt], kt ? ak[mt] : f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(k[mt], sl[kt], ak[mt]);
+        }
+        const float unit = pow2(un), ms = largest();
+        f32x4 ka[4], xv[4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            ka[mt] = row4(b.ka, tok_of(mt, 4 * g));
+            const f32x4 kb = row4(b.kb, tok_of(mt, 4 * g)) * unit;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xv[mt][i] = kb[i] * bf_one(v[4 * mt + i]);
+        }
+        f16x8 th[kTriTiles], tl[kTriTiles];
+#pragma unroll
+        for (int i = 0; i < kTriTiles; ++i) { th[i] = tile_of(b.th, i, lane); tl[i] = tile_of(b.tl, i, lane); }
+        __builtin_amdgcn_sched_barrier(0);
+        // X, scaled to 2^12
+        float xm = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xv[mt][i] = fmaf(-ka[mt][i], ak[mt][i], xv[mt][i]);
+                xm = fmaxf(xm, fabsf(xv[mt][i]));
+            }
+        const int xe = exp_of(max_groups(xm));
+        const float xs = pow2(12 - xe);
+        // z = T X
+        f32x4 z[4];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            float f[8];
+            f16x8 xh, xl;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = xv[2 * tt + (j >> 2)][j & 3] * xs;
+            split8(f, xh, xl);
+#pragma unroll
+            for (int mt = 2 * tt; mt < 4; ++mt) z[mt] = mfma(th[tri_tile(mt, tt)], xh, tt ? z[mt] : f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int mt = 2 * tt; mt < 4; ++mt) z[mt] = mfma(th[tri_tile(mt, tt)], xl, z[mt]);
+#pragma unroll
+            for (int mt = 2 * tt; mt < 4; ++mt) z[mt] = mfma(tl[tri_tile(mt, tt)], xh, z[mt]);
+        }
+        fetch(t0 + kC, v);                             // (rows behind the end read as zero)
+        const float last = b.last;
+        f32x4 eg[4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) eg[mt] = row4(b.eg, tok_of(mt, 4 * g));
+        f16x8 kc[2 * KT];
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d) kc[d] = col_tile_of(b.kt, d, 0, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        const Units u = next_unit(z, ms, last, xe);
+        float y[2][8];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const f32x4 e[2] = {eg[2 * tt], eg[2 * tt + 1]};
+            ex->z[tt * 64 + lane] = scaled(z, tt, u.zs, e, y[tt]);
+        }
+        if (lane < 16) ex->ninv[lane] = u.ninv;
+        hand_over(ready);
+        // S += K^T y
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d) S[d] *= u.sc;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            f16x8 yh, yl;
+            split8(y[tt], yh, yl);
+            if (tt)
+#pragma unroll
+                for (int d = 0; d < 2 * KT; ++d) kc[d] = col_tile_of(b.kt, d, 1, lane);
+#pragma unroll
+            for (int d = 0; d < 2 * KT; ++d) S[d] = mfma(kc[d], yh, S[d]);
+#pragma unroll
+            for (int d = 0; d < 2 * KT; ++d) S[d] = mfma(kc[d], yl, S[d]);
+        }
+    }
+
+    // The output of one chunk from what the state wave hands over; `done` halves came before.  All but z's own product
+    // is ready when z comes.
+    __device__ __forceinline__ void emit(int64_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
+        const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
+        f32x4 aq[4], qf[4];
+        f16x8 q[4], pt[kTriTiles];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) q[mt] = row_tile_of(b.q, mt * KT, 0, lane);
         await(ready, done + 1);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             const f16x8 s = ex->s[kt * 64 + lane];
+            if (kt)
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) aq[mt] = mfma(row_tile_of(b.q, mt * KT + kt, kt, lane), s, aq[mt]);
+                for (int mt = 0; mt < 4; ++mt) q[mt] = row_tile_of(b.q, mt * KT + kt, kt, lane);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) aq[mt] = mfma(q[mt], s, kt ? aq[mt] : f32x4{0, 0, 0, 0});
         }
+        const float oinv = ex->oinv[n];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            qf[mt] = row4(b.qf, tok_of(mt, 4 * g));
+            aq[mt] *= row4(b.qe, tok_of(mt, 4 * g)) * oinv;
+        }
+#pragma unroll
+        for (int i = 0; i < kTriTiles; ++i) pt[i] = tile_of(b.p, i, lane);
+        __builtin_amdgcn_sched_barrier(0);
         await(ready, done + 2);
         const f16x8 zh[2] = {ex->z[lane], ex->z[64 + lane]};
-        output(t0, b, lane, aq, zh, ex->oinv[n], ex->ninv[n]);
+        const float ninv = ex->ninv[n];
+        f32x4 pz[4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) pz[mt] = mfma(pt[tri_tile(mt, 0)], zh[0], f32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int mt = 2; mt < 4; ++mt) pz[mt] = mfma(pt[tri_tile(mt, 1)], zh[1], pz[mt]);
+        float o[16];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[mt][i] * ninv, pz[mt][i], aq[mt][i]);
+        store(t0, o);
     }
 };
 
@@ -905,10 +994,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
         uint32_t word = 0;
         if (more) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
-        if (work) {
-            uint16_t v[16];
-            st.template chunk<true>(c * kC, tiles, v, nullptr, nullptr);
-        }
+        if (work) st.chunk(c * kC, tiles);
         asm volatile("" : : "v"(word));
         __syncthreads();
     }
@@ -1040,7 +1126,7 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
     st.fetch(0, v);
     __syncthreads();
     for (int64_t c = 0; c < nc; ++c) {
-        if (work) st.template chunk<false>(c * kC, buf[c & 1], v, &exchange[unit], &ready[unit]);
+        if (work) st.advance(c * kC, buf[c & 1], v, &exchange[unit], &ready[unit]);
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
