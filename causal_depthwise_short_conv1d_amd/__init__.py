@@ -546,18 +546,31 @@ def sconv_paged_fused_multi(xs, weights, cache, positions, slot_mapping, query_s
 
 # ------------------------------------------------------- gated delta rule --
 
+def _ptr(t, dtype, name, dev):
+    """Address of a checked tensor (None passes); the failing checks are _dev's."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != dev or not t.is_cuda:
+        _dev(t, dtype, name, dev)
+    return t.data_ptr()
+
+
 def _gdr_gates(g, beta, A_log, dt_bias, lead, hv, dev):
     """The two gate tensors and the layer's parameters, checked and marshalled."""
-    if (A_log is None) != (dt_bias is None):
-        raise ValueError("A_log and dt_bias go together")
-    dt = torch.float32 if A_log is None else torch.bfloat16
-    if g.shape != (*lead, hv) or beta.shape != (*lead, hv):
+    want = (*lead, hv)
+    if g.shape != want or beta.shape != want:
         raise ValueError("g and beta need one value per token and value head")
+    f32 = torch.float32
+    if A_log is None and dt_bias is None:
+        return (_ptr(g, f32, "g", dev), *g.stride(), _ptr(beta, f32, "beta", dev), *beta.stride(), None, None)
+    if A_log is None or dt_bias is None:
+        raise ValueError("A_log and dt_bias go together")
     for t in (A_log, dt_bias):
-        if t is not None and (t.shape != (hv,) or (hv > 1 and t.stride(0) != 1)):
+        if t.shape != (hv,) or (hv > 1 and t.stride(0) != 1):
             raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
-    return (_dev(g, dt, "g", dev), *g.stride(), _dev(beta, dt, "beta", dev), *beta.stride(),
-            _dev(A_log, torch.float32, "A_log", dev), _dev(dt_bias, torch.float32, "dt_bias", dev))
+    bf = torch.bfloat16
+    return (_ptr(g, bf, "g", dev), *g.stride(), _ptr(beta, bf, "beta", dev), *beta.stride(),
+            _ptr(A_log, f32, "A_log", dev), _ptr(dt_bias, f32, "dt_bias", dev))
 
 
 def _gdr_shapes(q, k, v, state, out):
@@ -600,24 +613,24 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     batch = query_start_loc.numel() - 1
     bf = torch.bfloat16
     args = (
-        _dev(q, bf, "q", dev), *q.stride(), _dev(k, bf, "k", dev), *k.stride(),
-        _dev(v, bf, "v", dev), *v.stride(),
+        _ptr(q, bf, "q", dev), *q.stride(), _ptr(k, bf, "k", dev), *k.stride(),
+        _ptr(v, bf, "v", dev), *v.stride(),
         *_gdr_gates(g, beta, A_log, dt_bias, (total,), hv, dev),
-        _dev(state, torch.float32, "state", dev),
+        _ptr(state, torch.float32, "state", dev),
         *(state.stride() if state is not None else (0, 0, 0, 0)),
         state.shape[0] if state is not None else 0,
         _index(cache_indices, torch.int32, "cache_indices", dev, batch),
         _index(has_initial_state, torch.bool, "has_initial_state", dev, batch),
         _index(query_start_loc, torch.int32, "query_start_loc", dev),
         batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
-        1 if use_qk_l2norm else 0, pad_slot_id, _dev(out, bf, "out", dev), *out.stride(),
+        1 if use_qk_l2norm else 0, pad_slot_id, _ptr(out, bf, "out", dev), *out.stride(),
     )
-    vector = dk % 8 == 0 and q.stride(2) == 1 and k.stride(2) == 1 and all(
-        t.data_ptr() % 16 == 0 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 for t in (q, k)) and all(
-        t.stride(0) >= t.shape[2] * t.stride(2) for t in (q, k, v, out))
+    vector = dk % 8 == 0 and dv % 8 == 0 and all(
+        t.stride(2) == 1 and t.stride(0) >= t.shape[2] and t.stride(0) % n == 0 and t.stride(1) % n == 0 and
+        t.data_ptr() % (2 * n) == 0 for t, n in ((q, 8), (k, 8), (v, 8), (out, 4)))
     need = load_library().gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    args += (_dev(ws, torch.uint8, "workspace", dev), need)
+    args += (ws.data_ptr() if need else None, need)
     _launch("gdr_fwd_varlen", dev, args)
     return out
 
@@ -665,15 +678,15 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
         raise ValueError("output_state_indices must be (batch, >= seqlen)")
     bf, i32 = torch.bfloat16, torch.int32
     args = (
-        _dev(q, bf, "q", dev), *q.stride(), _dev(k, bf, "k", dev), *k.stride(),
-        _dev(v, bf, "v", dev), *v.stride(),
+        _ptr(q, bf, "q", dev), *q.stride(), _ptr(k, bf, "k", dev), *k.stride(),
+        _ptr(v, bf, "v", dev), *v.stride(),
         *_gdr_gates(g, beta, A_log, dt_bias, (batch, seqlen), hv, dev),
-        _dev(state, torch.float32, "state", dev), *state.stride(), state.shape[0],
-        _dev(ci, i32, "cache_indices", dev), *ci_st, steps,
+        _ptr(state, torch.float32, "state", dev), *state.stride(), state.shape[0],
+        _ptr(ci, i32, "cache_indices", dev), *ci_st, steps,
         _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
-        _dev(osi, i32, "output_state_indices", dev), *(osi.stride() if osi is not None else (0, 0)),
+        _ptr(osi, i32, "output_state_indices", dev), *(osi.stride() if osi is not None else (0, 0)),
         batch, seqlen, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
-        1 if use_qk_l2norm else 0, pad_slot_id, _dev(ov, bf, "out", dev), *ov.stride(),
+        1 if use_qk_l2norm else 0, pad_slot_id, _ptr(ov, bf, "out", dev), *ov.stride(),
     )
     _launch("gdr_update", dev, args)
     return out
@@ -719,15 +732,15 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
     args = (
         _index(draft_tokens, i32, "draft_tokens", dev),
         _index(draft_start_loc, i32, "draft_start_loc", dev),
-        _dev(target_probs, f32, "target_probs", dev), target_probs.stride(0),
-        _dev(draft_probs, f32, "draft_probs", dev),
+        _ptr(target_probs, f32, "target_probs", dev), target_probs.stride(0),
+        _ptr(draft_probs, f32, "draft_probs", dev),
         draft_probs.stride(0) if draft_probs is not None else 0,
         _index(accept_uniform, f32, "accept_uniform", dev, nd),
         _index(sample_uniform, f32, "sample_uniform", dev, batch),
         batch, nd, vocab, max_drafts,
-        _dev(tokens, i32, "tokens", dev), tokens.stride(0),
+        _ptr(tokens, i32, "tokens", dev), tokens.stride(0),
         _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
-        _dev(ws, torch.uint8, "workspace", dev), ws_bytes,
+        ws.data_ptr(), ws_bytes,
     )
     _launch("sconv_verify_drafts", dev, args)
     return tokens, num_accepted_tokens

@@ -165,14 +165,13 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
     p.group = p.Hv / p.Hk;
     const int64_t T = total_tokens;
     if (p.Dk <= kGdrMaxChunkK) {
-        // 16-byte rows of q and k; rows longer than a head, a chunk's within the 31 bits of a descriptor's offsets
-        const auto rows = [](const GdrTensor &t, int64_t d) {
-            return t.sd < (1 << 24) && d * t.sd <= t.st && t.st < (1 << 23);
+        // 16-byte pieces of q, k and v, 8-byte ones of out; rows longer than a head, a chunk's within the 31 bits of a
+        // descriptor's offsets
+        const auto rows = [&](const void *a, const GdrTensor &t, int32_t heads, int32_t d, int n) {
+            return d % n == 0 && t.sd == 1 && d <= t.st && t.st < (1 << 23) && groups_of(a, n, 2, {T, heads}, {t.st, t.sh});
         };
-        const bool vec8 = rows(p.qs, p.Dk) && rows(p.ks, p.Dk) && rows(p.vs, p.Dv) && rows(p.os, p.Dv) && p.Dk % 8 == 0 &&
-                          p.qs.sd == 1 && p.ks.sd == 1 &&
-                          groups_of(q, 8, 2, {T, p.Hk}, {p.qs.st, p.qs.sh}) &&
-                          groups_of(k, 8, 2, {T, p.Hk}, {p.ks.st, p.ks.sh});
+        const bool vec8 = rows(q, p.qs, p.Hk, p.Dk, 8) && rows(k, p.ks, p.Hk, p.Dk, 8) && rows(v, p.vs, p.Hv, p.Dv, 8) &&
+                          rows(out, p.os, p.Hv, p.Dv, 4);
         const bool svec = state && p.Dk % 4 == 0 && p.s_sk == 1 &&
                           groups_of(state, 4, 4, {p.num_lines, p.Hv, p.Dv}, {p.s_sl, p.s_sh, p.s_sv});
         const int64_t need = gdr_fwd_workspace_bytes(batch, T, p.Hk, p.Hv, p.Dk, p.Dv, vec8);

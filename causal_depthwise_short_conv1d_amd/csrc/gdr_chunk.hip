@@ -38,7 +38,7 @@ namespace {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kC = 64;                 // tokens per chunk
 constexpr int kWaves = 8;              // waves per workgroup, 16 value channels each
@@ -551,7 +551,7 @@ struct Consumer {
     const int lane0;
     const uint16_t *vh;                // the head's first channel of v, row 0 of the sequence
     uint16_t *oh;
-    int32_t col;                       // this lane's channel
+    int32_t c0;                        // the wave's first channel; lane l has c0 + l % 16
     f32x4 S[2 * KT];                   // the state times 2^un
     int un;
 
@@ -559,7 +559,7 @@ struct Consumer {
     template <class F>
     __device__ __forceinline__ void rows_of(float *rows, F f) {
         const int lane = fresh(lane0), g = lane >> 4;
-        const int32_t c = col - (lane0 & 15) + (lane & 15);
+        const int32_t c = c0 + (lane & 15);
         float *row = rows + c * p.s_sv;
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d) f(d, row, 32 * (d >> 1) + 8 * g + 4 * (d & 1), c < p.Dv);
@@ -602,47 +602,65 @@ struct Consumer {
         });
     }
 
-    // Element (token, channel) accesses of the result layout: rows tok_of(mt, 4 g + i) = 8 g + a constant.  VEC: a
-    // descriptor over the chunk's rows, each longer than the head's channels, so what does not exist lies past its end.
+    // Rows of v and out, channels 8 or 4 at a time.  VEC: through a descriptor over the chunk's rows, each longer than the
+    // head's channels, so what does not exist lies past its end.
     __device__ __forceinline__ Rsrc rows(const uint16_t *base, int64_t t0, const GdrTensor &ts) const {
         const int64_t left = sp.n - t0 < kC ? sp.n - t0 : kC;
         return make_rsrc(base + t0 * ts.st, left * ts.st * 2);
     }
-    template <class F>
-    __device__ __forceinline__ void each(const GdrTensor &ts, F f) {
-        const int lane = fresh(lane0);
-        const int32_t c = col - (lane0 & 15) + (lane & 15);
-        const uint32_t row = uint32_t(ts.st) * 2;
-        const uint32_t at = c < p.Dv ? uint32_t(8 * (lane >> 4)) * row + uint32_t(c) * uint32_t(ts.sd) * 2 : kOob;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) f(r, at + uint32_t(tok_of(r >> 2, r & 3)) * row);
-    }
 
-    // The chunk's values: [4 mt + i].
-    __device__ __forceinline__ void fetch(int64_t t0, uint16_t (&v)[16]) {
-        const int g = lane0 >> 4;
+    // The chunk's values as left operands: tile mt has token tok_of(mt, n) in row n, the wave's 16 channels in its first
+    // columns.  Times the identity they become results, a channel a lane, like everything they meet (with bf16 values
+    // nothing is rounded; it takes 4 loads where that layout would take 16).
+    __device__ __forceinline__ void fetch(int64_t t0, u32x4 (&v)[4]) {
+        const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
+        const int32_t c = c0 + 8 * g;
         if constexpr (VEC) {
             const Rsrc rs = rows(vh, t0, p.vs);
-            each(p.vs, [&](int r, uint32_t off) { v[r] = buf_ld16(rs, off); });
+            const uint32_t row = uint32_t(p.vs.st) * 2;
+            const uint32_t at = g < 2 && c < p.Dv ? uint32_t(tok_of(0, n)) * row + uint32_t(c) * 2 : kOob;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) v[mt] = buf_ld128<0>(rs, at + uint32_t(tok_of(mt, 0)) * row);
         } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t t = t0 + tok_of(r >> 2, 4 * g + (r & 3));
-                v[r] = t < sp.n && col < p.Dv ? vh[t * p.vs.st + col * p.vs.sd] : uint16_t(0);
+            for (int mt = 0; mt < 4; ++mt) {
+                const int64_t t = t0 + tok_of(mt, n);
+                const bool live = g < 2 && t < sp.n;
+                v[mt] = load8(vh + (live ? t : 0) * p.vs.st, p.vs.sd, c, p.Dv, live);
             }
         }
     }
+    // The identity as a right operand.
+    static __device__ __forceinline__ bf16x8 identity(int lane) {
+        bf16x8 r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = 8 * (lane >> 4) + j == (lane & 15) ? __bf16(1.0f) : __bf16(0.0f);
+        return r;
+    }
+    static __device__ __forceinline__ f32x4 values(const u32x4 &v, const bf16x8 &id) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), id, f32x4{0, 0, 0, 0}, 0, 0, 0);
+    }
 
-    __device__ __forceinline__ void store(int64_t t0, const float (&o)[16]) {
-        const int g = lane0 >> 4;
+    // The output of tile mt comes as a transpose: token tok_of(mt, n) in the lane, channels 4 g .. in its registers.
+    __device__ __forceinline__ void store(int64_t t0, const f32x4 (&o)[4]) {
+        const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
+        const int32_t c = c0 + 4 * g;
         if constexpr (VEC) {
             const Rsrc rs = rows(oh, t0, p.os);
-            each(p.os, [&](int r, uint32_t off) { __builtin_amdgcn_raw_buffer_store_b16(to_bf16(o[r]), rs, off, 0, 0); });
+            const uint32_t row = uint32_t(p.os.st) * 2;
+            const uint32_t at = c < p.Dv ? uint32_t(tok_of(0, n)) * row + uint32_t(c) * 2 : kOob;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                const u32x2 w = {pack_bf16x2(o[mt][0], o[mt][1]), pack_bf16x2(o[mt][2], o[mt][3])};
+                __builtin_amdgcn_raw_buffer_store_b64(w, rs, at + uint32_t(tok_of(mt, 0)) * row, 0, 0);
+            }
         } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t t = t0 + tok_of(r >> 2, 4 * g + (r & 3));
-                if (t < sp.n && col < p.Dv) oh[t * p.os.st + col * p.os.sd] = to_bf16(o[r]);
+            for (int mt = 0; mt < 4; ++mt) {
+                const int64_t t = t0 + tok_of(mt, n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t < sp.n && c + i < p.Dv) oh[t * p.os.st + (c + i) * p.os.sd] = to_bf16(o[mt][i]);
             }
         }
     }
@@ -707,22 +725,23 @@ struct Consumer {
             for (int mt = 0; mt < 4; ++mt) {
                 const f16x8 kf = row_tile_of(b.k, mt * KT + kt, kt, lane), qf = row_tile_of(b.q, mt * KT + kt, kt, lane);
                 ak[mt] = mfma(kf, hi, ak[mt]);
-                aq[mt] = mfma(qf, hi, aq[mt]);
+                aq[mt] = mfma(hi, qf, aq[mt]);         // (transposed, as the output is)
                 ak[mt] = mfma(kf, lo, ak[mt]);
                 if (mt == 1) __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         // X, scaled to 2^12
-        uint16_t v[16];
+        u32x4 v[4];
         fetch(t0, v);                                  // (from L2; registers are what bounds the products above)
         float x[16], xm = 0.0f;
+        const bf16x8 id = identity(lane);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            const f32x4 ka = row4(b.ka, tok_of(mt, 4 * g)), kb = row4(b.kb, tok_of(mt, 4 * g));
+            const f32x4 ka = row4(b.ka, tok_of(mt, 4 * g)), kb = row4(b.kb, tok_of(mt, 4 * g)), vv = values(v[mt], id);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * bf_one(v[4 * mt + i]));
+                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * vv[i]);
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
@@ -768,22 +787,23 @@ struct Consumer {
             __builtin_amdgcn_sched_barrier(0);
         }
         // o
-        float o[16];
+        f32x4 o[4], oi, ni;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { oi[i] = __shfl(oinv, 4 * g + i); ni[i] = __shfl(u.ninv, 4 * g + i); }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             f32x4 pz = {0, 0, 0, 0};
 #pragma unroll
-            for (int tt = 0; tt <= mt / 2; ++tt) pz = mfma(tile_of(b.p, tri_tile(mt, tt), lane), zh[tt], pz);
-            const f32x4 qf = row4(b.qf, tok_of(mt, 4 * g)), qe = row4(b.qe, tok_of(mt, 4 * g));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[i] * u.ninv, pz[i], qe[i] * oinv * aq[mt][i]);
+            for (int tt = 0; tt <= mt / 2; ++tt) pz = mfma(zh[tt], tile_of(b.p, tri_tile(mt, tt), lane), pz);
+            const int t = tok_of(mt, lane & 15);
+            o[mt] = b.qf[t] * ni * pz + b.qe[t] * oi * aq[mt];
         }
         store(t0, o);
     }
 
     // The state alone through one chunk, one wave a SIMD: what a product needs beside the last one's result is read and
     // computed before that result is there.  v comes in and goes out with the next chunk's.
-    __device__ __forceinline__ void advance(int64_t t0, const Tiles<KT> &b, uint16_t (&v)[16], Exchange<KT> *ex, int *ready) {
+    __device__ __forceinline__ void advance(int64_t t0, const Tiles<KT> &b, u32x4 (&v)[4], Exchange<KT> *ex, int *ready) {
         const int lane = fresh(lane0), g = lane >> 4;
         f16x8 sh[KT], sl[KT];
 #pragma unroll
@@ -807,12 +827,11 @@ struct Consumer {
         }
         const float unit = pow2(un), ms = largest();
         f32x4 ka[4], xv[4];
+        const bf16x8 id = identity(lane);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             ka[mt] = row4(b.ka, tok_of(mt, 4 * g));
-            const f32x4 kb = row4(b.kb, tok_of(mt, 4 * g)) * unit;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xv[mt][i] = kb[i] * bf_one(v[4 * mt + i]);
+            xv[mt] = row4(b.kb, tok_of(mt, 4 * g)) * unit * values(v[mt], id);
         }
         f16x8 th[kTriTiles], tl[kTriTiles];
 #pragma unroll
@@ -884,7 +903,7 @@ struct Consumer {
     // is ready when z comes.
     __device__ __forceinline__ void emit(int64_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
-        f32x4 aq[4], qf[4];
+        f32x4 aq[4];
         f16x8 q[4], pt[kTriTiles];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) q[mt] = row_tile_of(b.q, mt * KT, 0, lane);
@@ -896,30 +915,28 @@ struct Consumer {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) q[mt] = row_tile_of(b.q, mt * KT + kt, kt, lane);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) aq[mt] = mfma(q[mt], s, kt ? aq[mt] : f32x4{0, 0, 0, 0});
+            for (int mt = 0; mt < 4; ++mt) aq[mt] = mfma(s, q[mt], kt ? aq[mt] : f32x4{0, 0, 0, 0});
         }
-        const float oinv = ex->oinv[n];
+        const f32x4 oinv = row4(ex->oinv, 4 * g);
+        float qf[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
-            qf[mt] = row4(b.qf, tok_of(mt, 4 * g));
-            aq[mt] *= row4(b.qe, tok_of(mt, 4 * g)) * oinv;
+            qf[mt] = b.qf[tok_of(mt, n)];
+            aq[mt] *= b.qe[tok_of(mt, n)] * oinv;
         }
 #pragma unroll
         for (int i = 0; i < kTriTiles; ++i) pt[i] = tile_of(b.p, i, lane);
         __builtin_amdgcn_sched_barrier(0);
         await(ready, done + 2);
         const f16x8 zh[2] = {ex->z[lane], ex->z[64 + lane]};
-        const float ninv = ex->ninv[n];
-        f32x4 pz[4];
+        const f32x4 ninv = row4(ex->ninv, 4 * g);
+        f32x4 o[4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) pz[mt] = mfma(pt[tri_tile(mt, 0)], zh[0], f32x4{0, 0, 0, 0});
+        for (int mt = 0; mt < 4; ++mt) o[mt] = mfma(zh[0], pt[tri_tile(mt, 0)], f32x4{0, 0, 0, 0});
 #pragma unroll
-        for (int mt = 2; mt < 4; ++mt) pz[mt] = mfma(pt[tri_tile(mt, 1)], zh[1], pz[mt]);
-        float o[16];
+        for (int mt = 2; mt < 4; ++mt) o[mt] = mfma(zh[1], pt[tri_tile(mt, 1)], o[mt]);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[4 * mt + i] = fmaf(qf[mt][i] * ninv, pz[mt][i], aq[mt][i]);
+        for (int mt = 0; mt < 4; ++mt) o[mt] = qf[mt] * ninv * o[mt] + aq[mt];
         store(t0, o);
     }
 };
@@ -956,10 +973,35 @@ __device__ __forceinline__ bool sequence(const GdrParams &p, int32_t b, Span64 &
     return !(p.state && (line < 0 || line >= p.num_lines));
 }
 
+constexpr int kMaxRanked = 64 * kWaves;
+
+// The sequence that is r-th by length (the longest first): a workgroup takes as long as its sequence, and one that starts
+// late with a long one leaves the chip idle behind it.  A thread a sequence counts those before it.  More sequences than
+// threads stay in order.
+__device__ __forceinline__ int32_t ranked(const GdrParams &p, int32_t r, int32_t *len, int32_t *out) {
+    if (p.batch > kMaxRanked) return r;
+    const int t = threadIdx.x;
+    Span64 sp;
+    int64_t line;
+    int32_t n = 0;
+    if (t < p.batch) {
+        n = sequence(p, t, sp, line) ? int32_t(sp.n) : 0;
+        len[t] = n;
+    }
+    __syncthreads();
+    if (t < p.batch) {
+        int32_t before = 0;
+        for (int32_t i = 0; i < p.batch; ++i) before += len[i] > n || (len[i] == n && i < t);
+        if (before == r) *out = t;
+    }
+    __syncthreads();
+    return *out;
+}
+
 template <int KT, bool VEC>
 __device__ __forceinline__ Consumer<KT, VEC> consumer(const GdrParams &p, const Span64 &sp, int lane, int32_t h, int32_t tile) {
     Consumer<KT, VEC> st{p, sp, lane};
-    st.col = tile * 16 + (lane & 15);
+    st.c0 = tile * 16;
     st.vh = p.v + sp.t0 * p.vs.st + h * p.vs.sh;
     st.oh = p.out + sp.t0 * p.os.st + h * p.os.sh;
     return st;
@@ -969,8 +1011,10 @@ template <int KT, bool VEC>
 __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, int32_t groups, bool svec) {
     __shared__ Tiles<KT> tiles;
     __shared__ Scratch sh;
-    const Place pl = place_of(p, groups);
+    Place pl = place_of(p, groups);
     if (!pl.ok) return;
+    pl.b = __builtin_amdgcn_readfirstlane(
+        ranked(p, pl.b, reinterpret_cast<int32_t *>(sh.diag), reinterpret_cast<int32_t *>(sh.diag) + kMaxRanked));
     Span64 sp;
     int64_t line;
     if (!sequence(p, pl.b, sp, line)) return;
@@ -1095,13 +1139,26 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
             for (int i = 0; i < kHeadPer; ++i)
                 if (t + i * kN < kHead) h[t + i * kN] = rh[i];
         };
+        // the values are read a chunk ahead by the state waves, from memory some 2000 cycles away: one word of each row's
+        // 128 bytes brings them to L2 before
+        const auto touch = [&](int64_t c) {
+            uint32_t word = 0;
+            if constexpr (VEC) {
+                const int32_t ch = pl.cg * 16 * kWalkers;
+                if (t < kC && c * kC + t < sp.n && ch < p.Dv)
+                    word = p.v[(sp.t0 + c * kC + t) * p.vs.st + pl.h * p.vs.sh + ch];
+            }
+            return word;
+        };
         load(0);
         put(buf[0]);
         load(nc > 1 ? 1 : 0);
         __syncthreads();
         for (int64_t c = 0; c < nc; ++c) {
             put(buf[(c + 1) & 1]);
+            const uint32_t word = touch(c + 2);
             load(c + 2 < nc ? c + 2 : nc - 1);
+            asm volatile("" : : "v"(word));
             __syncthreads();
         }
         return;
@@ -1122,7 +1179,7 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
     float *rows = p.state ? p.state + line * p.s_sl + pl.h * p.s_sh : nullptr;
     if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
     else st.zero();
-    uint16_t v[16];
+    u32x4 v[4];
     st.fetch(0, v);
     __syncthreads();
     for (int64_t c = 0; c < nc; ++c) {

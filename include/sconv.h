@@ -425,8 +425,9 @@ int sconv_paged_fused_multi(int32_t num_streams,
  * num_v_heads must be a multiple of num_k_heads and head_dim_k at most 256
  *   (else SCONV_ERR_SHAPE).
  * Layouts and speed (results agree to rounding): unit channel strides with
- *   head_dim_k a multiple of 4 (decode) or of 8 (prefill) and rows aligned to
- *   16 bytes take the vector loads; every other layout loads by elements.
+ *   head_dim_k a multiple of 4 (decode), or head_dim_k and head_dim_v of 8
+ *   (prefill), and rows aligned to 16 bytes take the vector loads; every other
+ *   layout loads by elements.
  * Errors: a NULL tensor, or one of a_log / dt_bias without the other ->
  *   SCONV_ERR_NULL; bad sizes -> SCONV_ERR_SHAPE; a negative stride, or out /
  *   state with two elements at one address -> SCONV_ERR_STRIDE; a pointer not
