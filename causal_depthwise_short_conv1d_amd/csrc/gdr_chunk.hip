@@ -162,7 +162,23 @@ __device__ __forceinline__ f16x8 col_tile_of(const _Float16 *base, int d, int tt
     return *reinterpret_cast<const f16x8 *>(base + (2 * d + tt) * kTile + (lane ^ (d >> 1)) * 8);
 }
 
-struct Span64 { int64_t t0; int64_t n; };              // a sequence's first row and length
+struct Span32 { int32_t t0, n; };      // a sequence's first row and length
+
+// A head's rows of one tensor, from the sequence's first on.  VEC reads and writes them through a descriptor over a
+// chunk's rows, each longer than the head's channels, so that what does not exist lies past its end.
+struct Rows {
+    const uint16_t *base;
+    uint32_t row;                      // bytes (VEC)
+    const GdrTensor *ts;
+};
+__device__ __forceinline__ Rows rows_of(const uint16_t *t, const GdrTensor &ts, int32_t t0, int32_t h) {
+    return {t + t0 * ts.st + h * ts.sh, uint32_t(ts.st) * 2, &ts};
+}
+__device__ __forceinline__ Rsrc chunk_rsrc(const Rows &r, const Span32 &sp, int32_t c0) {
+    const int32_t left = sp.n - c0 < kC ? sp.n - c0 : kC;
+    const char *a = reinterpret_cast<const char *>(r.base) + uint64_t(uint32_t(c0)) * r.row;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(a), short(0), left <= 0 ? 0 : int(left * r.row), 0x00020000);
+}
 
 // --------------------------------------------------- preparing the chunk --
 
@@ -180,25 +196,20 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *row, int64_t sd, int c, i
 // Four token rows of eight channels each, as a producer thread holds them.
 struct Quad { u32x4 r[4]; };
 
-// VEC: 16-byte loads through a descriptor over the chunk's rows, each longer than the head's channels, so what does
-// not exist lies past its end.
 template <bool VEC>
-__device__ __forceinline__ Quad load_quad(const uint16_t *head, const GdrTensor &ts, const Span64 &sp, int64_t c0,
-                                          int quad, int kc, int32_t Dk) {
+__device__ __forceinline__ Quad load_quad(const Rows &r, const Span32 &sp, int32_t c0, int quad, int kc, int32_t Dk) {
     Quad q;
     if constexpr (VEC) {
-        const int64_t left = sp.n - c0 < kC ? sp.n - c0 : kC;
-        const Rsrc rs = make_rsrc(head + (sp.t0 + c0) * ts.st, left * ts.st * 2);
-        const uint32_t row = uint32_t(ts.st) * 2;
-        const uint32_t at = 8 * kc < Dk ? uint32_t(4 * quad) * row + 16u * kc : kOob;
+        const Rsrc rs = chunk_rsrc(r, sp, c0);
+        const uint32_t at = 8 * kc < Dk ? uint32_t(4 * quad) * r.row + 16u * kc : kOob;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q.r[i] = buf_ld128<0>(rs, at + i * row);
+        for (int i = 0; i < 4; ++i) q.r[i] = buf_ld128<0>(rs, at + i * r.row);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t t = c0 + 4 * quad + i;
+            const int32_t t = c0 + 4 * quad + i;
             const bool live = t < sp.n;
-            q.r[i] = load8(head + (sp.t0 + (live ? t : 0)) * ts.st, ts.sd, 8 * kc, Dk, live);
+            q.r[i] = load8(r.base + (live ? t : 0) * r.ts->st, r.ts->sd, 8 * kc, Dk, live);
         }
     }
     return q;
@@ -288,36 +299,34 @@ struct Prepare {
     _Float16 *k, *q;                   // the chunk's rows as tiles, in LDS
     KeyTiles<KT> *kt;                  // where the tiles go: LDS (k and q are its own) or memory
     HeadTiles *ht;
-    const Span64 sp;
+    const Span32 sp;
     const int lane0, w;
     int h;                             // value head
-    const uint16_t *qh, *kh;
+    const Rows qr, kr;
 
     // The first waves stage the keys, as many after them the queries: 4 KT threads a row, four rows a thread.
     static constexpr int kStage = KT;  // waves
     __device__ __forceinline__ int quad_of(int lane) const { return (64 * (w & (kStage - 1)) + lane) / (4 * KT); }
 
-    __device__ __forceinline__ void stage(int64_t c0) {
+    __device__ __forceinline__ void stage(int32_t c0) {
         const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
         if (w < kStage)
-            stage_quad<KT, true>(load_quad<VEC>(kh, p.ks, sp, c0, quad, kc, p.Dk), k, kt->k == k ? nullptr : kt->k, kt->kt,
+            stage_quad<KT, true>(load_quad<VEC>(kr, sp, c0, quad, kc, p.Dk), k, kt->k == k ? nullptr : kt->k, kt->kt,
                                  sh.kf, quad, kc, 1.0f, p.l2norm);
         else if (w < 2 * kStage)
-            stage_quad<KT, false>(load_quad<VEC>(qh, p.qs, sp, c0, quad, kc, p.Dk), q, kt->q == q ? nullptr : kt->q, nullptr,
+            stage_quad<KT, false>(load_quad<VEC>(qr, sp, c0, quad, kc, p.Dk), q, kt->q == q ? nullptr : kt->q, nullptr,
                                   sh.qf, quad, kc, p.scale, p.l2norm);
     }
 
     // Reads one word of each 128-byte line that the chunk's rows will be read from: the lines wait in L2 and the
     // registers stay free.  The caller keeps the word until the reads have had their time.
-    __device__ __forceinline__ uint32_t touch(int64_t c0, const uint16_t *vh, int32_t v0) {
+    __device__ __forceinline__ uint32_t touch(int32_t c0, const Rows &vr, int32_t v0) {
         uint32_t word = 0;
         if constexpr (VEC) {
-            const int lane = fresh(lane0), i = 64 * (w & 1) + lane, r = i >> 1;
-            const int64_t left = sp.n - c0 < kC ? sp.n - c0 : kC;
-            const GdrTensor &ts = w < 2 ? p.ks : w < 4 ? p.qs : p.vs;
-            const uint16_t *base = (w < 2 ? kh : w < 4 ? qh : vh) + (sp.t0 + c0) * ts.st;
-            const int32_t first = w < 4 ? 0 : v0, end = w < 4 ? p.Dk : p.Dv, c = first + 64 * (i & 1);
-            if (w < 6 && c < end) word = buf_ld16(make_rsrc(base, left * ts.st * 2), uint32_t(r * ts.st + c * ts.sd) * 2);
+            const int lane = fresh(lane0), i = 64 * (w & 1) + lane;
+            const Rows &r = w < 2 ? kr : w < 4 ? qr : vr;
+            const int32_t end = w < 4 ? p.Dk : p.Dv, c = (w < 4 ? 0 : v0) + 64 * (i & 1);
+            if (w < 6 && c < end) word = buf_ld16(chunk_rsrc(r, sp, c0), uint32_t(i >> 1) * r.row + uint32_t(c) * 2);
         }
         return word;
     }
@@ -339,12 +348,12 @@ struct Prepare {
 
     // Gates of a chunk, one token a lane.  The running sum is in fp64 and kept in two fp32 parts: a difference of two of
     // its values keeps every bit of a small decay behind a large one.  Every e^ below is of a difference <= 0.
-    __device__ __forceinline__ void gates(int64_t c0) {
+    __device__ __forceinline__ void gates(int32_t c0) {
         const int lane = fresh(lane0);
-        const int64_t t = c0 + lane;
+        const int32_t t = c0 + lane;
         Gates gt = {0.0f, 0.0f};
         if (t < sp.n)
-            gt = gdr_gates(p, (sp.t0 + t) * p.gs.st + h * p.gs.sh, (sp.t0 + t) * p.bs.st + h * p.bs.sh, h);
+            gt = gdr_gates(p, int64_t(sp.t0 + t) * p.gs.st + h * p.gs.sh, int64_t(sp.t0 + t) * p.bs.st + h * p.bs.sh, h);
         double G = (gt.g < -1e4f ? -1e4 : double(gt.g)) * 1.4426950408889634;   // e^-10000 is 0, as of anything below
         G = dpp_add64<0x111, 0xf>(G);                  // row_shr 1, 2, 4, 8, then the rows' last values
         G = dpp_add64<0x112, 0xf>(G);
@@ -547,17 +556,16 @@ __device__ __forceinline__ void await(int *ready, int count) {
 template <int KT, bool VEC>
 struct Consumer {
     const GdrParams &p;
-    const Span64 sp;
+    const Span32 sp;
     const int lane0;
-    const uint16_t *vh;                // the head's first channel of v, row 0 of the sequence
-    uint16_t *oh;
+    const Rows vr, out;
     int32_t c0;                        // the wave's first channel; lane l has c0 + l % 16
     f32x4 S[2 * KT];                   // the state times 2^un
     int un;
 
     // The state's rows in memory: this lane has channels 8 g + 4 t .. of each 32 of its value channel's row.
     template <class F>
-    __device__ __forceinline__ void rows_of(float *rows, F f) {
+    __device__ __forceinline__ void state_rows(float *rows, F f) {
         const int lane = fresh(lane0), g = lane >> 4;
         const int32_t c = c0 + (lane & 15);
         float *row = rows + c * p.s_sv;
@@ -572,7 +580,7 @@ struct Consumer {
     __device__ __forceinline__ void load(float *rows, bool svec) {
         zero();
         float m = 0.0f;
-        rows_of(rows, [&](int d, const float *row, int k, bool ok) {
+        state_rows(rows, [&](int d, const float *row, int k, bool ok) {
             if (svec) {
                 if (ok && k < p.Dk) S[d] = *reinterpret_cast<const f32x4 *>(row + k);
             } else {
@@ -590,7 +598,7 @@ struct Consumer {
     }
     __device__ __forceinline__ void save(float *rows, bool svec) {
         const float inv = pow2(-un);
-        rows_of(rows, [&](int d, float *row, int k, bool ok) {
+        state_rows(rows, [&](int d, float *row, int k, bool ok) {
             const f32x4 s = S[d] * inv;
             if (svec) {
                 if (ok && k < p.Dk) *reinterpret_cast<f32x4 *>(row + k) = s;
@@ -602,31 +610,24 @@ struct Consumer {
         });
     }
 
-    // Rows of v and out, channels 8 or 4 at a time.  VEC: through a descriptor over the chunk's rows, each longer than the
-    // head's channels, so what does not exist lies past its end.
-    __device__ __forceinline__ Rsrc rows(const uint16_t *base, int64_t t0, const GdrTensor &ts) const {
-        const int64_t left = sp.n - t0 < kC ? sp.n - t0 : kC;
-        return make_rsrc(base + t0 * ts.st, left * ts.st * 2);
-    }
-
     // The chunk's values as left operands: tile mt has token tok_of(mt, n) in row n, the wave's 16 channels in its first
     // columns.  Times the identity they become results, a channel a lane, like everything they meet (with bf16 values
     // nothing is rounded; it takes 4 loads where that layout would take 16).
-    __device__ __forceinline__ void fetch(int64_t t0, u32x4 (&v)[4]) {
+    __device__ __forceinline__ void fetch(int32_t t0, u32x4 (&v)[4]) {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
         const int32_t c = c0 + 8 * g;
         if constexpr (VEC) {
-            const Rsrc rs = rows(vh, t0, p.vs);
-            const uint32_t row = uint32_t(p.vs.st) * 2;
+            const Rsrc rs = chunk_rsrc(vr, sp, t0);
+            const uint32_t row = vr.row;
             const uint32_t at = g < 2 && c < p.Dv ? uint32_t(tok_of(0, n)) * row + uint32_t(c) * 2 : kOob;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) v[mt] = buf_ld128<0>(rs, at + uint32_t(tok_of(mt, 0)) * row);
         } else {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const int64_t t = t0 + tok_of(mt, n);
+                const int32_t t = t0 + tok_of(mt, n);
                 const bool live = g < 2 && t < sp.n;
-                v[mt] = load8(vh + (live ? t : 0) * p.vs.st, p.vs.sd, c, p.Dv, live);
+                v[mt] = load8(vr.base + (live ? t : 0) * p.vs.st, p.vs.sd, c, p.Dv, live);
             }
         }
     }
@@ -642,12 +643,12 @@ struct Consumer {
     }
 
     // The output of tile mt comes as a transpose: token tok_of(mt, n) in the lane, channels 4 g .. in its registers.
-    __device__ __forceinline__ void store(int64_t t0, const f32x4 (&o)[4]) {
+    __device__ __forceinline__ void store(int32_t t0, const f32x4 (&o)[4]) {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
         const int32_t c = c0 + 4 * g;
         if constexpr (VEC) {
-            const Rsrc rs = rows(oh, t0, p.os);
-            const uint32_t row = uint32_t(p.os.st) * 2;
+            const Rsrc rs = chunk_rsrc(out, sp, t0);
+            const uint32_t row = out.row;
             const uint32_t at = c < p.Dv ? uint32_t(tok_of(0, n)) * row + uint32_t(c) * 2 : kOob;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
@@ -657,10 +658,11 @@ struct Consumer {
         } else {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const int64_t t = t0 + tok_of(mt, n);
+                const int32_t t = t0 + tok_of(mt, n);
+                uint16_t *row = const_cast<uint16_t *>(out.base) + t * p.os.st;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (t < sp.n && c + i < p.Dv) oh[t * p.os.st + (c + i) * p.os.sd] = to_bf16(o[mt][i]);
+                    if (t < sp.n && c + i < p.Dv) row[(c + i) * p.os.sd] = to_bf16(o[mt][i]);
             }
         }
     }
@@ -710,7 +712,7 @@ struct Consumer {
     static __device__ __forceinline__ f32x4 row4(const float *v, int t) { return *reinterpret_cast<const f32x4 *>(v + t); }
 
     // The state and the output through one chunk, in as few registers as go: four waves a SIMD hide what each waits for.
-    __device__ __forceinline__ void chunk(int64_t t0, const Tiles<KT> &b) {
+    __device__ __forceinline__ void chunk(int32_t t0, const Tiles<KT> &b) {
         const int lane = fresh(lane0), g = lane >> 4;
         f32x4 ak[4], aq[4];
 #pragma unroll
@@ -803,7 +805,7 @@ struct Consumer {
 
     // The state alone through one chunk, one wave a SIMD: what a product needs beside the last one's result is read and
     // computed before that result is there.  v comes in and goes out with the next chunk's.
-    __device__ __forceinline__ void advance(int64_t t0, const Tiles<KT> &b, u32x4 (&v)[4], Exchange<KT> *ex, int *ready) {
+    __device__ __forceinline__ void advance(int32_t t0, const Tiles<KT> &b, u32x4 (&v)[4], Exchange<KT> *ex, int *ready) {
         const int lane = fresh(lane0), g = lane >> 4;
         f16x8 sh[KT], sl[KT];
 #pragma unroll
@@ -812,7 +814,6 @@ struct Consumer {
             ex->s[kt * 64 + lane] = sh[kt];
         }
         if (lane < 16) ex->oinv[lane] = pow2(-un);
-        hand_over(ready);
         // K S
         f32x4 ak[4];
 #pragma unroll
@@ -825,7 +826,8 @@ struct Consumer {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(k[mt], sl[kt], ak[mt]);
         }
-        const float unit = pow2(un), ms = largest();
+        hand_over(ready);
+        const float unit = pow2(un);
         f32x4 ka[4], xv[4];
         const bf16x8 id = identity(lane);
 #pragma unroll
@@ -865,7 +867,7 @@ struct Consumer {
             for (int mt = 2 * tt; mt < 4; ++mt) z[mt] = mfma(tl[tri_tile(mt, tt)], xh, z[mt]);
         }
         fetch(t0 + kC, v);                             // (rows behind the end read as zero)
-        const float last = b.last;
+        const float last = b.last, ms = largest();
         f32x4 eg[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) eg[mt] = row4(b.eg, tok_of(mt, 4 * g));
@@ -901,7 +903,7 @@ struct Consumer {
 
     // The output of one chunk from what the state wave hands over; `done` halves came before.  All but z's own product
     // is ready when z comes.
-    __device__ __forceinline__ void emit(int64_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
+    __device__ __forceinline__ void emit(int32_t t0, const Tiles<KT> &b, const Exchange<KT> *ex, int *ready, int done) {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
         f32x4 aq[4];
         f16x8 q[4], pt[kTriTiles];
@@ -958,12 +960,12 @@ __device__ __forceinline__ Place place_of(const GdrParams &p, int32_t groups) {
 }
 
 // Sequence b's rows and line; false when nothing is to be done for it.
-__device__ __forceinline__ bool sequence(const GdrParams &p, int32_t b, Span64 &sp, int64_t &line) {
+__device__ __forceinline__ bool sequence(const GdrParams &p, int32_t b, Span32 &sp, int64_t &line) {
     int64_t a = p.qsl[b], e = p.qsl[b + 1];
     a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
     e = e < a ? a : (e > p.total_T ? p.total_T : e);
-    sp.t0 = a;
-    sp.n = e - a;
+    sp.t0 = int32_t(a);
+    sp.n = int32_t(e - a);
     if (sp.n == 0) return false;
     line = b;
     if (p.ci) {
@@ -981,11 +983,11 @@ constexpr int kMaxRanked = 64 * kWaves;
 __device__ __forceinline__ int32_t ranked(const GdrParams &p, int32_t r, int32_t *len, int32_t *out) {
     if (p.batch > kMaxRanked) return r;
     const int t = threadIdx.x;
-    Span64 sp;
+    Span32 sp;
     int64_t line;
     int32_t n = 0;
     if (t < p.batch) {
-        n = sequence(p, t, sp, line) ? int32_t(sp.n) : 0;
+        n = sequence(p, t, sp, line) ? sp.n : 0;
         len[t] = n;
     }
     __syncthreads();
@@ -999,11 +1001,9 @@ __device__ __forceinline__ int32_t ranked(const GdrParams &p, int32_t r, int32_t
 }
 
 template <int KT, bool VEC>
-__device__ __forceinline__ Consumer<KT, VEC> consumer(const GdrParams &p, const Span64 &sp, int lane, int32_t h, int32_t tile) {
-    Consumer<KT, VEC> st{p, sp, lane};
+__device__ __forceinline__ Consumer<KT, VEC> consumer(const GdrParams &p, const Span32 &sp, int lane, int32_t h, int32_t tile) {
+    Consumer<KT, VEC> st{p, sp, lane, rows_of(p.v, p.vs, sp.t0, h), rows_of(p.out, p.os, sp.t0, h)};
     st.c0 = tile * 16;
-    st.vh = p.v + sp.t0 * p.vs.st + h * p.vs.sh;
-    st.oh = p.out + sp.t0 * p.os.st + h * p.os.sh;
     return st;
 }
 
@@ -1015,14 +1015,15 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     if (!pl.ok) return;
     pl.b = __builtin_amdgcn_readfirstlane(
         ranked(p, pl.b, reinterpret_cast<int32_t *>(sh.diag), reinterpret_cast<int32_t *>(sh.diag) + kMaxRanked));
-    Span64 sp;
+    Span32 sp;
     int64_t line;
     if (!sequence(p, pl.b, sp, line)) return;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t nc = (sp.n + kC - 1) / kC;
+    const int32_t nc = int32_t((int64_t(sp.n) + kC - 1) / kC);
     const int hk = pl.h / p.group;
-    Prepare<KT, VEC> pr{p, sh, tiles.k, tiles.q, &tiles, &tiles, sp, lane, wave, pl.h, p.q + hk * p.qs.sh, p.k + hk * p.ks.sh};
+    Prepare<KT, VEC> pr{p, sh, tiles.k, tiles.q, &tiles, &tiles, sp, lane, wave, pl.h, rows_of(p.q, p.qs, sp.t0, hk),
+                        rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(0);
 
     const int32_t tile = pl.cg * kWaves + wave;
@@ -1032,12 +1033,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
     else st.zero();
 
-    for (int64_t c = 0; c < nc; ++c) {
+    for (int32_t c = 0; c < nc; ++c) {
         const bool more = c + 1 < nc;
         pr.stage(c * kC);
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
         uint32_t word = 0;
-        if (more) word = pr.touch((c + 1) * kC, st.vh - sp.t0 * p.vs.st, pl.cg * kWaves * 16);
+        if (more) word = pr.touch((c + 1) * kC, st.vr, pl.cg * kWaves * 16);
         if (work) st.chunk(c * kC, tiles);
         asm volatile("" : : "v"(word));
         __syncthreads();
@@ -1070,16 +1071,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
         const int32_t mid = (lo + hi + 1) >> 1;
         if (first_slot(p, mid) <= slot) lo = mid; else hi = mid - 1;
     }
-    Span64 sp;
+    Span32 sp;
     int64_t line;
     if (!sequence(p, lo, sp, line)) return;
-    const int64_t c = slot - first_slot(p, lo);
-    if (c < 0 || c * kC >= sp.n) return;
+    const int64_t chunk = slot - first_slot(p, lo);
+    if (chunk < 0 || chunk * kC >= sp.n) return;
+    const int32_t c = int32_t(chunk);
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     HeadTiles *ht = heads + slot * p.Hv + hk * p.group;
-    Prepare<KT, VEC> pr{p, sh, k, q, keys + slot * p.Hk + hk, ht, sp, lane, wave, hk * p.group, p.q + hk * p.qs.sh,
-                        p.k + hk * p.ks.sh};
+    Prepare<KT, VEC> pr{p, sh, k, q, keys + slot * p.Hk + hk, ht, sp, lane, wave, hk * p.group, rows_of(p.q, p.qs, sp.t0, hk),
+                        rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(c * kC);
     pr.stage(c * kC);
     for (int32_t x = 0; x < p.group; ++x) {
@@ -1094,13 +1096,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
     }
 }
 
-constexpr int kWalkers = 4;            // state waves of a walking workgroup
+constexpr int kWalkers = 2;            // state waves of a walking workgroup
 constexpr int kLoaders = 4;
 
 // Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers,
 // four take the state of 16 channels each through the present one, four compute those channels' output beside them.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
+__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLoaders) / 4) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
                                                                                  const HeadTiles *heads, int32_t groups,
                                                                                  bool svec) {
     __shared__ Tiles<KT> buf[2];
@@ -1108,11 +1110,12 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
     __shared__ int ready[kWalkers];
     const Place pl = place_of(p, groups);
     if (!pl.ok) return;
-    Span64 sp;
+    Span32 sp;
     int64_t line;
     if (!sequence(p, pl.b, sp, line)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t nc = (sp.n + kC - 1) / kC, slot = first_slot(p, pl.b);
+    const int32_t nc = int32_t((int64_t(sp.n) + kC - 1) / kC);
+    const int64_t slot = first_slot(p, pl.b);
     if (threadIdx.x < kWalkers) ready[threadIdx.x] = 0;
 
     if (wave >= 2 * kWalkers) {
@@ -1121,7 +1124,7 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
         constexpr int kKeyPer = (kKey + kN - 1) / kN, kHeadPer = (kHead + kN - 1) / kN;
         const int t = (wave - 2 * kWalkers) * 64 + lane;
         u32x4 rk[kKeyPer], rh[kHeadPer];
-        const auto load = [&](int64_t c) {
+        const auto load = [&](int32_t c) {
             const u32x4 *k = reinterpret_cast<const u32x4 *>(keys + (slot + c) * p.Hk + pl.h / p.group);
             const u32x4 *h = reinterpret_cast<const u32x4 *>(heads + (slot + c) * p.Hv + pl.h);
 #pragma unroll
@@ -1139,26 +1142,13 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
             for (int i = 0; i < kHeadPer; ++i)
                 if (t + i * kN < kHead) h[t + i * kN] = rh[i];
         };
-        // the values are read a chunk ahead by the state waves, from memory some 2000 cycles away: one word of each row's
-        // 128 bytes brings them to L2 before
-        const auto touch = [&](int64_t c) {
-            uint32_t word = 0;
-            if constexpr (VEC) {
-                const int32_t ch = pl.cg * 16 * kWalkers;
-                if (t < kC && c * kC + t < sp.n && ch < p.Dv)
-                    word = p.v[(sp.t0 + c * kC + t) * p.vs.st + pl.h * p.vs.sh + ch];
-            }
-            return word;
-        };
         load(0);
         put(buf[0]);
         load(nc > 1 ? 1 : 0);
         __syncthreads();
-        for (int64_t c = 0; c < nc; ++c) {
+        for (int32_t c = 0; c < nc; ++c) {
             put(buf[(c + 1) & 1]);
-            const uint32_t word = touch(c + 2);
             load(c + 2 < nc ? c + 2 : nc - 1);
-            asm volatile("" : : "v"(word));
             __syncthreads();
         }
         return;
@@ -1170,8 +1160,8 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
     const bool work = tile * 16 < p.Dv;
     if (wave >= kWalkers) {
         __syncthreads();
-        for (int64_t c = 0; c < nc; ++c) {
-            if (work) st.emit(c * kC, buf[c & 1], &exchange[unit], &ready[unit], int(2 * c));
+        for (int32_t c = 0; c < nc; ++c) {
+            if (work) st.emit(c * kC, buf[c & 1], &exchange[unit], &ready[unit], 2 * c);
             __syncthreads();
         }
         return;
@@ -1182,7 +1172,7 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), 3) void gdr_walk_ke
     u32x4 v[4];
     st.fetch(0, v);
     __syncthreads();
-    for (int64_t c = 0; c < nc; ++c) {
+    for (int32_t c = 0; c < nc; ++c) {
         if (work) st.advance(c * kC, buf[c & 1], v, &exchange[unit], &ready[unit]);
         __syncthreads();
     }
