@@ -335,14 +335,14 @@ struct Prepare {
     template <class F>
     __device__ __forceinline__ void tiles(F ahead) {
         __syncthreads();
-        if (w < 4) key_products();
-        else query_products();
+        key_products();
         if (w == 7) factors();
         __syncthreads();
         if (w == 0) invert_diagonal();
-        if (w == 7) ahead();
+        else if (w < 7) query_products();              // (the inverse waits for one wave)
         __syncthreads();
         if (w < 4) invert_rest();
+        else if (w == 7) ahead();
         __syncthreads();
     }
 
@@ -397,7 +397,7 @@ struct Prepare {
         return r;
     }
 
-    // K K^T and Q K^T: 12 tile pairs meet the lower triangle, three a wave.  K K^T has its rows in the registers, Q K^T
+    // K K^T and Q K^T: 12 tile pairs meet the lower triangle, one or two a wave.  K K^T has its rows in the registers, Q K^T
     // (as its transpose) its columns: what a lane holds is then one piece of the operand that it becomes.
     static __device__ __forceinline__ void pair(int pr, int &mt, int &nt) {
         mt = pr < 4 ? pr >> 1 : 2 + ((pr - 4) >> 2);
@@ -405,25 +405,16 @@ struct Prepare {
     }
     __device__ __forceinline__ void key_products() {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
-        f32x4 kk[3];
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
+        for (int pr = w; pr < 12; pr += 8) {
             int mt, nt;
-            pair(3 * w + x, mt, nt);
-            kk[x] = f32x4{0, 0, 0, 0};
+            pair(pr, mt, nt);
+            f32x4 kk = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < KT; ++i)
-                kk[x] = mfma(row_tile_of(k, mt * KT + i, i, lane), row_tile_of(k, nt * KT + i, i, lane), kk[x]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            int mt, nt;
-            pair(3 * w + x, mt, nt);
+            for (int i = 0; i < KT; ++i) kk = mfma(row_tile_of(k, mt * KT + i, i, lane), row_tile_of(k, nt * KT + i, i, lane), kk);
             const int tj = tok_of(nt, n), ti = tok_of(mt, 4 * g);
             const int bi = ti >> 4, bj = tj >> 4;
             const f32x4 kf = *reinterpret_cast<const f32x4 *>(sh.kf + ti);
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(sh.beta + ti) * kf * kf * decay<false>(ti, tj) * kk[x];
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(sh.beta + ti) * kf * kf * decay<false>(ti, tj) * kk;
             f16x4 hi, lo;
             split4(a, hi, lo);
             _Float16 *op = bi > bj ? sh.off + (bi * (bi - 1) / 2 + bj) * kTile + ((tj & 15) + 4 * (ti & 12)) * 8
@@ -433,23 +424,23 @@ struct Prepare {
                 *reinterpret_cast<f32x4 *>(bi == bj ? sh.diag + bi * 256 + (tj & 15) * 16 + (ti & 15) : sh.dump) = a;
         }
     }
+    // Waves 1 to 6.
     __device__ __forceinline__ void query_products() {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
-        f32x4 qk[3];
+        f32x4 qk[2];
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
+        for (int x = 0; x < 2; ++x) {
             int mt, nt;
-            pair(3 * (w - 4) + x, mt, nt);
+            pair(2 * (w - 1) + x, mt, nt);
             qk[x] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < KT; ++i)
                 qk[x] = mfma(row_tile_of(k, nt * KT + i, i, lane), row_tile_of(q, mt * KT + i, i, lane), qk[x]);
-            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
+        for (int x = 0; x < 2; ++x) {
             int mt, nt;
-            pair(3 * (w - 4) + x, mt, nt);
+            pair(2 * (w - 1) + x, mt, nt);
             const int ti = tok_of(mt, n), tj = tok_of(nt, 4 * g);
             const f32x4 d = decay<true>(tj, ti);
             float v[4];
@@ -631,12 +622,16 @@ struct Consumer {
             }
         }
     }
-    // The identity as a right operand.
-    static __device__ __forceinline__ bf16x8 identity(int lane) {
-        bf16x8 r;
+    // The identity as a right operand, times the column's unit (a power of two, within bf16's range).
+    __device__ __forceinline__ bf16x8 identity(int lane) const {
+        const uint32_t one = uint32_t(un + 127) << 7;
+        u32x4 r;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = 8 * (lane >> 4) + j == (lane & 15) ? __bf16(1.0f) : __bf16(0.0f);
-        return r;
+        for (int j = 0; j < 4; ++j) {
+            const int at = 8 * (lane >> 4) + 2 * j - (lane & 15);
+            r[j] = at == 0 ? one : at == -1 ? one << 16 : 0u;
+        }
+        return __builtin_bit_cast(bf16x8, r);
     }
     static __device__ __forceinline__ f32x4 values(const u32x4 &v, const bf16x8 &id) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), id, f32x4{0, 0, 0, 0}, 0, 0, 0);
@@ -717,7 +712,7 @@ struct Consumer {
         f32x4 ak[4], aq[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) { ak[mt] = f32x4{0, 0, 0, 0}; aq[mt] = f32x4{0, 0, 0, 0}; }
-        const float ms = largest(), oinv = pow2(-un), unit = pow2(un);
+        const float ms = largest(), oinv = pow2(-un);
         // K S and Q S, the state split on the way (its largest element is below 2^15)
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
@@ -743,7 +738,7 @@ struct Consumer {
             const f32x4 ka = row4(b.ka, tok_of(mt, 4 * g)), kb = row4(b.kb, tok_of(mt, 4 * g)), vv = values(v[mt], id);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * unit * vv[i]);
+                x[4 * mt + i] = fmaf(-ka[i], ak[mt][i], kb[i] * vv[i]);
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
@@ -827,13 +822,12 @@ struct Consumer {
             for (int mt = 0; mt < 4; ++mt) ak[mt] = mfma(k[mt], sl[kt], ak[mt]);
         }
         hand_over(ready);
-        const float unit = pow2(un);
         f32x4 ka[4], xv[4];
         const bf16x8 id = identity(lane);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             ka[mt] = row4(b.ka, tok_of(mt, 4 * g));
-            xv[mt] = row4(b.kb, tok_of(mt, 4 * g)) * unit * values(v[mt], id);
+            xv[mt] = row4(b.kb, tok_of(mt, 4 * g)) * values(v[mt], id);
         }
         f16x8 th[kTriTiles], tl[kTriTiles];
 #pragma unroll
