@@ -193,7 +193,7 @@ int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num
     if (batch < 1 || total_tokens < 1 || num_k_heads < 1 || num_v_heads < 1 || head_dim_k < 1 || head_dim_v < 1 ||
         head_dim_k > kGdrMaxChunkK)
         return 0;
-    if (vector_layout && !gdr_few_heads(batch, num_v_heads, head_dim_v)) return 0;
+    if (vector_layout && !gdr_few_heads(total_tokens, batch, num_v_heads, head_dim_v)) return 0;
     const int64_t slots = gdr_slots(total_tokens, batch);
     if (slots * num_k_heads >= (int64_t(1) << 31)) return 0;
     return gdr_workspace_bytes(total_tokens, batch, num_k_heads, num_v_heads, head_dim_k);

@@ -197,39 +197,48 @@ __global__ __launch_bounds__(kVfBlock) void verify_pick_kernel(VerifyParams p) {
                     }
             }
         }
-        double round[kRounds], all = 0.0;
+        // sums of the rounds (all at once), then of the waves before
+        double round[kRounds], total[kRounds], all = 0.0;
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             round[r] = 0.0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) round[r] += left_of(d, w0 + 256 * r + 4 * lane + e, x[r][e], y[r][e]);
-            all += round[r];
+            total[r] = round[r];
         }
-        all = wave_sum(all);
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1)
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) total[r] += __shfl_xor(total[r], m);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) all += total[r];
         if (lane == 0) part[w] = all;
         __syncthreads();
         double c = before;
         for (int i = 0; i < w; ++i) c += part[i];
+        // the first round that passes the goal, entry by entry; of the others only the last entry with mass counts
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
-            if (hit != INT32_MAX) break;
-            const double end = wave_scan(round[r]);
-            double run = c + (end - round[r]);
-            int32_t h = INT32_MAX, l = -1;
+            if (hit == INT32_MAX && total[r] > 0.0) {
+                const bool over = c + total[r] > goal;
+                double run = over ? c + (wave_scan(round[r]) - round[r]) : 0.0;
+                int32_t h = INT32_MAX, l = -1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int32_t i = w0 + 256 * r + 4 * lane + e;
-                const double m = left_of(d, i, x[r][e], y[r][e]);
-                run += m;
-                if (m > 0.0) {
-                    l = i;
-                    if (h == INT32_MAX && run > goal) h = i;
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t i = w0 + 256 * r + 4 * lane + e;
+                    const double m = left_of(d, i, x[r][e], y[r][e]);
+                    run += m;
+                    if (m > 0.0) {
+                        l = i;
+                        if (over && h == INT32_MAX && run > goal) h = i;
+                    }
                 }
+                const uint64_t hs = __ballot(h != INT32_MAX), ls = __ballot(l >= 0);
+                top = __shfl(l, 63 - __builtin_clzll(ls));
+                if (hs) hit = __shfl(h, __builtin_ctzll(hs));
+                else if (over) hit = top;              // (the same sum in another order fell short by its last bit)
+                c += total[r];
             }
-            const uint64_t hs = __ballot(h != INT32_MAX), ls = __ballot(l >= 0);
-            if (hs) hit = __shfl(h, __builtin_ctzll(hs));
-            if (ls) top = __shfl(l, 63 - __builtin_clzll(ls));
-            c += __shfl(end, 63);
         }
         if (lane == 0) { found[w] = hit; last[w] = top; }
         __syncthreads();

@@ -29,13 +29,14 @@ def fwd(lib, **kw):
 
 
 def test_fwd_workspace(lib):
-    need = lib.gdr_fwd_workspace_bytes(2, 10, 4, 8, 64, 64, 1)
+    need = lib.gdr_fwd_workspace_bytes(2, 1000, 4, 8, 64, 64, 1)
     assert need > 0
-    assert fwd(lib, ws=addr(11), wb=need) == ELAUNCH
-    assert fwd(lib, ws=addr(11), wb=need - 1) == ESHAPE
-    assert fwd(lib, ws=ctypes.c_void_p(BASE + 11 * GB + 8), wb=need) == EALIGN
+    assert fwd(lib, T=1000, ws=addr(11), wb=need) == ELAUNCH
+    assert fwd(lib, T=1000, ws=addr(11), wb=need - 1) == ESHAPE
+    assert fwd(lib, T=1000, ws=ctypes.c_void_p(BASE + 11 * GB + 8), wb=need) == EALIGN
     for x in (1, 2, 3, 4, 5, 6, 10):
-        assert fwd(lib, ws=addr(x), wb=need) == EALIAS, x
+        assert fwd(lib, T=1000, ws=addr(x), wb=need) == EALIAS, x
+    assert lib.gdr_fwd_workspace_bytes(2, 256, 4, 8, 64, 64, 1) == 0            # short sequences: one kernel
     assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 1) == 0          # many heads: one kernel
     assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 0) > 0
     for bad in ((0, 10, 4, 8, 64, 64, 1), (2, 0, 4, 8, 64, 64, 1), (2, 10, 0, 8, 64, 64, 1), (2, 10, 4, 8, 129, 64, 1),
