@@ -545,46 +545,65 @@ def sconv_paged_fused_multi(xs, weights, cache, positions, slot_mapping, query_s
 
 
 # ------------------------------------------------------- gated delta rule --
+#
+# These calls take many tensors, and small ones are over in a few
+# microseconds: what is checked is checked with few Python calls.
 
-def _ptr(t, dtype, name, dev):
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _ptr(t, dtype, name, dev, index):
     """Address of a checked tensor (None passes); the failing checks are _dev's."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != dev or not t.is_cuda:
+    if t.dtype is not dtype or index < 0 or t.get_device() != index:
         _dev(t, dtype, name, dev)
     return t.data_ptr()
 
 
-def _gdr_gates(g, beta, A_log, dt_bias, lead, hv, dev):
-    """The two gate tensors and the layer's parameters, checked and marshalled."""
-    want = (*lead, hv)
-    if g.shape != want or beta.shape != want:
-        raise ValueError("g and beta need one value per token and value head")
-    f32 = torch.float32
-    if A_log is None and dt_bias is None:
-        return (_ptr(g, f32, "g", dev), *g.stride(), _ptr(beta, f32, "beta", dev), *beta.stride(), None, None)
-    if A_log is None or dt_bias is None:
-        raise ValueError("A_log and dt_bias go together")
-    for t in (A_log, dt_bias):
-        if t.shape != (hv,) or (hv > 1 and t.stride(0) != 1):
-            raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
-    bf = torch.bfloat16
-    return (_ptr(g, bf, "g", dev), *g.stride(), _ptr(beta, bf, "beta", dev), *beta.stride(),
-            _ptr(A_log, f32, "A_log", dev), _ptr(dt_bias, f32, "dt_bias", dev))
+def _vec(t, dtype, name, dev, index, n):
+    """Address of a checked contiguous 1-D tensor of at least n entries."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or index < 0 or t.get_device() != index or t.dim() != 1 or t.numel() < n or not t.is_contiguous():
+        _index(t, dtype, name, dev, n)
+    return t.data_ptr()
 
 
-def _gdr_shapes(q, k, v, state, out):
-    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
+def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index):
+    """Shapes (num_k_heads, num_v_heads, head_dim_k, head_dim_v) and the marshalled inputs, state and output of a call
+    whose tensors have one and the same leading dimensions."""
+    qs, vs = q.shape, v.shape
+    if k.shape != qs or vs[:-2] != qs[:-2]:
         raise ValueError("q and k need one shape, and v the same tokens")
-    hk, dk = q.shape[-2:]
-    hv, dv = v.shape[-2:]
+    hk, dk = qs[-2:]
+    hv, dv = vs[-2:]
     if hk < 1 or hv % hk:
         raise ValueError("v's heads must be a multiple of q's")
-    if state is not None and (state.dim() != 4 or state.shape[1:] != (hv, dv, dk)):
-        raise ValueError("state must be (lines, num_v_heads, head_dim_v, head_dim_k)")
-    if out.shape != v.shape:
+    if g.shape != vs[:-1] or beta.shape != vs[:-1]:
+        raise ValueError("g and beta need one value per token and value head")
+    if out.shape != vs:
         raise ValueError("out must have v's shape")
-    return hk, hv, dk, dv
+    gate = _F32
+    if A_log is not None or dt_bias is not None:
+        if A_log is None or dt_bias is None:
+            raise ValueError("A_log and dt_bias go together")
+        gate = _BF16
+        for t in (A_log, dt_bias):
+            if t.dim() != 1 or t.numel() != hv or not t.is_contiguous():
+                raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
+    if state is None:
+        st = (None, 0, 0, 0, 0, 0)
+    else:
+        ss = state.shape
+        if len(ss) != 4 or ss[1] != hv or ss[2] != dv or ss[3] != dk:
+            raise ValueError("state must be (lines, num_v_heads, head_dim_v, head_dim_k)")
+        st = (_ptr(state, _F32, "state", dev, index), *state.stride(), ss[0])
+    ins = (_ptr(q, _BF16, "q", dev, index), *q.stride(), _ptr(k, _BF16, "k", dev, index), *k.stride(),
+           _ptr(v, _BF16, "v", dev, index), *v.stride(),
+           _ptr(g, gate, "g", dev, index), *g.stride(), _ptr(beta, gate, "beta", dev, index), *beta.stride(),
+           _ptr(A_log, _F32, "A_log", dev, index), _ptr(dt_bias, _F32, "dt_bias", dev, index), *st)
+    return (hk, hv, dk, dv), ins, (_ptr(out, _BF16, "out", dev, index), *out.stride())
 
 
 def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
@@ -604,34 +623,30 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     scale defaults to head_dim_k ** -0.5.  Returns out (T, num_v_heads,
     head_dim_v); rows of padded sequences are left as they are."""
     dev = q.device
+    index = q.get_device()
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be (T, heads, head_dim)")
     if out is None:
         out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    hk, hv, dk, dv = _gdr_shapes(q, k, v, state, out)
+    (hk, hv, dk, dv), ins, (o, o_tok, o_head, o_dim) = _gdr_tensors(
+        q, k, v, g, beta, A_log, dt_bias, state, out, dev, index)
     total = q.shape[0]
     batch = query_start_loc.numel() - 1
-    bf = torch.bfloat16
-    args = (
-        _ptr(q, bf, "q", dev), *q.stride(), _ptr(k, bf, "k", dev), *k.stride(),
-        _ptr(v, bf, "v", dev), *v.stride(),
-        *_gdr_gates(g, beta, A_log, dt_bias, (total,), hv, dev),
-        _ptr(state, torch.float32, "state", dev),
-        *(state.stride() if state is not None else (0, 0, 0, 0)),
-        state.shape[0] if state is not None else 0,
-        _index(cache_indices, torch.int32, "cache_indices", dev, batch),
-        _index(has_initial_state, torch.bool, "has_initial_state", dev, batch),
-        _index(query_start_loc, torch.int32, "query_start_loc", dev),
-        batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
-        1 if use_qk_l2norm else 0, pad_slot_id, _ptr(out, bf, "out", dev), *out.stride(),
-    )
-    vector = dk % 8 == 0 and dv % 8 == 0 and all(
-        t.stride(2) == 1 and t.stride(0) >= t.shape[2] and t.stride(0) % n == 0 and t.stride(1) % n == 0 and
-        t.data_ptr() % (2 * n) == 0 for t, n in ((q, 8), (k, 8), (v, 8), (out, 4)))
-    need = load_library().gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
+    qa, q_tok, q_head, q_dim, ka, k_tok, k_head, k_dim, va, v_tok, v_head, v_dim = ins[:12]
+    vector = (q_dim == k_dim == v_dim == o_dim == 1 and not (
+        (dk | dv | q_tok | q_head | k_tok | k_head | v_tok | v_head) & 7 or (o_tok | o_head) & 3 or
+        (qa | ka | va) & 15 or o & 7) and q_tok >= dk and k_tok >= dk and v_tok >= dv and o_tok >= dv)
+    lib = load_library()
+    need = lib.gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
+    # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    args += (ws.data_ptr() if need else None, need)
-    _launch("gdr_fwd_varlen", dev, args)
+    _launch("gdr_fwd_varlen", dev, (
+        *ins, _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
+        _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),
+        _vec(query_start_loc, _I32, "query_start_loc", dev, index, 1),
+        batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
+        1 if use_qk_l2norm else 0, pad_slot_id, o, o_tok, o_head, o_dim,
+        ws.data_ptr() if need else None, need))
     return out
 
 
@@ -649,11 +664,11 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
     of the line that was read; the lines of one call are the next call's
     cache_indices.  Returns out, shaped like v."""
     dev = q.device
-    single = q.dim() == 3
+    index = q.get_device()
     if out is None:
         out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     ov = out
-    if single:
+    if q.dim() == 3:
         if v.dim() != 3 or g.dim() != 2 or beta.dim() != 2 or out.dim() != 3:
             raise ValueError("q, k, v, g, beta and out must all be without a token dimension, or none")
         q, k, v, g, beta, ov = (t.unsqueeze(1) for t in (q, k, v, g, beta, out))
@@ -661,34 +676,29 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
         raise ValueError("q, k and v must be (batch, [seqlen,] heads, head_dim)")
     if state is None:
         raise ValueError("state is required")
-    hk, hv, dk, dv = _gdr_shapes(q, k, v, state, ov)
     batch, seqlen = q.shape[:2]
-    ci, ci_st, steps = cache_indices, (0, 0), 1
+    ci, ci_seq, ci_step, steps = cache_indices, 0, 0, 1
     if ci is not None:
-        if ci.dim() not in (1, 2) or ci.shape[0] < batch:
+        d = ci.dim()
+        if d not in (1, 2) or ci.shape[0] < batch:
             raise ValueError("cache_indices must be (batch,) or (batch, steps)")
-        if ci.dim() == 2:
-            ci_st, steps = ci.stride(), ci.shape[1]
-        else:
-            ci_st = (ci.stride(0), 0)
+        ci_seq = ci.stride(0)
+        if d == 2:
+            ci_step, steps = ci.stride(1), ci.shape[1]
     if num_accepted_tokens is not None and (ci is None or ci.dim() != 2):
         raise ValueError("num_accepted_tokens needs cache_indices of (batch, steps)")
-    osi = output_state_indices
-    if osi is not None and (osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen):
-        raise ValueError("output_state_indices must be (batch, >= seqlen)")
-    bf, i32 = torch.bfloat16, torch.int32
-    args = (
-        _ptr(q, bf, "q", dev), *q.stride(), _ptr(k, bf, "k", dev), *k.stride(),
-        _ptr(v, bf, "v", dev), *v.stride(),
-        *_gdr_gates(g, beta, A_log, dt_bias, (batch, seqlen), hv, dev),
-        _ptr(state, torch.float32, "state", dev), *state.stride(), state.shape[0],
-        _ptr(ci, i32, "cache_indices", dev), *ci_st, steps,
-        _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
-        _ptr(osi, i32, "output_state_indices", dev), *(osi.stride() if osi is not None else (0, 0)),
+    osi, osi_seq, osi_step = output_state_indices, 0, 0
+    if osi is not None:
+        if osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen:
+            raise ValueError("output_state_indices must be (batch, >= seqlen)")
+        osi_seq, osi_step = osi.stride()
+    (hk, hv, dk, dv), ins, outs = _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, ov, dev, index)
+    _launch("gdr_update", dev, (
+        *ins, _ptr(ci, _I32, "cache_indices", dev, index), ci_seq, ci_step, steps,
+        _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch),
+        _ptr(osi, _I32, "output_state_indices", dev, index), osi_seq, osi_step,
         batch, seqlen, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
-        1 if use_qk_l2norm else 0, pad_slot_id, _ptr(ov, bf, "out", dev), *ov.stride(),
-    )
-    _launch("gdr_update", dev, args)
+        1 if use_qk_l2norm else 0, pad_slot_id, *outs))
     return out
 
 
@@ -708,39 +718,41 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
     (batch, max_drafts + 1) with the standing drafts, the drawn token, then -1;
     int32 (batch,) with standing drafts + 1, as conv1d_update and gdr_update
     take it."""
-    dev = target_probs.device
+    p, q = target_probs, draft_probs
+    dev, index = p.device, p.get_device()
     batch = draft_start_loc.numel() - 1
     nd = draft_tokens.numel()
-    if target_probs.dim() != 2 or target_probs.shape[0] < nd + batch:
+    if p.dim() != 2 or p.shape[0] < nd + batch:
         raise ValueError("target_probs must be (num_drafts + batch, vocab)")
-    vocab = target_probs.shape[1]
-    if draft_probs is not None and (draft_probs.dim() != 2 or draft_probs.shape[0] < nd or
-                                    draft_probs.shape[1] != vocab):
-        raise ValueError("draft_probs must be (num_drafts, vocab)")
-    for name, t in (("target_probs", target_probs), ("draft_probs", draft_probs)):
-        if t is not None and vocab > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have a unit vocabulary stride")
-    i32, f32 = torch.int32, torch.float32
+    vocab = p.shape[1]
+    if vocab > 1 and p.stride(1) != 1:
+        raise ValueError("target_probs must have a unit vocabulary stride")
+    q_row = 0
+    if q is not None:
+        if q.dim() != 2 or q.shape[0] < nd or q.shape[1] != vocab:
+            raise ValueError("draft_probs must be (num_drafts, vocab)")
+        if vocab > 1 and q.stride(1) != 1:
+            raise ValueError("draft_probs must have a unit vocabulary stride")
+        q_row = q.stride(0)
+        if nd == 0:
+            q = None
     if tokens is None:
-        tokens = torch.empty((max(batch, 0), max_drafts + 1), dtype=i32, device=dev)
-    if tokens.shape != (batch, max_drafts + 1) or tokens.stride(1) != 1:
+        tokens = torch.empty((max(batch, 0), max_drafts + 1), dtype=_I32, device=dev)
+    elif tokens.shape != (batch, max_drafts + 1) or tokens.stride(1) != 1:
         raise ValueError("tokens must be (batch, max_drafts + 1) with a unit inner stride")
     if num_accepted_tokens is None:
-        num_accepted_tokens = torch.empty((batch,), dtype=i32, device=dev)
+        num_accepted_tokens = torch.empty((batch,), dtype=_I32, device=dev)
     ws_bytes = load_library().sconv_verify_workspace_bytes(batch, vocab)
+    # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
     ws = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
-    args = (
-        _index(draft_tokens, i32, "draft_tokens", dev),
-        _index(draft_start_loc, i32, "draft_start_loc", dev),
-        _ptr(target_probs, f32, "target_probs", dev), target_probs.stride(0),
-        _ptr(draft_probs, f32, "draft_probs", dev),
-        draft_probs.stride(0) if draft_probs is not None else 0,
-        _index(accept_uniform, f32, "accept_uniform", dev, nd),
-        _index(sample_uniform, f32, "sample_uniform", dev, batch),
-        batch, nd, vocab, max_drafts,
-        _ptr(tokens, i32, "tokens", dev), tokens.stride(0),
-        _index(num_accepted_tokens, i32, "num_accepted_tokens", dev, batch),
-        ws.data_ptr(), ws_bytes,
-    )
-    _launch("sconv_verify_drafts", dev, args)
+    _launch("sconv_verify_drafts", dev, (
+        _vec(draft_tokens, _I32, "draft_tokens", dev, index, nd),
+        _vec(draft_start_loc, _I32, "draft_start_loc", dev, index, batch + 1),
+        _ptr(p, _F32, "target_probs", dev, index), p.stride(0),
+        _ptr(q, _F32, "draft_probs", dev, index), q_row,
+        _vec(accept_uniform, _F32, "accept_uniform", dev, index, nd),
+        _vec(sample_uniform, _F32, "sample_uniform", dev, index, batch),
+        batch, nd, vocab, max_drafts, _ptr(tokens, _I32, "tokens", dev, index), tokens.stride(0),
+        _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch), ws.data_ptr(),
+        ws_bytes))
     return tokens, num_accepted_tokens
