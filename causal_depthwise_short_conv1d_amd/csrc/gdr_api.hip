@@ -196,7 +196,7 @@ int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num
     if (vector_layout && !gdr_few_heads(total_tokens, batch, num_v_heads, head_dim_v)) return 0;
     const int64_t slots = gdr_slots(total_tokens, batch);
     if (slots * num_k_heads >= (int64_t(1) << 31)) return 0;
-    return gdr_workspace_bytes(total_tokens, batch, num_k_heads, num_v_heads, head_dim_k);
+    return gdr_workspace_bytes(total_tokens, batch, num_v_heads);
 }
 
 int gdr_update(const void *q, int64_t q_stride_seq, int64_t q_stride_tok, int64_t q_stride_head,

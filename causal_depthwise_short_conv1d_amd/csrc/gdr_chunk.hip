@@ -58,7 +58,6 @@ struct alignas(16) KeyTiles {          // of a chunk's keys and queries
     _Float16 k[4 * KT * kTile];        // [mt][kt] rows tokens
     _Float16 q[4 * KT * kTile];
     _Float16 kt[4 * KT * kTile];       // [2 KT channel tiles][2] rows key channels, columns tokens
-    float qf[kC];
 };
 struct alignas(16) HeadTiles {         // ... with a value head's gates
     _Float16 th[kTriTiles * kTile];    // T, high and low parts
@@ -67,6 +66,7 @@ struct alignas(16) HeadTiles {         // ... with a value head's gates
     float kb[kC];                      // kf beta
     float ka[kC];                      // kf beta e^G kf
     float eg[kC];                      // e^(G_last - G)
+    float qf[kC];
     float qe[kC];                      // qf e^G
     float last;                        // e^G_last
 };
@@ -217,10 +217,10 @@ __device__ __forceinline__ Quad load_quad(const Rows &r, const Span32 &sp, int32
 
 // Scales a row by a power of two (to a norm of 2^-0.5 .. 2^0.5), writes it as a row of the operand tiles (and, for
 // keys, transposed), and its factor: the power, times the norm's inverse and `scale`.
-// `copy`: the same rows again (in memory), or null.
-template <int KT, bool KEYS>
-__device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Float16 *copy, _Float16 *cols, float *factor,
-                                           int quad, int kc, float scale, bool l2norm) {
+// `cols` or `factor` may be null: not wanted.
+template <int KT>
+__device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Float16 *cols, float *factor, int quad, int kc,
+                                           float scale, bool l2norm) {
     f16x8 h[4];
     const int kt = kc >> 2, g = kc & 3;
 #pragma unroll
@@ -241,14 +241,13 @@ __device__ __forceinline__ void stage_quad(const Quad &in, _Float16 *rows, _Floa
         for (int j = 0; j < 8; ++j) f[j] *= s;
         h[i] = half8(f);
         const int t = 4 * quad + i;
-        if (kc == i)
+        if (factor && kc == i)
             factor[t] = scale * (l2norm ? __builtin_amdgcn_rsqf(ss + kL2Eps) : 1.0f) * __uint_as_float((64u + e) << 23);
         // (row, columns 8 kc ..) of tile (row tile, kt)
         const int at = (row_tile(t) * KT + kt) * kTile + (swz_rows(row_in(t), g, kt) + 16 * g) * 8;
         *reinterpret_cast<f16x8 *>(rows + at) = h[i];
-        if (copy) *reinterpret_cast<f16x8 *>(copy + at) = h[i];
     }
-    if constexpr (KEYS) {
+    if (cols) {
         // channel 8 kc + j: result tile d = 2 kt + j / 4, row 4 g + j % 4; tokens 4 quad ..
         const int c = (4 * quad) & 31;
 #pragma unroll
@@ -296,9 +295,8 @@ template <int KT, bool VEC>
 struct Prepare {
     const GdrParams &p;
     Scratch &sh;
-    _Float16 *k, *q;                   // the chunk's rows as tiles, in LDS
-    KeyTiles<KT> *kt;                  // where the tiles go: LDS (k and q are its own) or memory
-    HeadTiles *ht;
+    _Float16 *k, *q, *cols;            // the chunk's rows as tiles, and the keys' transposed or null, in LDS
+    HeadTiles *ht;                     // in LDS or in memory
     const Span32 sp;
     const int lane0, w;
     int h;                             // value head
@@ -311,11 +309,9 @@ struct Prepare {
     __device__ __forceinline__ void stage(int32_t c0) {
         const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
         if (w < kStage)
-            stage_quad<KT, true>(load_quad<VEC>(kr, sp, c0, quad, kc, p.Dk), k, kt->k == k ? nullptr : kt->k, kt->kt,
-                                 sh.kf, quad, kc, 1.0f, p.l2norm);
+            stage_quad<KT>(load_quad<VEC>(kr, sp, c0, quad, kc, p.Dk), k, cols, sh.kf, quad, kc, 1.0f, p.l2norm);
         else if (w < 2 * kStage)
-            stage_quad<KT, false>(load_quad<VEC>(qr, sp, c0, quad, kc, p.Dk), q, kt->q == q ? nullptr : kt->q, nullptr,
-                                  sh.qf, quad, kc, p.scale, p.l2norm);
+            stage_quad<KT>(load_quad<VEC>(qr, sp, c0, quad, kc, p.Dk), q, nullptr, sh.qf, quad, kc, p.scale, p.l2norm);
     }
 
     // Reads one word of each 128-byte line that the chunk's rows will be read from: the lines wait in L2 and the
@@ -377,7 +373,7 @@ struct Prepare {
     __device__ __forceinline__ void factors() {
         const int lane = fresh(lane0);
         const float kf = sh.kf[lane], qf = sh.qf[lane], eG = sh.eG[lane], kb = kf * sh.beta[lane];
-        kt->qf[lane] = qf;
+        ht->qf[lane] = qf;
         ht->kb[lane] = kb;
         ht->ka[lane] = kb * eG * kf;
         ht->eg[lane] = sh.eg[lane];
@@ -489,25 +485,33 @@ struct Prepare {
     __device__ __forceinline__ void invert_rest() {
         const int lane = fresh(lane0), n = lane & 15, g = lane >> 4;
         const int ti = 16 * w + n;
+        // every operand at once, used or not: what is left is a chain of products
+        f16x8 off[6], left[3];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) off[i] = tile_of(sh.off, i, lane);
+        f32x4 d[3], t;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) d[j] = -*reinterpret_cast<const f32x4 *>(sh.diag + j * 256 + n * 16 + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = sh.diag[w * 256 + (4 * g + e) * 16 + n];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            f16x4 dh, dl;
+            split4(d[j], dh, dl);
+            left[j] = f16x8{dh[0], dh[1], dh[2], dh[3], dl[0], dl[1], dl[2], dl[3]};
+        }
         f16x4 hi[4], lo[4];
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
             if (j > w) continue;
-            f32x4 t;
-            if (j == w) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) t[e] = sh.diag[j * 256 + (4 * g + e) * 16 + n];
-            } else {
+            if (j < w) {
                 f32x4 m = {0, 0, 0, 0};
 #pragma unroll
                 for (int k = 3; k >= 0; --k)
-                    if (k > j && k <= w) m = block_mfma(tile_of(sh.off, k * (k - 1) / 2 + j, lane), hi[k], lo[k], m);
-                f16x4 mh, ml, dh, dl;
+                    if (k > j && k <= w) m = block_mfma(off[k * (k - 1) / 2 + j], hi[k], lo[k], m);
+                f16x4 mh, ml;
                 split4(m, mh, ml);
-                const f32x4 d = -*reinterpret_cast<const f32x4 *>(sh.diag + j * 256 + n * 16 + 4 * g);
-                split4(d, dh, dl);
-                const f16x8 left = {dh[0], dh[1], dh[2], dh[3], dl[0], dl[1], dl[2], dl[3]};
-                t = block_mfma(left, mh, ml, f32x4{0, 0, 0, 0});
+                t = block_mfma(left[j < 3 ? j : 0], mh, ml, f32x4{0, 0, 0, 0});
             }
             split4(t, hi[j], lo[j]);
             const int tj = 16 * j + 4 * g;
@@ -1016,7 +1020,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int32_t nc = int32_t((int64_t(sp.n) + kC - 1) / kC);
     const int hk = pl.h / p.group;
-    Prepare<KT, VEC> pr{p, sh, tiles.k, tiles.q, &tiles, &tiles, sp, lane, wave, pl.h, rows_of(p.q, p.qs, sp.t0, hk),
+    Prepare<KT, VEC> pr{p, sh, tiles.k, tiles.q, tiles.kt, &tiles, sp, lane, wave, pl.h, rows_of(p.q, p.qs, sp.t0, hk),
                         rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(0);
 
@@ -1043,7 +1047,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
 // ------------------------------------------------------------ two kernels --
 //
 // Where a call has few heads to walk, the walk's length is what counts, and the tiles of all chunks are prepared
-// beforehand by every CU into a workspace: [slots][Hk] KeyTiles, then [slots][Hv] HeadTiles.  Chunk j of sequence i has
+// beforehand by every CU into a workspace: [slots][Hv] HeadTiles.  Chunk j of sequence i has
 // slot floor(start_i / 64) + i + j: no two chunks share one, and floor(T / 64) + batch + 2 of them are enough for any
 // offsets, so no kernel has to count chunks.
 
@@ -1055,7 +1059,7 @@ __device__ __forceinline__ int64_t first_slot(const GdrParams &p, int32_t b) {
 
 // A workgroup prepares one chunk of one key head, for all the value heads that share it.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, KeyTiles<KT> *keys, HeadTiles *heads) {
+__global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, HeadTiles *heads) {
     __shared__ _Float16 k[4 * KT * kTile], q[4 * KT * kTile];
     __shared__ Scratch sh;
     const int64_t slot = blockIdx.x / uint32_t(p.Hk);
@@ -1074,7 +1078,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     HeadTiles *ht = heads + slot * p.Hv + hk * p.group;
-    Prepare<KT, VEC> pr{p, sh, k, q, keys + slot * p.Hk + hk, ht, sp, lane, wave, hk * p.group, rows_of(p.q, p.qs, sp.t0, hk),
+    Prepare<KT, VEC> pr{p, sh, k, q, nullptr, ht, sp, lane, wave, hk * p.group, rows_of(p.q, p.qs, sp.t0, hk),
                         rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(c * kC);
     pr.stage(c * kC);
@@ -1093,12 +1097,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
 constexpr int kWalkers = 2;            // state waves of a walking workgroup
 constexpr int kLoaders = 4;
 
-// Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers,
-// four take the state of 16 channels each through the present one, four compute those channels' output beside them.
+// Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers (and
+// convert its keys and queries again, which costs less than their tiles in memory), two take the state of 16 channels
+// each through the present one, two compute those channels' output beside them.  Four state waves would ask more of the
+// LDS than it gives: 174 against 150 us at 4195 tokens.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLoaders) / 4) void gdr_walk_kernel(GdrParams p, const KeyTiles<KT> *keys,
-                                                                                 const HeadTiles *heads, int32_t groups,
-                                                                                 bool svec) {
+__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLoaders) / 4) void gdr_walk_kernel(GdrParams p, const HeadTiles *heads,
+                                                                                   int32_t groups, bool svec) {
     __shared__ Tiles<KT> buf[2];
     __shared__ Exchange<KT> exchange[kWalkers];
     __shared__ int ready[kWalkers];
@@ -1113,28 +1118,28 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLo
     if (threadIdx.x < kWalkers) ready[threadIdx.x] = 0;
 
     if (wave >= 2 * kWalkers) {
-        constexpr int kN = 64 * kLoaders;
-        constexpr int kKey = sizeof(KeyTiles<KT>) / 16, kHead = sizeof(HeadTiles) / 16;
-        constexpr int kKeyPer = (kKey + kN - 1) / kN, kHeadPer = (kHead + kN - 1) / kN;
-        const int t = (wave - 2 * kWalkers) * 64 + lane;
-        u32x4 rk[kKeyPer], rh[kHeadPer];
+        constexpr int kN = 64 * kLoaders, kHead = sizeof(HeadTiles) / 16, kPer = (kHead + kN - 1) / kN;
+        const int lw = wave - 2 * kWalkers, t = lw * 64 + lane, kc = t % (4 * KT), hk = pl.h / p.group;
+        // 16 quads of rows: with 128 channels every wave has four of keys and of queries, else two waves the keys
+        const bool keys = KT == 4 || lw < 2, queries = KT == 4 || lw >= 2;
+        const int quad = t / (4 * KT) & 15;
+        const Rows kr = rows_of(p.k, p.ks, sp.t0, hk), qr = rows_of(p.q, p.qs, sp.t0, hk);
+        u32x4 rh[kPer];
+        Quad k, q;
         const auto load = [&](int32_t c) {
-            const u32x4 *k = reinterpret_cast<const u32x4 *>(keys + (slot + c) * p.Hk + pl.h / p.group);
             const u32x4 *h = reinterpret_cast<const u32x4 *>(heads + (slot + c) * p.Hv + pl.h);
 #pragma unroll
-            for (int i = 0; i < kKeyPer; ++i) rk[i] = k[t + i * kN < kKey ? t + i * kN : 0];
-#pragma unroll
-            for (int i = 0; i < kHeadPer; ++i) rh[i] = h[t + i * kN < kHead ? t + i * kN : 0];
+            for (int i = 0; i < kPer; ++i) rh[i] = h[t + i * kN < kHead ? t + i * kN : 0];
+            if (keys) k = load_quad<VEC>(kr, sp, c * kC, quad, kc, p.Dk);
+            if (queries) q = load_quad<VEC>(qr, sp, c * kC, quad, kc, p.Dk);
         };
         const auto put = [&](Tiles<KT> &b) {
-            u32x4 *k = reinterpret_cast<u32x4 *>(static_cast<KeyTiles<KT> *>(&b));
             u32x4 *h = reinterpret_cast<u32x4 *>(static_cast<HeadTiles *>(&b));
 #pragma unroll
-            for (int i = 0; i < kKeyPer; ++i)
-                if (t + i * kN < kKey) k[t + i * kN] = rk[i];
-#pragma unroll
-            for (int i = 0; i < kHeadPer; ++i)
+            for (int i = 0; i < kPer; ++i)
                 if (t + i * kN < kHead) h[t + i * kN] = rh[i];
+            if (keys) stage_quad<KT>(k, b.k, b.kt, nullptr, quad, kc, 1.0f, false);
+            if (queries) stage_quad<KT>(q, b.q, nullptr, nullptr, quad, kc, 1.0f, false);
         };
         load(0);
         put(buf[0]);
@@ -1188,20 +1193,18 @@ hipError_t launch_one(const GdrParams &p, bool svec, hipStream_t s) {
 template <int KT, bool VEC>
 hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream_t s) {
     const int64_t slots = gdr_slots(p.total_T, p.batch);
-    KeyTiles<KT> *keys = static_cast<KeyTiles<KT> *>(workspace);
-    HeadTiles *heads = reinterpret_cast<HeadTiles *>(keys + slots * p.Hk);
-    gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, keys, heads);
+    HeadTiles *heads = static_cast<HeadTiles *>(workspace);
+    gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, heads);
     const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
     gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
-        p, keys, heads, groups, svec);
+        p, heads, groups, svec);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hk, int32_t Hv, int32_t Dk) {
-    const int64_t key = Dk <= 64 ? sizeof(KeyTiles<2>) : sizeof(KeyTiles<4>);
-    return gdr_slots(T, batch) * (Hk * key + Hv * int64_t(sizeof(HeadTiles)));
+int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hv) {
+    return gdr_slots(T, batch) * Hv * int64_t(sizeof(HeadTiles));
 }
 
 hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, void *workspace, hipStream_t s) {

@@ -67,7 +67,7 @@ hipError_t launch_gdr_recurrent(const GdrParams &p, bool vec, hipStream_t s);
 // elements; `svec`: the state's rows in 16-byte pieces.  Dk at most kGdrMaxChunkK.
 // With a workspace of gdr_workspace_bytes(), 16-byte aligned: two kernels, the
 // tiles of all chunks first; without (vec only): one kernel.
-int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hk, int32_t Hv, int32_t Dk);
+int64_t gdr_workspace_bytes(int64_t T, int64_t batch, int32_t Hv);
 hipError_t launch_gdr_chunk(const GdrParams &p, bool vec, bool svec, void *workspace, hipStream_t s);
 hipError_t launch_verify_drafts(const VerifyParams &p, hipStream_t s);
 
