@@ -314,19 +314,6 @@ struct Prepare {
             stage_quad<KT>(load_quad<VEC>(qr, sp, c0, quad, kc, p.Dk), q, nullptr, sh.qf, quad, kc, p.scale, p.l2norm);
     }
 
-    // Reads one word of each 128-byte line that the chunk's rows will be read from: the lines wait in L2 and the
-    // registers stay free.  The caller keeps the word until the reads have had their time.
-    __device__ __forceinline__ uint32_t touch(int32_t c0, const Rows &vr, int32_t v0) {
-        uint32_t word = 0;
-        if constexpr (VEC) {
-            const int lane = fresh(lane0), i = 64 * (w & 1) + lane;
-            const Rows &r = w < 2 ? kr : w < 4 ? qr : vr;
-            const int32_t end = w < 4 ? p.Dk : p.Dv, c = (w < 4 ? 0 : v0) + 64 * (i & 1);
-            if (w < 6 && c < end) word = buf_ld16(chunk_rsrc(r, sp, c0), uint32_t(i >> 1) * r.row + uint32_t(c) * 2);
-        }
-        return word;
-    }
-
     // From the chunk's staged rows and its gates in LDS to its tiles.  `ahead` runs in wave 7 once the gates' place is free.
     template <class F>
     __device__ __forceinline__ void tiles(F ahead) {
@@ -710,17 +697,19 @@ struct Consumer {
     }
     static __device__ __forceinline__ f32x4 row4(const float *v, int t) { return *reinterpret_cast<const f32x4 *>(v + t); }
 
-    // The state and the output through one chunk, in as few registers as go: four waves a SIMD hide what each waits for.
+    // The state and the output through one chunk, in 128 registers: four waves a SIMD hide what each waits for.
     __device__ __forceinline__ void chunk(int32_t t0, const Tiles<KT> &b) {
         const int lane = fresh(lane0), g = lane >> 4;
         f32x4 ak[4], aq[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) { ak[mt] = f32x4{0, 0, 0, 0}; aq[mt] = f32x4{0, 0, 0, 0}; }
         const float ms = largest(), oinv = pow2(-un);
+        u32x4 v[4];
         // K S and Q S, the state split on the way (its largest element is below 2^15)
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             f16x8 hi, lo;
+            if (kt == KT - 1) fetch(t0, v);            // (from L2)
             split_state(kt, hi, lo);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
@@ -728,13 +717,9 @@ struct Consumer {
                 ak[mt] = mfma(kf, hi, ak[mt]);
                 aq[mt] = mfma(hi, qf, aq[mt]);         // (transposed, as the output is)
                 ak[mt] = mfma(kf, lo, ak[mt]);
-                if (mt == 1) __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
         // X, scaled to 2^12
-        u32x4 v[4];
-        fetch(t0, v);                                  // (from L2; registers are what bounds the products above)
         float x[16], xm = 0.0f;
         const bf16x8 id = identity(lane);
 #pragma unroll
@@ -765,7 +750,6 @@ struct Consumer {
                 z[mt] = mfma(h, xl, z[mt]);
                 z[mt] = mfma(l, xh, z[mt]);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
         const Units u = next_unit(z, ms, b.last, xe);
 #pragma unroll
@@ -785,7 +769,6 @@ struct Consumer {
                 S[d] = mfma(k, yh, S[d]);
                 S[d] = mfma(k, yl, S[d]);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
         // o
         f32x4 o[4], oi, ni;
@@ -1035,10 +1018,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
         const bool more = c + 1 < nc;
         pr.stage(c * kC);
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
-        uint32_t word = 0;
-        if (more) word = pr.touch((c + 1) * kC, st.vr, pl.cg * kWaves * 16);
         if (work) st.chunk(c * kC, tiles);
-        asm volatile("" : : "v"(word));
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
