@@ -45,7 +45,7 @@ __device__ __forceinline__ void load_state(const float *p, int64_t sk, int32_t D
         const int c = 32 * i + 4 * j;
         if constexpr (VEC) {
             f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (row && c < Dk) w = *reinterpret_cast<const f32x4 *>(p + c);
+            if (row && c < Dk) w = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p + c));
             f[4 * i] = w.x; f[4 * i + 1] = w.y; f[4 * i + 2] = w.z; f[4 * i + 3] = w.w;
         } else {
 #pragma unroll
@@ -62,7 +62,7 @@ __device__ __forceinline__ void store_state(float *p, int64_t sk, int32_t Dk, in
         const int c = 32 * i + 4 * j;
         if constexpr (VEC) {
             const f32x4 w = {f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-            if (row && c < Dk) *reinterpret_cast<f32x4 *>(p + c) = w;
+            if (row && c < Dk) __builtin_nontemporal_store(w, reinterpret_cast<f32x4 *>(p + c));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
