@@ -271,7 +271,7 @@ int gdr_update(const void *q, int64_t q_stride_seq, int64_t q_stride_tok, int64_
 int64_t sconv_verify_workspace_bytes(int32_t batch, int32_t vocab) {
     if (batch <= 0 || vocab <= 0) return 0;
     const int64_t slice = verify_slice(batch, vocab);
-    return int64_t(batch) * ((vocab + slice - 1) / slice) * 16;
+    return int64_t(batch) * ((vocab + slice - 1) / slice) * 16 + (int64_t(batch) + 1) / 2 * 8;
 }
 
 int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_loc,
@@ -336,6 +336,7 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
     p.slice = verify_slice(batch, vocab);
     p.slices = int32_t((int64_t(vocab) + p.slice - 1) / p.slice);
     p.sums_ws = static_cast<double *>(workspace);
+    p.count_ws = reinterpret_cast<int32_t *>(p.sums_ws + int64_t(batch) * p.slices * 2);
     p.tokens = tokens;
     p.t_sr = t_stride_row;
     p.num_accepted = num_accepted_tokens;

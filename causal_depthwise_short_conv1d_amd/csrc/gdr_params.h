@@ -54,6 +54,7 @@ struct VerifyParams {
     int32_t batch, num_drafts, vocab, max_drafts;
     int32_t slice, slices;          // vocabulary entries per workgroup, workgroups per request
     double *sums_ws;                // [batch][slices][2]
+    int32_t *count_ws;              // [batch]: standing drafts
     int32_t *tokens;                // [batch][max_drafts + 1]
     int64_t t_sr;
     int32_t *num_accepted;          // [batch]

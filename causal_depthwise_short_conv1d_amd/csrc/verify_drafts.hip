@@ -28,22 +28,39 @@ struct Decision {
     int32_t n;
 };
 
-// Which drafts stand: 64 at a time, a lane each, the first refusal by ballot.
-// Every wave of a request does this by itself (two dependent reads).
-__device__ __forceinline__ Decision decide(const VerifyParams &p, int32_t b) {
+__device__ __forceinline__ Decision request(const VerifyParams &p, int32_t b) {
     Decision r;
     int32_t a = p.start[b], e = p.start[b + 1];
     a = a < 0 ? 0 : (a > p.num_drafts ? p.num_drafts : a);
     e = e < a ? a : (e > p.num_drafts ? p.num_drafts : e);
     r.d0 = a;
     r.n = e - a < p.max_drafts ? e - a : p.max_drafts;
-    r.count = r.n;
+    return r;
+}
+// The rows that decide once `count` drafts stand.
+__device__ __forceinline__ void rows_after(const VerifyParams &p, int32_t b, int32_t count, Decision &r) {
+    r.count = count;
+    const int64_t d = int64_t(r.d0) + count;
+    r.p = p.p + (d + b) * p.p_sr;
+    r.q = nullptr;
+    r.out_token = -1;
+    if (count < r.n) {
+        if (p.q) r.q = p.q + d * p.q_sr;
+        else r.out_token = p.draft_tokens[d];
+    }
+}
+
+// Which drafts stand: 64 at a time, a lane each, the first refusal by ballot.  Every wave of the summing kernel does this
+// by itself (two dependent reads).
+__device__ __forceinline__ Decision decide(const VerifyParams &p, int32_t b) {
+    Decision r = request(p, b);
+    int32_t count = r.n;
     const int lane = threadIdx.x & 63;
     for (int32_t base = 0; base < r.n; base += 64) {
         const int32_t j = base + lane;
         bool refused = false;
         if (j < r.n) {
-            const int64_t d = a + j;
+            const int64_t d = r.d0 + j;
             const int32_t x = p.draft_tokens[d];
             refused = true;
             if (x >= 0 && x < p.vocab) {
@@ -54,18 +71,11 @@ __device__ __forceinline__ Decision decide(const VerifyParams &p, int32_t b) {
         }
         const uint64_t m = __ballot(refused);
         if (m) {
-            r.count = base + __builtin_ctzll(m);
+            count = base + __builtin_ctzll(m);
             break;
         }
     }
-    const int64_t d = int64_t(a) + r.count;
-    r.p = p.p + (d + b) * p.p_sr;
-    r.q = nullptr;
-    r.out_token = -1;
-    if (r.count < r.n) {
-        if (p.q) r.q = p.q + d * p.q_sr;
-        else r.out_token = p.draft_tokens[d];
-    }
+    rows_after(p, b, count, r);
     return r;
 }
 
@@ -89,10 +99,10 @@ __global__ __launch_bounds__(kVfBlock) void verify_sums_kernel(VerifyParams p) {
     const Decision d = decide(p, b);
     const int32_t lo = s * p.slice, hi = lo + p.slice < p.vocab ? lo + p.slice : p.vocab;
     double left = 0.0, all = 0.0;
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t i = lo + tid; i < hi; i += kVfBlock) {
-        const float pv = d.p[i];
-        const float qv = d.q ? d.q[i] : 0.0f;
+        const float pv = __builtin_nontemporal_load(d.p + i);
+        const float qv = d.q ? __builtin_nontemporal_load(d.q + i) : 0.0f;
         all += mass(pv);
         left += left_of(d, i, pv, qv);
     }
@@ -107,6 +117,7 @@ __global__ __launch_bounds__(kVfBlock) void verify_sums_kernel(VerifyParams p) {
         for (int w = 0; w < kVfBlock / 64; ++w) t += part[tid][w];
         p.sums_ws[(int64_t(b) * p.slices + s) * 2 + tid] = t;
     }
+    if (s == 0 && tid == 2) p.count_ws[b] = d.count;
 }
 
 // Inclusive running sum over a wave's lanes.
@@ -129,7 +140,8 @@ __global__ __launch_bounds__(kVfBlock) void verify_pick_kernel(VerifyParams p) {
     __shared__ double part[kVfBlock / 64];
     __shared__ int32_t found[kVfBlock / 64], last[kVfBlock / 64];
     const double *sums = p.sums_ws + int64_t(b) * p.slices * 2;
-    Decision d = decide(p, b);
+    Decision d = request(p, b);
+    rows_after(p, b, p.count_ws[b], d);
 
     // Every wave by itself: which slice.  A lane takes `per` consecutive slice sums.
     const int32_t per = (p.slices + 63) / 64;

@@ -164,8 +164,8 @@ def test_verify_refusals(lib):
 def test_workspace_bytes(lib):
     f = lib.sconv_verify_workspace_bytes
     assert f(0, 1000) == 0 and f(3, 0) == 0 and f(-1, 5) == 0
-    assert f(1, 1) == 16 and f(2, 1024) == 32
-    assert f(1 << 20, 1 << 20) % 16 == 0 and f(1 << 20, 1 << 20) > 1 << 24
+    assert f(1, 1) == 16 + 8 and f(2, 1024) == 32 + 8
+    assert f(1 << 20, 1 << 20) % 8 == 0 and f(1 << 20, 1 << 20) > 1 << 24
 
 
 def test_binding_refusals():
