@@ -119,7 +119,8 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
                    float scale, int32_t qk_l2norm, int32_t pad_slot_id,
                    void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
                    void *workspace, int64_t workspace_bytes, hipStream_t stream) {
-    if (batch < 0 || total_tokens < 0 || total_tokens > INT32_MAX || num_cache_lines < 0)
+    // token offsets of whole chunks stay within 31 bits
+    if (batch < 0 || total_tokens < 0 || total_tokens > INT32_MAX - 256 || num_cache_lines < 0)
         return SCONV_ERR_SHAPE;
     if (batch == 0 || total_tokens == 0) return SCONV_OK;
     if (!query_start_loc || (has_initial_state && !state)) return SCONV_ERR_NULL;
@@ -193,7 +194,10 @@ int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num
     if (batch < 1 || total_tokens < 1 || num_k_heads < 1 || num_v_heads < 1 || head_dim_k < 1 || head_dim_v < 1 ||
         head_dim_k > kGdrMaxChunkK)
         return 0;
-    if (vector_layout && !gdr_few_heads(total_tokens, batch, num_v_heads, head_dim_v)) return 0;
+    // many heads fill the chip by themselves; short sequences in layouts by elements go a token at a time, which takes
+    // some 2 us a token where a chunk's workspace is 19 KB a head
+    if (vector_layout ? !gdr_few_heads(total_tokens, batch, num_v_heads, head_dim_v) : total_tokens <= 32 * int64_t(batch))
+        return 0;
     const int64_t slots = gdr_slots(total_tokens, batch);
     if (slots * num_k_heads >= (int64_t(1) << 31)) return 0;
     return gdr_workspace_bytes(total_tokens, batch, num_v_heads);

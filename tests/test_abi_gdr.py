@@ -38,9 +38,10 @@ def test_fwd_workspace(lib):
         assert fwd(lib, T=1000, ws=addr(x), wb=need) == EALIAS, x
     assert lib.gdr_fwd_workspace_bytes(2, 256, 4, 8, 64, 64, 1) == 0            # short sequences: one kernel
     assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 1) == 0          # many heads: one kernel
-    assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 0) > 0
-    for bad in ((0, 10, 4, 8, 64, 64, 1), (2, 0, 4, 8, 64, 64, 1), (2, 10, 0, 8, 64, 64, 1), (2, 10, 4, 8, 129, 64, 1),
-                (2, 10, 4, 8, 64, 0, 1)):
+    assert lib.gdr_fwd_workspace_bytes(2000, 64000, 4, 8, 64, 64, 0) == 0       # short sequences, by elements
+    assert lib.gdr_fwd_workspace_bytes(2000, 64001, 4, 8, 64, 64, 0) > 0
+    for bad in ((0, 1000, 4, 8, 64, 64, 1), (2, 0, 4, 8, 64, 64, 1), (2, 1000, 0, 8, 64, 64, 1),
+                (2, 1000, 4, 8, 129, 64, 1), (2, 1000, 4, 8, 64, 0, 1)):
         assert lib.gdr_fwd_workspace_bytes(*bad) == 0
 
 
@@ -67,7 +68,7 @@ def test_fwd_nulls(lib):
 
 
 def test_fwd_sizes(lib):
-    for kw in (dict(batch=-1), dict(T=-1), dict(T=1 << 31), dict(hk=0), dict(hv=0), dict(hk=3), dict(dk=0), dict(dv=0),
+    for kw in (dict(batch=-1), dict(T=-1), dict(T=1 << 31), dict(T=(1 << 31) - 256), dict(hk=0), dict(hv=0), dict(hk=3), dict(dk=0), dict(dv=0),
                dict(dk=257, ss=(1 << 30, 1 << 24, 257, 1)), dict(lines=0), dict(ci=None, lines=1), dict(lines=-1),
                dict(batch=1 << 30)):
         assert fwd(lib, **kw) == ESHAPE, kw

@@ -365,6 +365,59 @@ def test_graph_replays_match_eager(op):
         assert torch.equal(st, want) and torch.equal(out, wout), i
 
 
+@pytest.mark.parametrize("nseq,T", [(1, 300), (60, 40)])
+def test_two_streams_at_once(nseq, T):
+    """Calls in flight together, each with its own workspace (one sequence) or none (many heads), give what they give alone."""
+    qsl = torch.arange(nseq + 1, dtype=torch.int32, device=DEV) * T
+    cases = []
+    for seed in (80, 81):
+        d = R.on(R.draw_inputs((nseq * T,), 2, 4, 64, 64, seed), DEV)
+        cases.append((d, torch.randn(nseq, 4, 64, 64, device=DEV) * 0.3))
+    has = torch.ones(nseq, dtype=torch.bool, device=DEV)
+
+    def call(d, st):
+        return S.gdr_fwd_varlen(d["q"], d["k"], d["v"], d["g"], d["beta"], st, qsl, None, has, A_log=d["A_log"],
+                                dt_bias=d["dt_bias"], use_qk_l2norm=True)
+    alone = []
+    for d, st in cases:
+        s = st.clone()
+        alone.append((call(d, s), s))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = [None, None]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        states = [st.clone() for _, st in cases]
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = call(cases[i][0], states[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(got[i], alone[i][0]) and torch.equal(states[i], alone[i][1])
+
+
+def test_prefill_short_sequences_by_elements():
+    """Odd sizes and short sequences: a token at a time, without a workspace."""
+    prefill([1 + i % 7 for i in range(40)], 1, 2, 36, 20, seed=90, pads=(5,))
+
+
+def test_one_kernel_and_two_agree():
+    """The same sequences alone (two kernels) and among many (one kernel)."""
+    d = R.on(R.draw_inputs((40 * 200,), 2, 8, 64, 64, 91), DEV)
+    st = torch.randn(40, 8, 64, 64, device=DEV) * 0.3
+    many, few = st.clone(), st[:1].clone()
+    kw = dict(A_log=d["A_log"], dt_bias=d["dt_bias"], use_qk_l2norm=True)
+    has = torch.ones(40, dtype=torch.bool, device=DEV)
+    a = S.gdr_fwd_varlen(d["q"], d["k"], d["v"], d["g"], d["beta"], many,
+                         torch.arange(41, dtype=torch.int32, device=DEV) * 200, None, has, **kw)
+    b = S.gdr_fwd_varlen(*(d[x][:200] for x in ("q", "k", "v", "g", "beta")), few,
+                         torch.tensor([0, 200], dtype=torch.int32, device=DEV), None, has[:1], **kw)
+    # the same products in the same order: the state to fp32's last bits, the output to a bf16 step
+    assert ((a[:200].float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 1e-6).all()
+    assert ((many[0] - few[0]).abs() <= 2.0 ** -20 * few[0].abs().amax(-1, keepdim=True)).all()
+
+
 def test_state_offsets_past_32_bits():
     """A cache of more than 2^31 elements; only its last line is touched."""
     hv, dv, dk = 32, 128, 128
