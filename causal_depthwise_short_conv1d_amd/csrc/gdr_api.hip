@@ -87,14 +87,15 @@ int check_gdr(const GdrParams &p, int64_t B, int64_t T, bool *vec) {
            groups_of(p.k, 4, 2, {B, T, p.Hk}, {p.ks.sb, p.ks.st, p.ks.sh}) &&
            (!p.state || (p.s_sk == 1 && groups_of(p.state, 4, 4, {p.num_lines, p.Hv, p.Dv},
                                                   {p.s_sl, p.s_sh, p.s_sv})));
-    // one workgroup takes at least 4 rows of 8 state rows: the grid fits 31 bits
-    const uint64_t tiles = uint64_t(p.batch) * uint64_t(p.Hv) * ((uint64_t(p.Dv) + 7) / 8);
-    if (tiles >= (uint64_t(1) << 31)) return SCONV_ERR_SHAPE;
+    // the recurrent kernel gives a wave to 8 state rows at least
+    const int64_t heads = int64_t(p.batch) * p.Hv;
+    if (heads > kMaxThreads / 64 || heads * ((int64_t(p.Dv) + 7) / 8) > kMaxThreads / 64 - 4) return SCONV_ERR_SHAPE;
     return SCONV_OK;
 }
 
-// Vocabulary entries a workgroup of the summing kernel takes: enough
-// workgroups to fill the chip twice, 1024 to 8192 entries each.
+// Vocabulary entries a workgroup of the summing kernel takes: some 2048
+// workgroups (8 a CU), 1024 to 8192 entries each; the picking kernel holds a
+// whole slice in registers.
 int32_t verify_slice(int64_t batch, int64_t vocab) {
     int64_t s = (batch * vocab + 2047) / 2048;
     s = (s + 255) / 256 * 256;
@@ -184,7 +185,8 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
                 return SCONV_ERR_ALIAS;
             return launch_status(launch_gdr_chunk(p, vec8, svec, workspace, stream));
         }
-        if (vec8) return launch_status(launch_gdr_chunk(p, vec8, svec, nullptr, stream));
+        if (vec8 && gdr_walk_grid(batch, p.Hk, p.Hv, (int64_t(p.Dv) + 127) / 128) <= kMaxThreads / kGdrThreads)
+            return launch_status(launch_gdr_chunk(p, vec8, svec, nullptr, stream));
     }
     return launch_status(launch_gdr_recurrent(p, vec, stream));
 }
@@ -192,14 +194,16 @@ int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, i
 int64_t gdr_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num_k_heads, int32_t num_v_heads,
                                 int32_t head_dim_k, int32_t head_dim_v, int32_t vector_layout) {
     if (batch < 1 || total_tokens < 1 || num_k_heads < 1 || num_v_heads < 1 || head_dim_k < 1 || head_dim_v < 1 ||
-        head_dim_k > kGdrMaxChunkK)
+        head_dim_k > kGdrMaxChunkK || num_v_heads % num_k_heads || int64_t(batch) * num_v_heads > kMaxThreads / 64)
         return 0;
     // many heads fill the chip by themselves; short sequences in layouts by elements go a token at a time, which takes
     // some 2 us a token where a chunk's workspace is 19 KB a head
     if (vector_layout ? !gdr_few_heads(total_tokens, batch, num_v_heads, head_dim_v) : total_tokens <= 32 * int64_t(batch))
         return 0;
     const int64_t slots = gdr_slots(total_tokens, batch);
-    if (slots * num_k_heads >= (int64_t(1) << 31)) return 0;
+    if (slots * num_k_heads > kMaxThreads / kGdrThreads ||
+        gdr_walk_grid(batch, num_k_heads, num_v_heads, (int64_t(head_dim_v) + 31) / 32) > kMaxThreads / kGdrThreads)
+        return 0;
     return gdr_workspace_bytes(total_tokens, batch, num_v_heads);
 }
 
@@ -344,7 +348,7 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
     p.tokens = tokens;
     p.t_sr = t_stride_row;
     p.num_accepted = num_accepted_tokens;
-    if (int64_t(p.slices) * batch >= (int64_t(1) << 31)) return SCONV_ERR_SHAPE;
+    if (int64_t(p.slices) * batch > kMaxThreads / 256) return SCONV_ERR_SHAPE;
     return launch_status(launch_verify_drafts(p, stream));
 }
 

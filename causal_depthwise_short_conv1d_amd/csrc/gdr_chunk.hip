@@ -10,13 +10,28 @@
 // Written with z, T has entries of order 1 whenever the rule contracts
 // (beta |k|^2 <= 2), whatever the keys' norms.
 //
-// A workgroup of 8 waves owns 128 value channels of one head and walks its
-// sequence.  Per chunk it prepares the operands in LDS (conversion, K K^T,
-// Q K^T, the inverse: phases between barriers), then each wave takes its 16
-// channels through the chunk with the state in its registers.  Two workgroups
-// share a CU, so that one's matrix products run beside the other's conversions
-// and waits.
-// Those waves never exchange anything: an MFMA result has its channel in
+// The rule by itself is some 100 K fp32 operations a token and head, each token
+// waiting for the one before.  Here the same work is matrix products, 64 tokens
+// at a time: 64 sequences of up to 2048 tokens, 32 heads of 128 x 128, take
+// 0.76 ms where a token at a time takes 18.7 ms.
+//
+// One kernel (many heads).  A workgroup of 8 waves owns 128 value channels of
+// one head and walks its sequence.  Per chunk it prepares the operands in LDS
+// (conversion, K K^T, Q K^T, the inverse: phases between barriers), then each
+// wave takes its 16 channels through the chunk with the state in its
+// registers.  Two workgroups share a CU (128 registers, 79 KB), so that one's
+// matrix products run beside the other's conversions and waits: 1.07 ms, where
+// waves that only prepare beside waves that only consume, one workgroup a CU,
+// took 1.21.  What bounds it now is the VALU, 73 % busy with conversions,
+// scaling and addresses (1200 instructions a wave and chunk), beside the MFMAs
+// (29 %); bytes alone would take 0.34 ms.
+//
+// Two kernels (few heads): a walk is a chain of chunks, so everything that does
+// not depend on the state is prepared before it by the whole chip.  At 4195
+// tokens, 32 heads: 29 us and 143 us for 66 chunks, 2.2 us each, half of it
+// MFMAs that wait for one another; at 14807 tokens 75 and 475 us.
+//
+// Waves of one state never exchange anything: an MFMA result has its channel in
 // the lane and 4 rows a register quad, and the next product takes it as its
 // right operand as it lies, since the order of a contracted index is free.  So
 // key channel 32 kt + 8 g + 4 t + i is row 4 g + i of result tile 2 kt + t and
@@ -42,6 +57,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kC = 64;                 // tokens per chunk
 constexpr int kWaves = 8;              // waves per workgroup, 16 value channels each
+static_assert(64 * kWaves == kGdrThreads, "the host's launch checks");
 
 // Tile-ordered operands in LDS: a 16-row x 32-column fp16 tile is 1 KiB, lane
 // l's 16 bytes (row l % 16, columns 8 (l / 16) ..) at 16 l, so a wave reads a
@@ -91,7 +107,7 @@ __device__ __forceinline__ int tok_of(int mt, int r) { return 32 * (mt >> 1) + 8
 __device__ __forceinline__ int in_tile(int r, int c) { return (r + 16 * (c >> 3)) * 8 + (c & 7); }
 
 // Rows of the k and q tiles are stored at r ^ (g + 4 (kt % 2)), g = column / 8, and rows of the transposed tiles at
-// r ^ (d / 2): the producers' 64 lanes then write to every bank alike, and a read is a permutation of 256 bytes.
+// r ^ (d / 2): the staging waves' 64 lanes then write to every bank alike, and a read is a permutation of 256 bytes.
 __device__ __forceinline__ int swz_rows(int r, int g, int kt) { return r ^ (g + 4 * (kt & 1)); }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }   // -126..127
@@ -193,7 +209,7 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *row, int64_t sd, int c, i
     return r;
 }
 
-// Four token rows of eight channels each, as a producer thread holds them.
+// Four token rows of eight channels each, as a staging thread holds them.
 struct Quad { u32x4 r[4]; };
 
 template <bool VEC>
@@ -268,7 +284,7 @@ __device__ __forceinline__ double dpp_add64(double x) {
     return x + __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
 
-// -row[j] of lane I's 16-lane row.
+// What lane I of the 16-lane row holds.
 template <int I>
 __device__ __forceinline__ float row_bcast(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + I, 0xf, 0xf, true));
@@ -1026,8 +1042,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
 
 // ------------------------------------------------------------ two kernels --
 //
-// Where a call has few heads to walk, the walk's length is what counts, and the tiles of all chunks are prepared
-// beforehand by every CU into a workspace: [slots][Hv] HeadTiles.  Chunk j of sequence i has
+// The tiles of all chunks are prepared into a workspace, [slots][Hv] HeadTiles (19 KB each).  Chunk j of sequence i has
 // slot floor(start_i / 64) + i + j: no two chunks share one, and floor(T / 64) + batch + 2 of them are enough for any
 // offsets, so no kernel has to count chunks.
 
@@ -1076,11 +1091,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
 
 constexpr int kWalkers = 2;            // state waves of a walking workgroup
 constexpr int kLoaders = 4;
+static_assert(64 * (2 * kWalkers + kLoaders) == kGdrThreads, "the host's launch checks");
 
 // Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers (and
-// convert its keys and queries again, which costs less than their tiles in memory), two take the state of 16 channels
-// each through the present one, two compute those channels' output beside them.  Four state waves would ask more of the
-// LDS than it gives: 174 against 150 us at 4195 tokens.
+// convert its keys and queries again, which costs less than their tiles in memory: 168 against 192 us at 4195 tokens),
+// two take the state of 16 channels each through the present one, two compute those channels' output beside them.  Four
+// state waves ask more of the LDS than it gives, 174 against 150 us at 4195 tokens; one, with
+// twice the workgroups, saves 2 % of the whole and is slower where these fill the chip.
 template <int KT, bool VEC>
 __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLoaders) / 4) void gdr_walk_kernel(GdrParams p, const HeadTiles *heads,
                                                                                    int32_t groups, bool svec) {
@@ -1158,15 +1175,10 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLo
     if (p.state) st.save(rows, svec);
 }
 
-// Workgroups of a kernel that walks sequences, `groups` a head (see place_of).
-int64_t walk_grid(const GdrParams &p, int32_t groups) {
-    return (int64_t(p.batch) * p.Hk + 7) / 8 * 8 * p.group * groups;
-}
-
 template <int KT>
 hipError_t launch_one(const GdrParams &p, bool svec, hipStream_t s) {
     const int32_t groups = (p.Dv + 16 * kWaves - 1) / (16 * kWaves);
-    gdr_chunk_kernel<KT, true><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * kWaves), 0, s>>>(p, groups, svec);
+    gdr_chunk_kernel<KT, true><<<dim3(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups))), dim3(64 * kWaves), 0, s>>>(p, groups, svec);
     return hipGetLastError();
 }
 
@@ -1176,7 +1188,7 @@ hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream
     HeadTiles *heads = static_cast<HeadTiles *>(workspace);
     gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, heads);
     const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
-    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(walk_grid(p, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
+    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
         p, heads, groups, svec);
     return hipGetLastError();
 }

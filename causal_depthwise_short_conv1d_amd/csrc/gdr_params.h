@@ -75,9 +75,17 @@ hipError_t launch_verify_drafts(const VerifyParams &p, hipStream_t s);
 // Slots for the 64-token chunks of any packing of T tokens into `batch` sequences.
 inline int64_t gdr_slots(int64_t T, int64_t batch) { return T / 64 + batch + 2; }
 
+// Workgroups of a kernel that walks sequences, `groups` a head: batch * Hk rounded up to the 8 XCDs.
+inline int64_t gdr_walk_grid(int64_t batch, int64_t Hk, int64_t Hv, int64_t groups) {
+    return (batch * Hk + 7) / 8 * 8 * (Hv / Hk) * groups;
+}
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;     // of a launch
+constexpr int kGdrThreads = 512;                               // a workgroup of the chunked kernels
+
 // Whether a call's heads are so few, and its sequences long enough, that walking prepared chunks in two kernels is
-// faster than one kernel.  Measured with 128 x 128 heads, two kernels / one: 32 heads of 2048 tokens 100 / 298 us, 128
-// heads 236 / 304, 256 heads 433 / 341; 32 heads of 256 tokens 28 / 45, of 64 tokens 29 / 23.
+// faster than one kernel.  Measured with 128 x 128 heads, two kernels / one: 32 heads of 2048 tokens 90 / 260 us, 128
+// heads 189 / 263, 192 heads 275 / 289, 256 heads 365 / 296; 32 heads of 256 tokens 25 / 38, of 128 tokens 21 / 23, of
+// 64 tokens 21 / 16; 128 heads of 256 tokens 42 / 40.
 inline bool gdr_few_heads(int64_t T, int64_t batch, int64_t Hv, int64_t Dv) {
     return batch * Hv * ((Dv + 63) / 64) <= 256 && T > 128 * batch;
 }

@@ -11,6 +11,10 @@
 // verify_sums_kernel streams the deciding row(s) once, a slice a workgroup,
 // and is bound by those reads; verify_pick_kernel (a workgroup a request)
 // scans the slice sums and reads one slice again, into registers).
+// 64 requests of 131072 entries: 13 us for the sums, which read 67 MB
+// (5.2 TB/s), and 7 us to pick: three dependent reads and as many scans, about
+// what any workgroup takes for them.  256 requests without draft rows: 22 and
+// 8 us.  (Reading the rows past the caches is worth 1 % either way.)
 #include "gdr_params.h"
 #include "sconv_device.h"
 
@@ -101,8 +105,8 @@ __global__ __launch_bounds__(kVfBlock) void verify_sums_kernel(VerifyParams p) {
     double left = 0.0, all = 0.0;
 #pragma unroll 8
     for (int32_t i = lo + tid; i < hi; i += kVfBlock) {
-        const float pv = __builtin_nontemporal_load(d.p + i);
-        const float qv = d.q ? __builtin_nontemporal_load(d.q + i) : 0.0f;
+        const float pv = d.p[i];
+        const float qv = d.q ? d.q[i] : 0.0f;
         all += mass(pv);
         left += left_of(d, i, pv, qv);
     }

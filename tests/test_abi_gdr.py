@@ -40,8 +40,14 @@ def test_fwd_workspace(lib):
     assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 1) == 0          # many heads: one kernel
     assert lib.gdr_fwd_workspace_bytes(2000, 64000, 4, 8, 64, 64, 0) == 0       # short sequences, by elements
     assert lib.gdr_fwd_workspace_bytes(2000, 64001, 4, 8, 64, 64, 0) > 0
+    # more threads than a launch can have: the prepared chunks', the walk's
+    assert lib.gdr_fwd_workspace_bytes(1, 1 << 26, 1, 8, 64, 64, 1) > 0
+    assert lib.gdr_fwd_workspace_bytes(1, 1 << 26, 8, 8, 64, 64, 1) == 0
+    assert lib.gdr_fwd_workspace_bytes(1 << 20, 1 << 26, 1, 1, 64, 64, 0) > 0
+    assert lib.gdr_fwd_workspace_bytes(1 << 20, 1 << 26, 1, 16, 64, 64, 0) == 0
     for bad in ((0, 1000, 4, 8, 64, 64, 1), (2, 0, 4, 8, 64, 64, 1), (2, 1000, 0, 8, 64, 64, 1),
-                (2, 1000, 4, 8, 129, 64, 1), (2, 1000, 4, 8, 64, 0, 1)):
+                (2, 1000, 4, 8, 129, 64, 1), (2, 1000, 4, 8, 64, 0, 1), (2, 1000, 3, 8, 64, 64, 1),
+                ((1 << 31) - 1, 1 << 30, 1, (1 << 31) - 1, 64, (1 << 31) - 1, 0)):
         assert lib.gdr_fwd_workspace_bytes(*bad) == 0
 
 
