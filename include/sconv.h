@@ -40,12 +40,15 @@
  *   - The library allocates nothing, never reads device memory on the host
  *     and never synchronises: each call validates its host arguments, then
  *     enqueues one kernel on `stream` (NULL = the default stream) and
- *     returns.  Two forms enqueue more, all on `stream`: a token-contiguous
- *     forward of 2^32 or more elements (one kernel per channel group), and a
+ *     returns.  Four forms enqueue more, all on `stream`: a token-contiguous
+ *     forward of 2^32 or more elements (one kernel per channel group), a
  *     token-contiguous batch of several sequences with rows of at least 2048
  *     tokens (a streaming kernel, then one that rewrites each sequence's
- *     first width-1 outputs and writes its state).  Calls are therefore safe
- *     to capture in a HIP graph.
+ *     first width-1 outputs and writes its state), gdr_fwd_varlen with a
+ *     workspace, and sconv_verify_drafts (two each).  Calls are therefore
+ *     safe to capture in a HIP graph.
+ *   - A workspace is the caller's, holds nothing between calls, and must not
+ *     be shared by calls (or graph replays) that may run at once.
  *   - Return value: SCONV_OK, or a negative sconv_status.  On any error
  *     other than SCONV_ERR_LAUNCH nothing is enqueued.  An empty problem
  *     (zero tokens, zero sequences) returns SCONV_OK without enqueueing
@@ -423,7 +426,8 @@ int sconv_paged_fused_multi(int32_t num_streams,
  * state        logical [num_cache_lines][num_v_heads][head_dim_v][head_dim_k]
  *              fp32, any strides without two elements at one address.
  * num_v_heads must be a multiple of num_k_heads and head_dim_k at most 256
- *   (else SCONV_ERR_SHAPE).
+ *   (else SCONV_ERR_SHAPE), total_tokens at most 2^31 - 257, and a call's
+ *   rows of state (entries x num_v_heads x head_dim_v) below about 2^29.
  * Layouts and speed (results agree to rounding): unit channel strides with
  *   head_dim_k a multiple of 4 (decode), or head_dim_k and head_dim_v of 8
  *   (prefill), and rows aligned to 16 bytes take the vector loads; every other
