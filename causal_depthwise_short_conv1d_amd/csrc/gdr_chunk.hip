@@ -144,14 +144,22 @@ __device__ __forceinline__ f16x2 cvt2(float a, float b) {
     const f32x2v v = {a, b};
     return __builtin_convertvector(v, f16x2);
 }
-// Eight values as a high and a low fp16 part: together 22 bits.
+// A factor of 1 that the compiler does not know: x - h in fp16 is then one instruction (a multiplication and addition of
+// mixed types) instead of a conversion, a subtraction and half a conversion.
+__device__ __forceinline__ float opaque_one() {
+    float one = 1.0f;
+    asm("" : "+s"(one));
+    return one;
+}
+// ... as they are.
 __device__ __forceinline__ void split8(const float (&x)[8], f16x8 &hi, f16x8 &lo) {
+    const float one = opaque_one();
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         const f16x2 h = cvt2(x[i], x[i + 1]);
-        const f16x2 l = cvt2(fmaf(float(h.x), -1.0f, x[i]), fmaf(float(h.y), -1.0f, x[i + 1]));
         hi[i] = h.x; hi[i + 1] = h.y;
-        lo[i] = l.x; lo[i + 1] = l.y;
+        lo[i] = _Float16(fmaf(x[i], one, -float(h.x)));
+        lo[i + 1] = _Float16(fmaf(x[i + 1], one, -float(h.y)));
     }
 }
 __device__ __forceinline__ f16x8 half8(const float (&x)[8]) {
@@ -298,12 +306,13 @@ __device__ __forceinline__ f32x4 block_mfma(const f16x8 &a, const f16x4 &bh, con
     return mfma(a, b2, mfma(a, b1, c));
 }
 __device__ __forceinline__ void split4(const f32x4 &x, f16x4 &hi, f16x4 &lo) {
+    const float one = opaque_one();
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         const f16x2 h = cvt2(x[i], x[i + 1]);
-        const f16x2 l = cvt2(fmaf(float(h.x), -1.0f, x[i]), fmaf(float(h.y), -1.0f, x[i + 1]));
         hi[i] = h.x; hi[i + 1] = h.y;
-        lo[i] = l.x; lo[i + 1] = l.y;
+        lo[i] = _Float16(fmaf(x[i], one, -float(h.x)));
+        lo[i + 1] = _Float16(fmaf(x[i + 1], one, -float(h.y)));
     }
 }
 
@@ -322,12 +331,14 @@ struct Prepare {
     static constexpr int kStage = KT;  // waves
     __device__ __forceinline__ int quad_of(int lane) const { return (64 * (w & (kStage - 1)) + lane) / (4 * KT); }
 
-    __device__ __forceinline__ void stage(int32_t c0) {
+    __device__ __forceinline__ Quad load(int32_t c0) const {
         const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
-        if (w < kStage)
-            stage_quad<KT>(load_quad<VEC>(kr, sp, c0, quad, kc, p.Dk), k, cols, sh.kf, quad, kc, 1.0f, p.l2norm);
-        else if (w < 2 * kStage)
-            stage_quad<KT>(load_quad<VEC>(qr, sp, c0, quad, kc, p.Dk), q, nullptr, sh.qf, quad, kc, p.scale, p.l2norm);
+        return load_quad<VEC>(w < kStage ? kr : qr, sp, c0, quad, kc, p.Dk);
+    }
+    __device__ __forceinline__ void stage(const Quad &in) {
+        const int lane = fresh(lane0), kc = lane & (4 * KT - 1), quad = quad_of(lane);
+        if (w < kStage) stage_quad<KT>(in, k, cols, sh.kf, quad, kc, 1.0f, p.l2norm);
+        else if (w < 2 * kStage) stage_quad<KT>(in, q, nullptr, sh.qf, quad, kc, p.scale, p.l2norm);
     }
 
     // From the chunk's staged rows and its gates in LDS to its tiles.  `ahead` runs in wave 7 once the gates' place is free.
@@ -714,7 +725,8 @@ struct Consumer {
     static __device__ __forceinline__ f32x4 row4(const float *v, int t) { return *reinterpret_cast<const f32x4 *>(v + t); }
 
     // The state and the output through one chunk, in 128 registers: four waves a SIMD hide what each waits for.
-    __device__ __forceinline__ void chunk(int32_t t0, const Tiles<KT> &b) {
+    template <class F>
+    __device__ __forceinline__ void chunk(int32_t t0, const Tiles<KT> &b, F ahead) {
         const int lane = fresh(lane0), g = lane >> 4;
         f32x4 ak[4], aq[4];
 #pragma unroll
@@ -786,6 +798,8 @@ struct Consumer {
                 S[d] = mfma(k, yl, S[d]);
             }
         }
+        ahead();                                       // (the next chunk's rows are under way while the output is computed)
+        __builtin_amdgcn_sched_barrier(0x7cf);         // VMEM reads stay here
         // o
         f32x4 o[4], oi, ni;
 #pragma unroll
@@ -1030,11 +1044,13 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     if (p.state && p.has_init && p.has_init[pl.b] != 0) st.load(rows, svec);
     else st.zero();
 
+    Quad rows4 = pr.load(0);
     for (int32_t c = 0; c < nc; ++c) {
         const bool more = c + 1 < nc;
-        pr.stage(c * kC);
+        pr.stage(rows4);
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
-        if (work) st.chunk(c * kC, tiles);
+        if (work) st.chunk(c * kC, tiles, [&]() { rows4 = pr.load((c + 1) * kC); });
+        else rows4 = pr.load((c + 1) * kC);            // (rows behind the end read as zero)
         __syncthreads();
     }
     if (p.state) st.save(rows, svec);
@@ -1076,7 +1092,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
     Prepare<KT, VEC> pr{p, sh, k, q, nullptr, ht, sp, lane, wave, hk * p.group, rows_of(p.q, p.qs, sp.t0, hk),
                         rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(c * kC);
-    pr.stage(c * kC);
+    pr.stage(pr.load(c * kC));
     for (int32_t x = 0; x < p.group; ++x) {
         pr.tiles([&]() {
             if (x + 1 < p.group) {
