@@ -599,11 +599,15 @@ def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index):
         if len(ss) != 4 or ss[1] != hv or ss[2] != dv or ss[3] != dk:
             raise ValueError("state must be (lines, num_v_heads, head_dim_v, head_dim_k)")
         st = (_ptr(state, _F32, "state", dev, index), *state.stride(), ss[0])
-    ins = (_ptr(q, _BF16, "q", dev, index), *q.stride(), _ptr(k, _BF16, "k", dev, index), *k.stride(),
-           _ptr(v, _BF16, "v", dev, index), *v.stride(),
-           _ptr(g, gate, "g", dev, index), *g.stride(), _ptr(beta, gate, "beta", dev, index), *beta.stride(),
+    if not (index >= 0 and q.dtype is k.dtype is v.dtype is out.dtype is _BF16 and g.dtype is beta.dtype is gate and
+            index == k.get_device() == v.get_device() == g.get_device() == beta.get_device() == out.get_device()):
+        for t, dtype, name in ((q, _BF16, "q"), (k, _BF16, "k"), (v, _BF16, "v"), (g, gate, "g"), (beta, gate, "beta"),
+                               (out, _BF16, "out")):
+            _dev(t, dtype, name, dev)
+    ins = (q.data_ptr(), *q.stride(), k.data_ptr(), *k.stride(), v.data_ptr(), *v.stride(),
+           g.data_ptr(), *g.stride(), beta.data_ptr(), *beta.stride(),
            _ptr(A_log, _F32, "A_log", dev, index), _ptr(dt_bias, _F32, "dt_bias", dev, index), *st)
-    return (hk, hv, dk, dv), ins, (_ptr(out, _BF16, "out", dev, index), *out.stride())
+    return (hk, hv, dk, dv), ins, (out.data_ptr(), *out.stride())
 
 
 def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
@@ -737,14 +741,14 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
         if nd == 0:
             q = None
     if tokens is None:
-        tokens = torch.empty((max(batch, 0), max_drafts + 1), dtype=_I32, device=dev)
+        tokens = torch.empty_strided((max(batch, 0), max_drafts + 1), (max_drafts + 1, 1), dtype=_I32, device=dev)
     elif tokens.shape != (batch, max_drafts + 1) or tokens.stride(1) != 1:
         raise ValueError("tokens must be (batch, max_drafts + 1) with a unit inner stride")
     if num_accepted_tokens is None:
-        num_accepted_tokens = torch.empty((batch,), dtype=_I32, device=dev)
+        num_accepted_tokens = torch.empty_strided((max(batch, 0),), (1,), dtype=_I32, device=dev)
     ws_bytes = load_library().sconv_verify_workspace_bytes(batch, vocab)
     # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
-    ws = torch.empty((ws_bytes,), dtype=torch.uint8, device=dev)
+    ws = torch.empty_strided((ws_bytes,), (1,), dtype=torch.uint8, device=dev)
     _launch("sconv_verify_drafts", dev, (
         _vec(draft_tokens, _I32, "draft_tokens", dev, index, nd),
         _vec(draft_start_loc, _I32, "draft_start_loc", dev, index, batch + 1),
