@@ -83,11 +83,15 @@ constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;     // of a launch
 constexpr int kGdrThreads = 512;                               // a workgroup of the chunked kernels
 
 // Whether a call's heads are so few, and its sequences long enough, that walking prepared chunks in two kernels is
-// faster than one kernel.  Measured with 128 x 128 heads, two kernels / one: 32 heads of 2048 tokens 90 / 260 us, 128
-// heads 189 / 263, 192 heads 275 / 289, 256 heads 365 / 296; 32 heads of 256 tokens 25 / 38, of 128 tokens 21 / 23, of
-// 64 tokens 21 / 16; 128 heads of 256 tokens 42 / 40.
+// faster than one kernel: a chunk takes a walk 2.2 us and the one kernel 7.3, but twice the workgroups and a launch more
+// gain nothing where CUs are full or there is one chunk.  Measured with 128 x 128 heads, us with two kernels / one:
+//   64 tokens a sequence: 32 heads 21 / 16;  65: 16 heads 19.4 / 21.0
+//   128: 16 heads 19.5 / 21.2, 64 heads 20.7 / 22.1, 96 heads 28 / 22, 128 heads 29 / 23
+//   256: 64 heads 27 / 37, 96 heads 36.8 / 37.4, 128 heads 40.6 / 38.5
+//   2048: 32 heads 84 / 246, 128 heads 187 / 249, 160 heads 256 / 253, 192 heads 271 / 264
 inline bool gdr_few_heads(int64_t T, int64_t batch, int64_t Hv, int64_t Dv) {
-    return batch * Hv * ((Dv + 63) / 64) <= 256 && T > 128 * batch;
+    const int64_t halves = batch * Hv * ((Dv + 63) / 64);
+    return (halves <= 128 && T > 64 * batch) || (halves <= 256 && T > 256 * batch);
 }
 
 constexpr int kVfMaxSlice = 8192;      // vocabulary entries of a slice, a multiple of 1024

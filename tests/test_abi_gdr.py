@@ -36,7 +36,10 @@ def test_fwd_workspace(lib):
     assert fwd(lib, T=1000, ws=ctypes.c_void_p(BASE + 11 * GB + 8), wb=need) == EALIGN
     for x in (1, 2, 3, 4, 5, 6, 10):
         assert fwd(lib, T=1000, ws=addr(x), wb=need) == EALIAS, x
-    assert lib.gdr_fwd_workspace_bytes(2, 256, 4, 8, 64, 64, 1) == 0            # short sequences: one kernel
+    assert lib.gdr_fwd_workspace_bytes(2, 128, 4, 8, 64, 64, 1) == 0            # short sequences: one kernel
+    assert lib.gdr_fwd_workspace_bytes(2, 129, 4, 8, 64, 64, 1) > 0
+    assert lib.gdr_fwd_workspace_bytes(8, 2048, 4, 32, 64, 64, 1) == 0          # more heads: longer ones
+    assert lib.gdr_fwd_workspace_bytes(8, 2049, 4, 32, 64, 64, 1) > 0
     assert lib.gdr_fwd_workspace_bytes(2000, 10, 4, 8, 64, 64, 1) == 0          # many heads: one kernel
     assert lib.gdr_fwd_workspace_bytes(2000, 64000, 4, 8, 64, 64, 0) == 0       # short sequences, by elements
     assert lib.gdr_fwd_workspace_bytes(2000, 64001, 4, 8, 64, 64, 0) > 0
