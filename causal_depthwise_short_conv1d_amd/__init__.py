@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -36,6 +37,7 @@ __all__ = ["conv1d_fwd_varlen", "conv1d_update_decode", "conv1d_update", "sconv_
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libsconv.so")
 _lib = None
+_packed = {}              # calls of many arguments: how to pack them, and the entry that takes them so
 
 ACT_NONE, ACT_SILU = 0, 1
 
@@ -96,6 +98,13 @@ def load_library(path: str | None = None):
         *([P, I64, I64, I64, I64] * 3), *([P, I64, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
         P, I64, I64, I32, P, P, I64, I64, I32, I32, I32, I32, I32, I32, F32, I32, I32,
         P, I64, I64, I64, I64, P]
+    packed = {}
+    for f in (lib.gdr_fwd_varlen, lib.gdr_update):
+        words = getattr(lib, f.__name__ + "_packed")
+        words.argtypes, words.restype = [ctypes.c_char_p], ctypes.c_int
+        # the words of a call as bytes: a float is the low half of its word
+        pack = struct.Struct("<" + "".join("f4x" if t is F32 else "q" for t in f.argtypes)).pack
+        packed[f.__name__] = (pack, words)
     lib.sconv_verify_drafts.argtypes = [
         P, P, P, I64, P, I64, P, P, I32, I32, I32, I32, P, I64, P, P, I64, P]
     lib.sconv_verify_workspace_bytes.argtypes = [I32, I32]
@@ -106,6 +115,7 @@ def load_library(path: str | None = None):
         f.restype = ctypes.c_int
     if path is None:
         _lib = lib
+        _packed.update(packed)
     return lib
 
 
@@ -113,7 +123,7 @@ def exported_symbols() -> list[str]:
     return ["sconv_status_string", "sconv_version", "conv1d_fwd_varlen",
             "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
             "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen",
-            "gdr_fwd_workspace_bytes", "gdr_update", "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
+            "gdr_fwd_varlen_packed", "gdr_fwd_workspace_bytes", "gdr_update", "gdr_update_packed", "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
 
 
 def version() -> tuple[int, int]:
@@ -189,6 +199,20 @@ def _launch(fn: str, dev, args) -> None:
     else:
         with torch.cuda.device(dev):
             _call(fn, *args, _stream(dev))
+
+
+def _launch_packed(fn: str, dev, args) -> None:
+    """_launch for calls of some 50 arguments, which ctypes converts one by one (2.5 us of a call's 12.5): packed into
+    words, they are one argument."""
+    index = dev.index
+    if index is not None and index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch_packed(fn, dev, args)
+    load_library()
+    pack, call = _packed[fn]
+    rc = call(pack(*args, _stream(dev).value or 0))
+    if rc != 0:
+        raise SconvError(fn, rc)
 
 
 def new_output(x: torch.Tensor) -> torch.Tensor:
@@ -553,24 +577,29 @@ _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
 def _ptr(t, dtype, name, dev, index):
-    """Address of a checked tensor (None passes); the failing checks are _dev's."""
+    """Address of a checked tensor (0 for None); the failing checks are _dev's."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or index < 0 or t.get_device() != index:
         _dev(t, dtype, name, dev)
     return t.data_ptr()
 
 
 def _vec(t, dtype, name, dev, index, n):
-    """Address of a checked contiguous 1-D tensor of at least n entries."""
+    """Address of a checked contiguous 1-D tensor of at least n entries (0 for None)."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or index < 0 or t.get_device() != index or t.dim() != 1 or t.numel() < n or not t.is_contiguous():
         _index(t, dtype, name, dev, n)
     return t.data_ptr()
 
 
-def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index):
+def _no_step(s):
+    """Strides with one of a token dimension that is not there."""
+    return (s[0], 0, *s[1:])
+
+
+def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, strides=tuple):
     """Shapes (num_k_heads, num_v_heads, head_dim_k, head_dim_v) and the marshalled inputs, state and output of a call
     whose tensors have one and the same leading dimensions."""
     qs, vs = q.shape, v.shape
@@ -593,7 +622,7 @@ def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index):
             if t.dim() != 1 or t.numel() != hv or not t.is_contiguous():
                 raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
     if state is None:
-        st = (None, 0, 0, 0, 0, 0)
+        st = (0, 0, 0, 0, 0, 0)
     else:
         ss = state.shape
         if len(ss) != 4 or ss[1] != hv or ss[2] != dv or ss[3] != dk:
@@ -604,10 +633,10 @@ def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index):
         for t, dtype, name in ((q, _BF16, "q"), (k, _BF16, "k"), (v, _BF16, "v"), (g, gate, "g"), (beta, gate, "beta"),
                                (out, _BF16, "out")):
             _dev(t, dtype, name, dev)
-    ins = (q.data_ptr(), *q.stride(), k.data_ptr(), *k.stride(), v.data_ptr(), *v.stride(),
-           g.data_ptr(), *g.stride(), beta.data_ptr(), *beta.stride(),
+    ins = (q.data_ptr(), *strides(q.stride()), k.data_ptr(), *strides(k.stride()), v.data_ptr(), *strides(v.stride()),
+           g.data_ptr(), *strides(g.stride()), beta.data_ptr(), *strides(beta.stride()),
            _ptr(A_log, _F32, "A_log", dev, index), _ptr(dt_bias, _F32, "dt_bias", dev, index), *st)
-    return (hk, hv, dk, dv), ins, (out.data_ptr(), *out.stride())
+    return (hk, hv, dk, dv), ins, (out.data_ptr(), *strides(out.stride()))
 
 
 def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
@@ -644,13 +673,13 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     need = lib.gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
     # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    _launch("gdr_fwd_varlen", dev, (
+    _launch_packed("gdr_fwd_varlen", dev, (
         *ins, _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
         _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),
         _vec(query_start_loc, _I32, "query_start_loc", dev, index, 1),
         batch, total, hk, hv, dk, dv, dk ** -0.5 if scale is None else float(scale),
         1 if use_qk_l2norm else 0, pad_slot_id, o, o_tok, o_head, o_dim,
-        ws.data_ptr() if need else None, need))
+        ws.data_ptr() if need else 0, need))
     return out
 
 
@@ -671,33 +700,38 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
     index = q.get_device()
     if out is None:
         out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    ov = out
-    if q.dim() == 3:
-        if v.dim() != 3 or g.dim() != 2 or beta.dim() != 2 or out.dim() != 3:
-            raise ValueError("q, k, v, g, beta and out must all be without a token dimension, or none")
-        q, k, v, g, beta, ov = (t.unsqueeze(1) for t in (q, k, v, g, beta, out))
-    elif q.dim() != 4 or v.dim() != 4:
+    shape = q.shape
+    batch, seqlen, strides = shape[0] if shape else 0, 1, _no_step
+    if len(shape) == 4:
+        seqlen, strides = shape[1], tuple
+        if v.dim() != 4:
+            raise ValueError("q, k and v must be (batch, [seqlen,] heads, head_dim)")
+    elif len(shape) != 3:
         raise ValueError("q, k and v must be (batch, [seqlen,] heads, head_dim)")
+    elif v.dim() != 3 or g.dim() != 2 or beta.dim() != 2 or out.dim() != 3:
+        raise ValueError("q, k, v, g, beta and out must all be without a token dimension, or none")
     if state is None:
         raise ValueError("state is required")
-    batch, seqlen = q.shape[:2]
-    ci, ci_seq, ci_step, steps = cache_indices, 0, 0, 1
+    ci, ci_seq, ci_step, steps, wide = cache_indices, 0, 0, 1, False
     if ci is not None:
-        d = ci.dim()
-        if d not in (1, 2) or ci.shape[0] < batch:
+        cs = ci.shape
+        wide = len(cs) == 2
+        if not (wide or len(cs) == 1) or cs[0] < batch:
             raise ValueError("cache_indices must be (batch,) or (batch, steps)")
-        ci_seq = ci.stride(0)
-        if d == 2:
-            ci_step, steps = ci.stride(1), ci.shape[1]
-    if num_accepted_tokens is not None and (ci is None or ci.dim() != 2):
+        if wide:
+            steps = cs[1]
+            ci_seq, ci_step = ci.stride()
+        else:
+            ci_seq = ci.stride(0)
+    if num_accepted_tokens is not None and not wide:
         raise ValueError("num_accepted_tokens needs cache_indices of (batch, steps)")
     osi, osi_seq, osi_step = output_state_indices, 0, 0
     if osi is not None:
         if osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen:
             raise ValueError("output_state_indices must be (batch, >= seqlen)")
         osi_seq, osi_step = osi.stride()
-    (hk, hv, dk, dv), ins, outs = _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, ov, dev, index)
-    _launch("gdr_update", dev, (
+    (hk, hv, dk, dv), ins, outs = _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, strides)
+    _launch_packed("gdr_update", dev, (
         *ins, _ptr(ci, _I32, "cache_indices", dev, index), ci_seq, ci_step, steps,
         _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch),
         _ptr(osi, _I32, "output_state_indices", dev, index), osi_seq, osi_step,

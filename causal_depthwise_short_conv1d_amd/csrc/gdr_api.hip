@@ -2,6 +2,9 @@
 // launches.  Nothing here touches device memory or synchronises.
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <utility>
 
 #include "gdr_params.h"
 #include "sconv.h"
@@ -102,9 +105,30 @@ int32_t verify_slice(int64_t batch, int64_t vocab) {
     return int32_t(s < 1024 ? 1024 : (s > kVfMaxSlice ? kVfMaxSlice : s));
 }
 
+// The word that holds an argument, as that argument.
+template <class A>
+A from_word(const unsigned char *w) {
+    static_assert(sizeof(A) == 4 || sizeof(A) == 8, "an argument fits a word");
+    A a;                               // (little endian: a shorter one is the low half)
+    memcpy(&a, w, sizeof(A));
+    return a;
+}
+template <class... A, size_t... I>
+int call_words(int (*f)(A...), const unsigned char *w, std::index_sequence<I...>) {
+    return f(from_word<A>(w + 8 * I)...);
+}
+template <class... A>
+int call_words(int (*f)(A...), const void *words) {
+    if (!words) return SCONV_ERR_NULL;
+    return call_words(f, static_cast<const unsigned char *>(words), std::index_sequence_for<A...>{});
+}
+
 }  // namespace
 
 extern "C" {
+
+int gdr_fwd_varlen_packed(const void *words) { return call_words(gdr_fwd_varlen, words); }
+int gdr_update_packed(const void *words) { return call_words(gdr_update, words); }
 
 int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, int64_t q_stride_dim,
                    const void *k, int64_t k_stride_tok, int64_t k_stride_head, int64_t k_stride_dim,

@@ -524,6 +524,12 @@ int gdr_update(const void *q, int64_t q_stride_seq, int64_t q_stride_tok, int64_
                void *out, int64_t o_stride_seq, int64_t o_stride_tok, int64_t o_stride_head,
                int64_t o_stride_dim, hipStream_t stream);
 
+/* The two calls with their arguments in one array of 64-bit host words, in
+ * order (a float in a word's low half): for callers whose foreign calls pay for
+ * every argument.  The words are read before the call returns. */
+int gdr_fwd_varlen_packed(const void *words);
+int gdr_update_packed(const void *words);
+
 /*
  * sconv_verify_drafts -- which drafted tokens stand, and the token after them,
  * by rejection sampling from given uniform numbers in [0, 1).  Two kernels.

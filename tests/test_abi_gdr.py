@@ -15,6 +15,19 @@ def lib():
     return S.load_library()
 
 
+def status(lib, name, *args):
+    """What a call returns, packed into words or not."""
+    rc = getattr(lib, name)(*args)
+    words = (ctypes.c_uint64 * len(args))()
+    for i, (a, t) in enumerate(zip(args, getattr(lib, name).argtypes)):
+        v = t(a) if not isinstance(a, ctypes.c_void_p) else a
+        ctypes.memmove(ctypes.addressof(words) + 8 * i, ctypes.byref(v), ctypes.sizeof(v))
+    packed = getattr(lib, name + "_packed")
+    assert packed(bytes(words)) == rc
+    assert packed(None) == ENULL
+    return rc
+
+
 def fwd(lib, **kw):
     no_gpu()
     a = dict(q=addr(1), qs=(256, 64, 1), k=addr(2), ks=(256, 64, 1), v=addr(3), vs=(512, 64, 1),
@@ -22,7 +35,7 @@ def fwd(lib, **kw):
              ss=(8 * 64 * 64, 64 * 64, 64, 1), lines=4, ci=addr(7), hi=addr(8), qsl=addr(9), batch=2, T=10, hk=4,
              hv=8, dk=64, dv=64, scale=1.0, l2=1, pad=-1, o=addr(10), os=(512, 64, 1), ws=None, wb=0)
     a.update(kw)
-    return lib.gdr_fwd_varlen(a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["g"], *a["gs"], a["b"],
+    return status(lib, "gdr_fwd_varlen", a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["g"], *a["gs"], a["b"],
                               *a["bs"], a["al"], a["dt"], a["st"], *a["ss"], a["lines"], a["ci"], a["hi"], a["qsl"],
                               a["batch"], a["T"], a["hk"], a["hv"], a["dk"], a["dv"], a["scale"], a["l2"], a["pad"],
                               a["o"], *a["os"], a["ws"], a["wb"], None)
@@ -114,7 +127,7 @@ def update(lib, **kw):
              osis=(4, 1), batch=2, seqlen=4, hk=4, hv=8, dk=64, dv=64, scale=1.0, l2=0, pad=-1, o=addr(10),
              os=(2048, 512, 64, 1))
     a.update(kw)
-    return lib.gdr_update(a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["g"], *a["gs"], a["b"], *a["bs"],
+    return status(lib, "gdr_update", a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["g"], *a["gs"], a["b"], *a["bs"],
                           a["al"], a["dt"], a["st"], *a["ss"], a["lines"], a["ci"], *a["cs"], a["steps"], a["acc"],
                           a["osi"], *a["osis"], a["batch"], a["seqlen"], a["hk"], a["hv"], a["dk"], a["dv"],
                           a["scale"], a["l2"], a["pad"], a["o"], *a["os"], None)

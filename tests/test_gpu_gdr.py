@@ -85,9 +85,8 @@ def test_prefill_many_heads(dk, dv):
 
 def test_prefill_without_workspace(monkeypatch):
     """The C entry with no workspace: one kernel for layouts with vector loads, a token at a time for others."""
-    import ctypes
-    real = S._launch
-    monkeypatch.setattr(S, "_launch", lambda fn, dev, args: real(fn, dev, (*args[:-2], ctypes.c_void_p(None), 0)))
+    real = S._launch_packed
+    monkeypatch.setattr(S, "_launch_packed", lambda fn, dev, args: real(fn, dev, (*args[:-2], 0, 0)))
     prefill([70, 5, 130], 2, 4, 128, 128, seed=1)
     prefill([70, 5, 130], 2, 4, 64, 100, seed=2)
     prefill([70, 5, 130], 2, 4, 36, 24, seed=3)
@@ -441,3 +440,22 @@ def test_state_offsets_past_32_bits():
     R.check(out, ref[0], ref[1], "out")
     R.check_state(st[-1:], ref[2], ref[3])
     assert not st[:-1].any()
+
+
+def test_decode_without_a_token_dimension():
+    """(batch, heads, head_dim) inputs, sliced and transposed too, as (batch, 1, heads, head_dim) ones."""
+    d = R.on(R.draw_inputs((6, 1), 2, 4, 64, 48, 95), DEV)
+    kw = dict(A_log=d["A_log"], dt_bias=d["dt_bias"], use_qk_l2norm=True)
+    st = torch.randn(6, 4, 48, 64, device=DEV)
+    want_st = st.clone()
+    want = S.gdr_update(d["q"], d["k"], d["v"], d["g"], d["beta"], want_st, **kw)
+    flat = [d[x][:, 0] for x in ("q", "k", "v", "g", "beta")]
+    odd = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in flat]
+    for ins in (flat, odd):
+        got_st = st.clone()
+        got = S.gdr_update(*ins, got_st, **kw)
+        assert got.shape == (6, 4, 48) and torch.equal(got, want[:, 0]) and torch.equal(got_st, want_st)
+    with pytest.raises(ValueError):
+        S.gdr_update(flat[0], flat[1], d["v"], flat[3], flat[4], st, **kw)
+    with pytest.raises(ValueError):
+        S.gdr_update(flat[0], flat[1], flat[2], d["g"], flat[4], st, **kw)
