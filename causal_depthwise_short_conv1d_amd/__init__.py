@@ -760,18 +760,21 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
     dev, index = p.device, p.get_device()
     batch = draft_start_loc.numel() - 1
     nd = draft_tokens.numel()
-    if p.dim() != 2 or p.shape[0] < nd + batch:
+    shape = p.shape
+    if len(shape) != 2 or shape[0] < nd + batch:
         raise ValueError("target_probs must be (num_drafts + batch, vocab)")
-    vocab = p.shape[1]
-    if vocab > 1 and p.stride(1) != 1:
+    vocab = shape[1]
+    p_row, p_one = p.stride()
+    if vocab > 1 and p_one != 1:
         raise ValueError("target_probs must have a unit vocabulary stride")
     q_row = 0
     if q is not None:
-        if q.dim() != 2 or q.shape[0] < nd or q.shape[1] != vocab:
+        shape = q.shape
+        if len(shape) != 2 or shape[0] < nd or shape[1] != vocab:
             raise ValueError("draft_probs must be (num_drafts, vocab)")
-        if vocab > 1 and q.stride(1) != 1:
+        q_row, q_one = q.stride()
+        if vocab > 1 and q_one != 1:
             raise ValueError("draft_probs must have a unit vocabulary stride")
-        q_row = q.stride(0)
         if nd == 0:
             q = None
     if tokens is None:
@@ -786,7 +789,7 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
     _launch("sconv_verify_drafts", dev, (
         _vec(draft_tokens, _I32, "draft_tokens", dev, index, nd),
         _vec(draft_start_loc, _I32, "draft_start_loc", dev, index, batch + 1),
-        _ptr(p, _F32, "target_probs", dev, index), p.stride(0),
+        _ptr(p, _F32, "target_probs", dev, index), p_row,
         _ptr(q, _F32, "draft_probs", dev, index), q_row,
         _vec(accept_uniform, _F32, "accept_uniform", dev, index, nd),
         _vec(sample_uniform, _F32, "sample_uniform", dev, index, batch),
