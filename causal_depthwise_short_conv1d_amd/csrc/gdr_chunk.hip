@@ -13,7 +13,7 @@
 // The rule by itself is some 100 K fp32 operations a token and head, each token
 // waiting for the one before.  Here the same work is matrix products, 64 tokens
 // at a time: 64 sequences of up to 2048 tokens, 32 heads of 128 x 128, take
-// 0.76 ms where a token at a time takes 18.7 ms.
+// 0.77 ms where a token at a time takes 18.7 ms.
 //
 // One kernel (many heads).  A workgroup of 8 waves owns 128 value channels of
 // one head and walks its sequence.  Per chunk it prepares the operands in LDS
@@ -22,14 +22,16 @@
 // registers.  Two workgroups share a CU (128 registers, 79 KB), so that one's
 // matrix products run beside the other's conversions and waits: 1.07 ms, where
 // waves that only prepare beside waves that only consume, one workgroup a CU,
-// took 1.21.  What bounds it now is the VALU, 73 % busy with conversions,
-// scaling and addresses (1200 instructions a wave and chunk), beside the MFMAs
-// (29 %); bytes alone would take 0.34 ms.
+// took 1.21.  What bounds it now: a chunk is a chain of phases, 8.7 us for a
+// workgroup alone on its CU and 11.9 for two sharing it, with the VALU 70 %
+// busy (conversions, scaling, addresses: 1200 instructions a wave and chunk)
+// and the MFMAs 28 %; a twentieth less VALU work alone changes nothing.  Bytes
+// would take 0.34 ms.
 //
 // Two kernels (few heads): a walk is a chain of chunks, so everything that does
 // not depend on the state is prepared before it by the whole chip.  At 4195
-// tokens, 32 heads: 29 us and 143 us for 66 chunks, 2.2 us each, half of it
-// MFMAs that wait for one another; at 14807 tokens 75 and 475 us.
+// tokens, 32 heads: 29 us and 141 us for 66 chunks, 2.1 us each, a chain of
+// products and of the conversions between them; at 14807 tokens 75 and 463 us.
 //
 // Waves of one state never exchange anything: an MFMA result has its channel in
 // the lane and 4 rows a register quad, and the next product takes it as its
@@ -1047,8 +1049,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
     Quad rows4 = pr.load(0);
     for (int32_t c = 0; c < nc; ++c) {
         const bool more = c + 1 < nc;
+        // The preparation's waves, few at a time and one chain, go before the other workgroup's products: 204 us for 384
+        // workgroups of 16 chunks (215), 1 % where the chip is full.
+        __builtin_amdgcn_s_setprio(2);
         pr.stage(rows4);
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
+        __builtin_amdgcn_s_setprio(0);
         if (work) st.chunk(c * kC, tiles, [&]() { rows4 = pr.load((c + 1) * kC); });
         else rows4 = pr.load((c + 1) * kC);            // (rows behind the end read as zero)
         __syncthreads();
