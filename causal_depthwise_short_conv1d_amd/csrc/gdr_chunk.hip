@@ -1074,13 +1074,14 @@ __device__ __forceinline__ int64_t first_slot(const GdrParams &p, int32_t b) {
     return (a >> 6) + b;
 }
 
-// A workgroup prepares one chunk of one key head, for all the value heads that share it.
+// A workgroup prepares one chunk of one key head, for `per` of the value heads that share it.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, HeadTiles *heads) {
+__global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p, HeadTiles *heads, int32_t per) {
     __shared__ _Float16 k[4 * KT * kTile], q[4 * KT * kTile];
     __shared__ Scratch sh;
-    const int64_t slot = blockIdx.x / uint32_t(p.Hk);
-    const int32_t hk = int32_t(blockIdx.x - uint32_t(slot) * uint32_t(p.Hk));
+    const uint32_t units = uint32_t(p.Hv / per);
+    const int64_t slot = blockIdx.x / units;
+    const int32_t h0 = int32_t(blockIdx.x - uint32_t(slot) * units) * per, hk = h0 / p.group;
     int32_t lo = 0, hi = p.batch - 1;                              // the last sequence whose slots start at or before
     while (lo < hi) {
         const int32_t mid = (lo + hi + 1) >> 1;
@@ -1094,19 +1095,19 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
     const int32_t c = int32_t(chunk);
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    HeadTiles *ht = heads + slot * p.Hv + hk * p.group;
-    Prepare<KT, VEC> pr{p, sh, k, q, nullptr, ht, sp, lane, wave, hk * p.group, rows_of(p.q, p.qs, sp.t0, hk),
+    HeadTiles *ht = heads + slot * p.Hv + h0;
+    Prepare<KT, VEC> pr{p, sh, k, q, nullptr, ht, sp, lane, wave, h0, rows_of(p.q, p.qs, sp.t0, hk),
                         rows_of(p.k, p.ks, sp.t0, hk)};
     if (wave == 7) pr.gates(c * kC);
     pr.stage(pr.load(c * kC));
-    for (int32_t x = 0; x < p.group; ++x) {
+    for (int32_t x = 0; x < per; ++x) {
         pr.tiles([&]() {
-            if (x + 1 < p.group) {
+            if (x + 1 < per) {
                 ++pr.h;
                 pr.gates(c * kC);
             }
         });
-        pr.h = hk * p.group + x + 1;
+        pr.h = h0 + x + 1;
         ++pr.ht;
     }
 }
@@ -1204,11 +1205,23 @@ hipError_t launch_one(const GdrParams &p, bool svec, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Value heads that a preparing workgroup takes one after the other: they share the rows' conversion, but a call of few
+// workgroups is over sooner when each takes fewer.  As many as leave two workgroups a CU: 32 heads and 7, 19, 35, 68
+// and 131 chunks took 9, 13, 19, 33 and 54 us with one (of 8) together, 12, 15, 17, 30 and 44 with two, 17, 20, 19, 30 and
+// 42 with four, 27, 29, 29, 39 and 43 with eight.
+int32_t heads_together(const GdrParams &p, int64_t slots) {
+    int32_t per = p.group;
+    if (per > 64) return per;          // (and no launch grows past the host's check)
+    while (per > 1 && (p.group % per || slots * (p.Hv / per) < 512)) --per;
+    return per;
+}
+
 template <int KT, bool VEC>
 hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream_t s) {
     const int64_t slots = gdr_slots(p.total_T, p.batch);
     HeadTiles *heads = static_cast<HeadTiles *>(workspace);
-    gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * p.Hk)), dim3(64 * kWaves), 0, s>>>(p, heads);
+    const int32_t per = heads_together(p, slots);
+    gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * (p.Hv / per))), dim3(64 * kWaves), 0, s>>>(p, heads, per);
     const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
     gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
         p, heads, groups, svec);

@@ -459,3 +459,9 @@ def test_decode_without_a_token_dimension():
         S.gdr_update(flat[0], flat[1], d["v"], flat[3], flat[4], st, **kw)
     with pytest.raises(ValueError):
         S.gdr_update(flat[0], flat[1], flat[2], d["g"], flat[4], st, **kw)
+
+
+@pytest.mark.parametrize("hk,hv,lens", [(1, 8, [130]), (1, 6, [4100]), (2, 12, [700, 500]), (1, 3, [12000]), (1, 7, [90])])
+def test_prefill_head_groups_prepared_together(hk, hv, lens):
+    """Few and many chunks of groups of 2, 3, 6, 7 and 8 value heads."""
+    prefill(lens, hk, hv, 64, 16, seed=hv)
