@@ -85,10 +85,10 @@ constexpr int kGdrThreads = 512;                               // a workgroup of
 // Whether a call's heads are so few, and its sequences long enough, that walking prepared chunks in two kernels is
 // faster than one kernel: a chunk takes a walk 2.2 us and the one kernel 7.3, but twice the workgroups and a launch more
 // gain nothing where CUs are full or there is one chunk.  Measured with 128 x 128 heads, us with two kernels / one:
-//   64 tokens a sequence: 32 heads 21 / 16;  65: 16 heads 19.4 / 21.0
-//   128: 16 heads 19.5 / 21.2, 64 heads 20.7 / 22.1, 96 heads 28 / 22, 128 heads 29 / 23
-//   256: 64 heads 27 / 37, 96 heads 36.8 / 37.4, 128 heads 40.6 / 38.5
-//   2048: 32 heads 84 / 246, 128 heads 187 / 249, 160 heads 256 / 253, 192 heads 271 / 264
+//   64 tokens a sequence: 32 heads 16.0 / 14.0;  65: 16 heads 16.7 / 20.8
+//   128: 16 heads 16.9 / 21.2, 64 heads 18.9 / 22.1, 96 heads 27 / 22, 128 heads 30 / 23
+//   256: 64 heads 25 / 36, 96 heads 37.8 / 37.3, 128 heads 40.4 / 38.0;  320: 96 heads 43.5 / 45.4, 128 heads 44.9 / 45.7
+//   2048: 32 heads 84 / 245, 128 heads 188 / 247, 160 heads 257 / 251, 192 heads 277 / 264
 inline bool gdr_few_heads(int64_t T, int64_t batch, int64_t Hv, int64_t Dv) {
     const int64_t halves = batch * Hv * ((Dv + 63) / 64);
     return (halves <= 128 && T > 64 * batch) || (halves <= 256 && T > 256 * batch);
