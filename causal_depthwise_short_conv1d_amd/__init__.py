@@ -594,38 +594,35 @@ def _vec(t, dtype, name, dev, index, n):
     return t.data_ptr()
 
 
-def _no_step(s):
-    """Strides with one of a token dimension that is not there."""
-    return (s[0], 0, *s[1:])
-
-
-def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, strides=tuple):
+def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, step=True):
     """Shapes (num_k_heads, num_v_heads, head_dim_k, head_dim_v) and the marshalled inputs, state and output of a call
-    whose tensors have one and the same leading dimensions."""
+    whose tensors have one and the same leading dimensions.  Without `step`, they lack the token dimension that the call
+    has: its strides are 0."""
     qs, vs = q.shape, v.shape
+    tokens = vs[:-1]
     if k.shape != qs or vs[:-2] != qs[:-2]:
         raise ValueError("q and k need one shape, and v the same tokens")
     hk, dk = qs[-2:]
     hv, dv = vs[-2:]
     if hk < 1 or hv % hk:
         raise ValueError("v's heads must be a multiple of q's")
-    if g.shape != vs[:-1] or beta.shape != vs[:-1]:
+    if g.shape != tokens or beta.shape != tokens:
         raise ValueError("g and beta need one value per token and value head")
     if out.shape != vs:
         raise ValueError("out must have v's shape")
-    gate = _F32
+    gate, layer = _F32, (0, 0)
     if A_log is not None or dt_bias is not None:
         if A_log is None or dt_bias is None:
             raise ValueError("A_log and dt_bias go together")
-        gate = _BF16
-        for t in (A_log, dt_bias):
-            if t.dim() != 1 or t.numel() != hv or not t.is_contiguous():
-                raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
+        gate, one = _BF16, (hv,)
+        if A_log.shape != one or dt_bias.shape != one or not (A_log.is_contiguous() and dt_bias.is_contiguous()):
+            raise ValueError("A_log and dt_bias must be contiguous (num_v_heads,) tensors")
+        layer = (_ptr(A_log, _F32, "A_log", dev, index), _ptr(dt_bias, _F32, "dt_bias", dev, index))
     if state is None:
         st = (0, 0, 0, 0, 0, 0)
     else:
         ss = state.shape
-        if len(ss) != 4 or ss[1] != hv or ss[2] != dv or ss[3] != dk:
+        if ss[1:] != (hv, dv, dk):
             raise ValueError("state must be (lines, num_v_heads, head_dim_v, head_dim_k)")
         st = (_ptr(state, _F32, "state", dev, index), *state.stride(), ss[0])
     if not (index >= 0 and q.dtype is k.dtype is v.dtype is out.dtype is _BF16 and g.dtype is beta.dtype is gate and
@@ -633,10 +630,15 @@ def _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, strid
         for t, dtype, name in ((q, _BF16, "q"), (k, _BF16, "k"), (v, _BF16, "v"), (g, gate, "g"), (beta, gate, "beta"),
                                (out, _BF16, "out")):
             _dev(t, dtype, name, dev)
-    ins = (q.data_ptr(), *strides(q.stride()), k.data_ptr(), *strides(k.stride()), v.data_ptr(), *strides(v.stride()),
-           g.data_ptr(), *strides(g.stride()), beta.data_ptr(), *strides(beta.stride()),
-           _ptr(A_log, _F32, "A_log", dev, index), _ptr(dt_bias, _F32, "dt_bias", dev, index), *st)
-    return (hk, hv, dk, dv), ins, (out.data_ptr(), *strides(out.stride()))
+    if step:
+        ins = (q.data_ptr(), *q.stride(), k.data_ptr(), *k.stride(), v.data_ptr(), *v.stride(), g.data_ptr(), *g.stride(),
+               beta.data_ptr(), *beta.stride(), *layer, *st)
+        return (hk, hv, dk, dv), ins, (out.data_ptr(), *out.stride())
+    ins = []
+    for t in (q, k, v, g, beta, out):
+        first, *rest = t.stride()
+        ins += (t.data_ptr(), first, 0, *rest)
+    return (hk, hv, dk, dv), (*ins[:-5], *layer, *st), ins[-5:]
 
 
 def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
@@ -672,7 +674,7 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     lib = load_library()
     need = lib.gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
     # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
-    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
     _launch_packed("gdr_fwd_varlen", dev, (
         *ins, _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
         _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),
@@ -701,9 +703,9 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
     if out is None:
         out = torch.empty(v.shape, dtype=v.dtype, device=dev)
     shape = q.shape
-    batch, seqlen, strides = shape[0] if shape else 0, 1, _no_step
+    batch, seqlen, step = shape[0] if shape else 0, 1, False
     if len(shape) == 4:
-        seqlen, strides = shape[1], tuple
+        seqlen, step = shape[1], True
         if v.dim() != 4:
             raise ValueError("q, k and v must be (batch, [seqlen,] heads, head_dim)")
     elif len(shape) != 3:
@@ -730,7 +732,7 @@ def gdr_update(q, k, v, g, beta, state, cache_indices=None, num_accepted_tokens=
         if osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen:
             raise ValueError("output_state_indices must be (batch, >= seqlen)")
         osi_seq, osi_step = osi.stride()
-    (hk, hv, dk, dv), ins, outs = _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, strides)
+    (hk, hv, dk, dv), ins, outs = _gdr_tensors(q, k, v, g, beta, A_log, dt_bias, state, out, dev, index, step)
     _launch_packed("gdr_update", dev, (
         *ins, _ptr(ci, _I32, "cache_indices", dev, index), ci_seq, ci_step, steps,
         _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch),
