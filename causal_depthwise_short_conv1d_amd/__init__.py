@@ -123,7 +123,8 @@ def exported_symbols() -> list[str]:
     return ["sconv_status_string", "sconv_version", "conv1d_fwd_varlen",
             "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
             "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen",
-            "gdr_fwd_varlen_packed", "gdr_fwd_workspace_bytes", "gdr_update", "gdr_update_packed", "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
+            "gdr_fwd_varlen_packed", "gdr_fwd_workspace_bytes", "gdr_update", "gdr_update_packed",
+            "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
 
 
 def version() -> tuple[int, int]:

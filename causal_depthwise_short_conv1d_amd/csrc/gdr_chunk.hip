@@ -1114,7 +1114,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_prepare_kernel(GdrParams p
 
 constexpr int kWalkers = 2;            // state waves of a walking workgroup
 constexpr int kLoaders = 4;
-static_assert(64 * (2 * kWalkers + kLoaders) == kGdrThreads, "the host's launch checks");
+constexpr int kWalkWaves = 2 * kWalkers + kLoaders;
+static_assert(64 * kWalkWaves == kGdrThreads, "the host's launch checks");
 
 // Walks a sequence over prepared tiles: four waves bring the next chunk's through registers into one of two buffers (and
 // convert its keys and queries again, which costs less than their tiles in memory: 168 against 192 us at 4195 tokens),
@@ -1122,7 +1123,7 @@ static_assert(64 * (2 * kWalkers + kLoaders) == kGdrThreads, "the host's launch 
 // state waves ask more of the LDS than it gives, 174 against 150 us at 4195 tokens; one, with
 // twice the workgroups, saves 2 % of the whole and is slower where these fill the chip.
 template <int KT, bool VEC>
-__global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLoaders) / 4) void gdr_walk_kernel(GdrParams p, const HeadTiles *heads,
+__global__ __launch_bounds__(64 * kWalkWaves, kWalkWaves / 4) void gdr_walk_kernel(GdrParams p, const HeadTiles *heads,
                                                                                    int32_t groups, bool svec) {
     __shared__ Tiles<KT> buf[2];
     __shared__ Exchange<KT> exchange[kWalkers];
@@ -1201,7 +1202,8 @@ __global__ __launch_bounds__(64 * (2 * kWalkers + kLoaders), (2 * kWalkers + kLo
 template <int KT>
 hipError_t launch_one(const GdrParams &p, bool svec, hipStream_t s) {
     const int32_t groups = (p.Dv + 16 * kWaves - 1) / (16 * kWaves);
-    gdr_chunk_kernel<KT, true><<<dim3(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups))), dim3(64 * kWaves), 0, s>>>(p, groups, svec);
+    const dim3 grid(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups)));
+    gdr_chunk_kernel<KT, true><<<grid, dim3(64 * kWaves), 0, s>>>(p, groups, svec);
     return hipGetLastError();
 }
 
@@ -1223,8 +1225,8 @@ hipError_t launch_walk(const GdrParams &p, bool svec, void *workspace, hipStream
     const int32_t per = heads_together(p, slots);
     gdr_prepare_kernel<KT, VEC><<<dim3(uint32_t(slots * (p.Hv / per))), dim3(64 * kWaves), 0, s>>>(p, heads, per);
     const int32_t groups = (p.Dv + 16 * kWalkers - 1) / (16 * kWalkers);
-    gdr_walk_kernel<KT, VEC><<<dim3(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups))), dim3(64 * (2 * kWalkers + kLoaders)), 0, s>>>(
-        p, heads, groups, svec);
+    const dim3 grid(uint32_t(gdr_walk_grid(p.batch, p.Hk, p.Hv, groups)));
+    gdr_walk_kernel<KT, VEC><<<grid, dim3(64 * kWalkWaves), 0, s>>>(p, heads, groups, svec);
     return hipGetLastError();
 }
 
