@@ -47,6 +47,7 @@
 // and a single fp16 operand would leave the state at 11 bits.  The output is
 // bf16, so the products that only feed it take single fp16 operands.
 #include "gdr_device.h"
+#include "gdr_units.h"
 
 namespace sconv {
 
@@ -113,10 +114,8 @@ __device__ __forceinline__ int in_tile(int r, int c) { return (r + 16 * (c >> 3)
 __device__ __forceinline__ int swz_rows(int r, int g, int kt) { return r ^ (g + 4 * (kt & 1)); }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }   // -126..127
-__device__ __forceinline__ int exp_of(float m) {       // m in [2^(e-1), 2^e), held to -100..127
-    int e = __builtin_amdgcn_frexp_expf(m);
-    e = e < -100 ? -100 : (e > 127 ? 127 : e);
-    return m == 0.0f ? -100 : e;
+__device__ __forceinline__ int exp_of(float m) {       // m in [2^(e-1), 2^e)
+    return m == 0.0f ? kMinExp : held_exp(__builtin_amdgcn_frexp_expf(m));
 }
 
 // The lane number anew, as a value that the compiler takes for unknown: what is computed from it stays in its phase.
@@ -603,7 +602,7 @@ struct Consumer {
             for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(S[d][i]));
         });
         m = max_groups(m);
-        un = m == 0.0f ? 0 : 14 - exp_of(m);
+        un = m == 0.0f ? 0 : first_unit(exp_of(m));
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d) S[d] *= pow2(un);
     }
@@ -643,8 +642,8 @@ struct Consumer {
         }
     }
     // The identity as a right operand, times the column's unit (a power of two, within bf16's range).
-    __device__ __forceinline__ bf16x8 identity(int lane) const {
-        const uint32_t one = uint32_t(un + 127) << 7;
+    static __device__ __forceinline__ bf16x8 identity(int lane, int unit) {
+        const uint32_t one = uint32_t(unit + 127) << 7;
         u32x4 r;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -692,13 +691,30 @@ struct Consumer {
 #pragma unroll
             for (int i = 0; i < 4; ++i) zm = fmaxf(zm, fabsf(z[mt][i]));
         const float bound = max_groups(fmaf(zm * pow2(xe - 12), 128.0f, ms * last));
-        int up = 14 - exp_of(bound);
-        up = up < -126 - un ? -126 - un : (up > 126 - un ? 126 - un : up);
-        up = up < -114 ? -114 : up;
-        int zu = xe - 12 + up;
-        zu = zu < -126 ? -126 : (zu > 126 ? 126 : zu);
-        un += up;
-        return {pow2(zu), last * pow2(up), pow2(-un)};
+        const UnitStep st = sconv::next_unit(un, bound == 0.0f, exp_of(bound), xe);
+        un += st.up;
+        return {pow2(st.zu), last * pow2(st.up), pow2(-un)};
+    }
+    // A column whose unit is high (its state is small) takes one that its chunk's values allow; v: those values.  Hardly any
+    // chunk has such a column.
+    __device__ __forceinline__ bool high_unit() const { return __builtin_amdgcn_ballot_w64(un > kPlainUnit) != 0; }
+    __device__ __forceinline__ void lower_unit(const u32x4 (&v)[4]) {
+        const int lane = fresh(lane0);
+        const bf16x8 id = identity(lane, 0);
+        float m = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const f32x4 vv = values(v[mt], id);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(vv[i]));
+        }
+        m = max_groups(m);
+        const int to = un > kPlainUnit ? unit_for_values(un, exp_of(m)) : un;
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[d][i] = ldexpf(S[d][i], to - un);
+        un = to;
     }
     __device__ __forceinline__ void split_state(int kt, f16x8 &hi, f16x8 &lo) const {
         float f[8];
@@ -751,7 +767,7 @@ struct Consumer {
         }
         // X, scaled to 2^12
         float x[16], xm = 0.0f;
-        const bf16x8 id = identity(lane);
+        const bf16x8 id = identity(lane, un);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             const f32x4 ka = row4(b.ka, tok_of(mt, 4 * g)), kb = row4(b.kb, tok_of(mt, 4 * g)), vv = values(v[mt], id);
@@ -820,6 +836,7 @@ struct Consumer {
     // The state alone through one chunk, one wave a SIMD: what a product needs beside the last one's result is read and
     // computed before that result is there.  v comes in and goes out with the next chunk's.
     __device__ __forceinline__ void advance(int32_t t0, const Tiles<KT> &b, u32x4 (&v)[4], Exchange<KT> *ex, int *ready) {
+        if (high_unit()) lower_unit(v);
         const int lane = fresh(lane0), g = lane >> 4;
         f16x8 sh[KT], sl[KT];
 #pragma unroll
@@ -842,7 +859,7 @@ struct Consumer {
         }
         hand_over(ready);
         f32x4 ka[4], xv[4];
-        const bf16x8 id = identity(lane);
+        const bf16x8 id = identity(lane, un);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             ka[mt] = row4(b.ka, tok_of(mt, 4 * g));
@@ -1053,6 +1070,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gdr_chunk_kernel(GdrParams p, 
         // workgroups of 16 chunks (215), 1 % where the chip is full.
         __builtin_amdgcn_s_setprio(2);
         pr.stage(rows4);
+        if (work && st.high_unit()) {                  // (here it costs nothing; before the products 2 to 4 %)
+            u32x4 v[4];
+            st.fetch(c * kC, v);
+            st.lower_unit(v);
+        }
         pr.tiles([&]() { if (more) pr.gates((c + 1) * kC); });
         __builtin_amdgcn_s_setprio(0);
         if (work) st.chunk(c * kC, tiles, [&]() { rows4 = pr.load((c + 1) * kC); });

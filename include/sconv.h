@@ -454,7 +454,8 @@ int sconv_paged_fused_multi(int32_t num_streams,
  *     rule to be stable at all; the inverse below it leaves fp16 far above;
  *   - an infinity or NaN in a token may reach the other tokens of its chunk,
  *     sequence and head, earlier ones too;
- *   - a value channel is held to about 2^-26 of its largest value in the chunk.
+ *   - a value channel is held to about 2^-26 of its largest value in the chunk;
+ *   - values, and beta |k| times them, may be as large as 2^80 (beta |k|: 2^20).
  * workspace    device memory, 16-byte aligned, in use until the call's work is
  *              done, or NULL.  With gdr_fwd_workspace_bytes() bytes of it, calls
  *              of few heads take two kernels (all chunks are prepared at once,
