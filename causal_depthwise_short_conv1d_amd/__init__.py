@@ -114,8 +114,8 @@ def load_library(path: str | None = None):
               lib.gdr_fwd_varlen, lib.gdr_update, lib.sconv_verify_drafts):
         f.restype = ctypes.c_int
     if path is None:
+        _packed.update(packed)        # before _lib: another thread's call looks there once it finds the library
         _lib = lib
-        _packed.update(packed)
     return lib
 
 
