@@ -657,7 +657,11 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     place; query_start_loc int32 (batch+1,), cache_indices int32 (batch,) or
     None, has_initial_state bool (batch,) or None: as for conv1d_fwd_varlen.
     scale defaults to head_dim_k ** -0.5.  Returns out (T, num_v_heads,
-    head_dim_v); rows of padded sequences are left as they are."""
+    head_dim_v); rows of padded sequences are left as they are.
+    Calls of few heads, and layouts without vector loads, take a workspace for
+    the time of the call: 19.3 KiB * (T / 64 + batch + 2) * num_v_heads, 1.3 GB
+    for 131072 tokens of 32 heads.  Where memory for it is short, a call takes a
+    slower form that needs none."""
     dev = q.device
     index = q.get_device()
     if q.dim() != 3 or v.dim() != 3:
@@ -675,7 +679,10 @@ def gdr_fwd_varlen(q, k, v, g, beta, state, query_start_loc, cache_indices=None,
     lib = load_library()
     need = lib.gdr_fwd_workspace_bytes(batch, total, hk, hv, dk, dv, vector)
     # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
-    ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
+    try:
+        ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
+    except torch.OutOfMemoryError:
+        need = 0                  # (the forms that take none are slower, and right)
     _launch_packed("gdr_fwd_varlen", dev, (
         *ins, _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
         _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),

@@ -462,7 +462,9 @@ int sconv_paged_fused_multi(int32_t num_streams,
  *              then walked), which is up to three times as fast for them, and
  *              layouts without vector loads can be processed in chunks; without
  *              it these go a token at a time.  Smaller than asked for ->
- *              SCONV_ERR_SHAPE.
+ *              SCONV_ERR_SHAPE.  It grows with the call: 19728 bytes *
+ *              (total_tokens / 64 + batch + 2) * num_v_heads, 1.3 GB for 131072
+ *              tokens of 32 heads; a caller short of memory passes NULL.
  */
 int gdr_fwd_varlen(const void *q, int64_t q_stride_tok, int64_t q_stride_head, int64_t q_stride_dim,
                    const void *k, int64_t k_stride_tok, int64_t k_stride_head, int64_t k_stride_dim,
