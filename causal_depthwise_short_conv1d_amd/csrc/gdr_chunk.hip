@@ -72,6 +72,12 @@ constexpr int kTile = 512;             // halves per tile
 __device__ __forceinline__ constexpr int tri_tile(int mt, int tt) { return mt < 2 ? mt : 2 + 2 * (mt - 2) + tt; }
 constexpr int kTriTiles = 6;
 
+// What decays between two tokens is small, and fp16 has no step below 2^-24: the triangles are held times powers of two.  A
+// and T, 4 at most where the rule contracts, have steps of 2^-30 so (and 2^10 is left above them where it hardly does); P,
+// at most 2.25, of 2^-38.
+constexpr float kTriScale = 1 << kTriExp, kTriInv = 1.0f / kTriScale;
+constexpr float kPScale = 1 << 14;
+
 template <int KT>
 struct alignas(16) KeyTiles {          // of a chunk's keys and queries
     _Float16 k[4 * KT * kTile];        // [mt][kt] rows tokens
@@ -79,13 +85,13 @@ struct alignas(16) KeyTiles {          // of a chunk's keys and queries
     _Float16 kt[4 * KT * kTile];       // [2 KT channel tiles][2] rows key channels, columns tokens
 };
 struct alignas(16) HeadTiles {         // ... with a value head's gates
-    _Float16 th[kTriTiles * kTile];    // T, high and low parts
+    _Float16 th[kTriTiles * kTile];    // T kTriScale, high and low parts
     _Float16 tl[kTriTiles * kTile];
-    _Float16 p[kTriTiles * kTile];     // e^(Gi - Gj) q16.k16
+    _Float16 p[kTriTiles * kTile];     // e^(Gi - Gj) q16.k16 kPScale
     float kb[kC];                      // kf beta
     float ka[kC];                      // kf beta e^G kf
     float eg[kC];                      // e^(G_last - G)
-    float qf[kC];
+    float qf[kC];                      // qf / kPScale
     float qe[kC];                      // qf e^G
     float last;                        // e^G_last
 };
@@ -93,8 +99,8 @@ template <int KT>
 struct Tiles : KeyTiles<KT>, HeadTiles {};
 
 struct alignas(16) Scratch {           // of the preparation
-    _Float16 off[6 * kTile];           // A's blocks below the diagonal: [4 rows / 4][column]: 4 high, 4 low parts
-    float diag[4 * 256];               // A's diagonal blocks by columns, then T's
+    _Float16 off[6 * kTile];           // A's blocks below the diagonal, times kTriScale: [4 rows / 4][column]: 4 high, 4 low parts
+    float diag[4 * 256];               // A's diagonal blocks by columns, then T's, times kTriScale
     float dump[4];                     // for what lies in neither
     float Gh[kC], Gl[kC];              // running log decay, in powers of 2: high and low parts
     float beta[kC], eG[kC], eg[kC], kf[kC], qf[kC];
@@ -388,7 +394,7 @@ struct Prepare {
     __device__ __forceinline__ void factors() {
         const int lane = fresh(lane0);
         const float kf = sh.kf[lane], qf = sh.qf[lane], eG = sh.eG[lane], kb = kf * sh.beta[lane];
-        ht->qf[lane] = qf;
+        ht->qf[lane] = qf * (1.0f / kPScale);
         ht->kb[lane] = kb;
         ht->ka[lane] = kb * eG * kf;
         ht->eg[lane] = sh.eg[lane];
@@ -427,7 +433,7 @@ struct Prepare {
             const f32x4 kf = *reinterpret_cast<const f32x4 *>(sh.kf + ti);
             const f32x4 a = *reinterpret_cast<const f32x4 *>(sh.beta + ti) * kf * kf * decay<false>(ti, tj) * kk;
             f16x4 hi, lo;
-            split4(a, hi, lo);
+            split4(a * kTriScale, hi, lo);
             _Float16 *op = bi > bj ? sh.off + (bi * (bi - 1) / 2 + bj) * kTile + ((tj & 15) + 4 * (ti & 12)) * 8
                                    : reinterpret_cast<_Float16 *>(sh.dump);
             *reinterpret_cast<f16x8 *>(op) = f16x8{hi[0], hi[1], hi[2], hi[3], lo[0], lo[1], lo[2], lo[3]};
@@ -456,7 +462,7 @@ struct Prepare {
             const f32x4 d = decay<true>(tj, ti);
             float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = tj + i <= ti ? d[i] * qk[x][i] : 0.0f;
+            for (int i = 0; i < 4; ++i) v[i] = tj + i <= ti ? d[i] * (qk[x][i] * kPScale) : 0.0f;
             const f16x2 lo = cvt2(v[0], v[1]), hi = cvt2(v[2], v[3]);
             *reinterpret_cast<f16x4 *>(ht->p + tri_tile(mt, nt >> 1) * kTile + in_tile(n, tj & 31)) =
                 f16x4{lo.x, lo.y, hi.x, hi.y};
@@ -477,7 +483,8 @@ struct Prepare {
         }
         substitute<0>(a, x);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) *reinterpret_cast<f32x4 *>(blk + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+        for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<f32x4 *>(blk + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]} * kTriScale;
     }
     // x[j] is final: takes it out of the rows below.
     template <int J>
@@ -525,8 +532,8 @@ struct Prepare {
                 for (int k = 3; k >= 0; --k)
                     if (k > j && k <= w) m = block_mfma(off[k * (k - 1) / 2 + j], hi[k], lo[k], m);
                 f16x4 mh, ml;
-                split4(m, mh, ml);
-                t = block_mfma(left[j < 3 ? j : 0], mh, ml, f32x4{0, 0, 0, 0});
+                split4(m * kTriInv, mh, ml);
+                t = block_mfma(left[j < 3 ? j : 0], mh, ml, f32x4{0, 0, 0, 0}) * kTriInv;
             }
             split4(t, hi[j], lo[j]);
             const int tj = 16 * j + 4 * g;
@@ -682,7 +689,7 @@ struct Consumer {
     }
 
     // The units of the next state: 2^14 above a bound of it (64 tokens, |k16| < 1.5, so the chunk adds at most 2^7 max |z|
-    // to what is left of the last one).  z comes in its own unit, 2^(xe - 12) of the state's.
+    // to what is left of the last one).  z comes in its own unit, 2^(xe - kZExp) of the state's.
     struct Units { float zs, sc, ninv; };
     __device__ __forceinline__ Units next_unit(const f32x4 (&z)[4], float ms, float last, int xe) {
         float zm = 0.0f;
@@ -690,7 +697,7 @@ struct Consumer {
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) zm = fmaxf(zm, fabsf(z[mt][i]));
-        const float bound = max_groups(fmaf(zm * pow2(xe - 12), 128.0f, ms * last));
+        const float bound = max_groups(fmaf(zm * pow2(xe - kZExp), 128.0f, ms * last));
         const UnitStep st = sconv::next_unit(un, bound == 0.0f, exp_of(bound), xe);
         un += st.up;
         return {pow2(st.zu), last * pow2(st.up), pow2(-un)};
@@ -765,7 +772,7 @@ struct Consumer {
                 ak[mt] = mfma(kf, lo, ak[mt]);
             }
         }
-        // X, scaled to 2^12
+        // X, scaled to 2^kXExp
         float x[16], xm = 0.0f;
         const bf16x8 id = identity(lane, un);
 #pragma unroll
@@ -777,8 +784,8 @@ struct Consumer {
                 xm = fmaxf(xm, fabsf(x[4 * mt + i]));
             }
         }
-        const int xe = exp_of(max_groups(xm));
-        const float xs = pow2(12 - xe);
+        const int xe = x_exp(exp_of(max_groups(xm)));
+        const float xs = pow2(kXExp - xe);
         // z = T X
         f32x4 z[4];
 #pragma unroll
@@ -869,7 +876,7 @@ struct Consumer {
 #pragma unroll
         for (int i = 0; i < kTriTiles; ++i) { th[i] = tile_of(b.th, i, lane); tl[i] = tile_of(b.tl, i, lane); }
         __builtin_amdgcn_sched_barrier(0);
-        // X, scaled to 2^12
+        // X, scaled to 2^kXExp
         float xm = 0.0f;
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -878,8 +885,8 @@ struct Consumer {
                 xv[mt][i] = fmaf(-ka[mt][i], ak[mt][i], xv[mt][i]);
                 xm = fmaxf(xm, fabsf(xv[mt][i]));
             }
-        const int xe = exp_of(max_groups(xm));
-        const float xs = pow2(12 - xe);
+        const int xe = x_exp(exp_of(max_groups(xm)));
+        const float xs = pow2(kXExp - xe);
         // z = T X
         f32x4 z[4];
 #pragma unroll

@@ -11,6 +11,11 @@ namespace sconv {
 constexpr int kMinExp = -112, kMaxExp = 127;
 __host__ __device__ inline int held_exp(int e) { return e < kMinExp ? kMinExp : (e > kMaxExp ? kMaxExp : e); }
 
+// A and T are held times 2^kTriExp, X is scaled to 2^kXExp by its own exponent xe, so z = T X comes in units of
+// 2^(xe - kZExp).
+constexpr int kTriExp = 6, kXExp = 12, kZExp = kXExp + kTriExp;
+__host__ __device__ inline int x_exp(int e) { return e < kZExp - 126 ? kZExp - 126 : e; }
+
 // The unit of a state whose largest element lies below 2^e: at 2^14.
 __host__ __device__ inline int first_unit(int e) { return 14 - held_exp(e); }
 
@@ -26,12 +31,12 @@ __host__ __device__ inline int unit_for_values(int un, int e) {
 
 struct UnitStep { int up, zu; };
 // From the unit un to the next one, un + up: 2^14 above a bound of the next state, below 2^e in units of un; a state of 0
-// says nothing about the next chunk's values and has the unit 1.  z, in units of 2^(xe - 12), takes 2^zu.
+// says nothing about the next chunk's values and has the unit 1.  z takes 2^zu.
 __host__ __device__ inline UnitStep next_unit(int un, bool zero, int e, int xe) {
     int up = zero ? -un : 14 - held_exp(e);
     up = up < -126 - un ? -126 - un : (up > 126 - un ? 126 - un : up);
     up = up < -114 ? -114 : up;
-    int zu = xe - 12 + up;
+    int zu = xe - kZExp + up;
     zu = zu < -126 ? -126 : (zu > 126 ? 126 : zu);
     return {up, zu};
 }

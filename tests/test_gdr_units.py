@@ -15,6 +15,9 @@ SHIM = r"""
 #include "gdr_units.h"
 extern "C" {
 int plain_unit() { return sconv::kPlainUnit; }
+int x_scale() { return sconv::kXExp; }
+int z_unit() { return sconv::kZExp; }
+int x_exp(int e) { return sconv::x_exp(e); }
 int held(int e) { return sconv::held_exp(e); }
 int first(int e) { return sconv::first_unit(e); }
 int for_values(int un, int e) { return sconv::unit_for_values(un, e); }
@@ -60,9 +63,10 @@ def test_every_step_has_factors_within_fp32(units):
     for un in range(-126, 127):
         for e in range(-150, 129, 3):
             for zero in (False, True):
-                for xe in (-112, -60, 0, 40, 113, 127):
+                for xe in (-112, -109, -60, 0, 40, 113, 127):
+                    xe = units.x_exp(xe)
                     up, zu = step(units, un, zero, units.held(e), xe)
-                    for x in (up, zu, un + up, -(un + up), 12 - xe, xe - 12):
+                    for x in (up, zu, un + up, -(un + up), units.x_scale() - xe, xe - units.z_unit()):
                         assert -126 <= x <= 126, (un, e, zero, xe, up, zu)
 
 
@@ -107,9 +111,10 @@ def column(u, chunks, s0, kb):
                 un = to
             assert abs(s) < 2 ** 15
             xv = f32(kb) * f32(v * pow2(un))
-            xe = exp_of(u, xv + s)
-            z = f32(64) * (xv * pow2(12 - xe)) + s * pow2(12 - xe)
-            bound = f32(z * pow2(xe - 12)) * f32(128) + s * last
+            xe = u.x_exp(exp_of(u, xv + s))
+            to_x, t = pow2(u.x_scale() - xe), f32(2.0 ** (u.z_unit() - u.x_scale()))
+            z = t * (f32(64) * (xv * to_x) + s * to_x)
+            bound = f32(z * pow2(xe - u.z_unit())) * f32(128) + s * last
             up, zu = step(u, un, bound == 0, exp_of(u, bound), xe)
             un += up
             y = z * pow2(zu)
