@@ -412,7 +412,9 @@ int sconv_paged_fused_multi(int32_t num_streams,
  *     S <- e^g S;   u = beta (v - S k);   S <- S + u k^T;   o = S q
  * where q and k are first divided by sqrt(sum of squares + 1e-6) when
  * qk_l2norm is non-zero, and q is multiplied by `scale`.  The state, all sums
- * and the gates are in fp32 or more; o is rounded once to bf16.
+ * and the gates are in fp32 or more, and o is rounded to bf16.  Decode, and
+ * prefill a token at a time, round nothing else below fp32; prefill in chunks
+ * takes some operands of its products in fewer bits (gdr_fwd_varlen).
  *
  * q, k         logical [.. tokens][num_k_heads][head_dim_k] bf16.
  * v, out       logical [.. tokens][num_v_heads][head_dim_v] bf16.  q, k and v
@@ -454,7 +456,11 @@ int sconv_paged_fused_multi(int32_t num_streams,
  *     rule to be stable at all; the inverse below it leaves fp16 far above;
  *   - an infinity or NaN in a token may reach the other tokens of its chunk,
  *     sequence and head, earlier ones too;
- *   - a value channel is held to about 2^-26 of its largest value in the chunk;
+ *   - products that feed the state have operands of 22 bits, those that only
+ *     feed out (q with the state, scores with u) of 11, where out itself has 8:
+ *     it is wrong by 0.00168 of its size, 0.00166 of which are its own rounding;
+ *   - a value channel is held to about 2^-26 of its largest value in the chunk,
+ *     and an element of a key or query to 2^-24 of its row's norm;
  *   - values, and beta |k| times them, may be as large as 2^80 (beta |k|: 2^20).
  * workspace    device memory, 16-byte aligned, in use until the call's work is
  *              done, or NULL.  With gdr_fwd_workspace_bytes() bytes of it, calls
