@@ -13,25 +13,25 @@
 // The rule by itself is some 100 K fp32 operations a token and head, each token
 // waiting for the one before.  Here the same work is matrix products, 64 tokens
 // at a time: 64 sequences of up to 2048 tokens, 32 heads of 128 x 128, take
-// 0.77 ms where a token at a time takes 18.7 ms.
+// 0.76 ms where a token at a time takes 18.7 ms.
 //
 // One kernel (many heads).  A workgroup of 8 waves owns 128 value channels of
 // one head and walks its sequence.  Per chunk it prepares the operands in LDS
 // (conversion, K K^T, Q K^T, the inverse: phases between barriers), then each
 // wave takes its 16 channels through the chunk with the state in its
 // registers.  Two workgroups share a CU (128 registers, 79 KB), so that one's
-// matrix products run beside the other's conversions and waits: 1.07 ms, where
-// waves that only prepare beside waves that only consume, one workgroup a CU,
-// took 1.21.  What bounds it now: a chunk is a chain of phases, 8.7 us for a
-// workgroup alone on its CU and 11.9 for two sharing it, with the VALU 70 %
-// busy (conversions, scaling, addresses: 1200 instructions a wave and chunk)
-// and the MFMAs 28 %; a twentieth less VALU work alone changes nothing.  Bytes
-// would take 0.34 ms.
+// matrix products run beside the other's conversions and waits (waves that only
+// prepare beside waves that only consume, one workgroup a CU, took 13 % more when
+// both were at 1.1 ms).  What bounds it now: a chunk is a chain of phases, 8.3 us
+// for a workgroup alone on its CU (7.6 with few on the chip) and 12.6 for two
+// sharing it, with the VALU 78 % busy (conversions, scaling, addresses: 1200
+// instructions a wave and chunk) and the MFMAs 31 %; a twentieth less VALU work
+// alone changes nothing.  Bytes would take 0.29 ms.
 //
 // Two kernels (few heads): a walk is a chain of chunks, so everything that does
 // not depend on the state is prepared before it by the whole chip.  At 4195
-// tokens, 32 heads: 29 us and 141 us for 66 chunks, 2.1 us each, a chain of
-// products and of the conversions between them; at 14807 tokens 75 and 463 us.
+// tokens, 32 heads: 29 us and 132 us for 66 chunks, 2.0 us each, a chain of
+// products and of the conversions between them; at 14807 tokens 74 and 452 us.
 //
 // Waves of one state never exchange anything: an MFMA result has its channel in
 // the lane and 4 rows a register quad, and the next product takes it as its

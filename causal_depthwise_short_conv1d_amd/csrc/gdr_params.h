@@ -83,12 +83,15 @@ constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;     // of a launch
 constexpr int kGdrThreads = 512;                               // a workgroup of the chunked kernels
 
 // Whether a call's heads are so few, and its sequences long enough, that walking prepared chunks in two kernels is
-// faster than one kernel: a chunk takes a walk 2.2 us and the one kernel 7.3, but twice the workgroups and a launch more
-// gain nothing where CUs are full or there is one chunk.  Measured with 128 x 128 heads, us with two kernels / one:
+// faster than one kernel: a chunk takes a walk 2.0 to 2.2 us and the one kernel 7.6, but twice the workgroups and a launch
+// more gain nothing where CUs are full or there is one chunk.  Measured with 128 x 128 heads and sequences of one length, us
+// with two kernels / one:
 //   64 tokens a sequence: 32 heads 16.0 / 14.0;  65: 16 heads 16.7 / 20.8
 //   128: 16 heads 16.9 / 21.2, 64 heads 18.9 / 22.1, 96 heads 27 / 22, 128 heads 30 / 23
 //   256: 64 heads 25 / 36, 96 heads 37.8 / 37.3, 128 heads 40.4 / 38.0;  320: 96 heads 43.5 / 45.4, 128 heads 44.9 / 45.7
 //   2048: 32 heads 84 / 245, 128 heads 188 / 247, 160 heads 257 / 251, 192 heads 277 / 264
+// The host knows only the mean length.  One long sequence among short ones counts as so many long ones and takes one kernel:
+// 4195 tokens beside four sequences of one token, 32 heads, 509 us, where they take 164 alone.
 inline bool gdr_few_heads(int64_t T, int64_t batch, int64_t Hv, int64_t Dv) {
     const int64_t halves = batch * Hv * ((Dv + 63) / 64);
     return (halves <= 128 && T > 64 * batch) || (halves <= 256 && T > 256 * batch);

@@ -10,8 +10,8 @@
 // 128-byte pieces and a sum over k is three lane exchanges.  The state is read
 // and written once however many tokens follow each other; everything else is
 // a few KiB.  Decode is bound by those bytes: 256 requests of 32 heads of
-// 128 x 128 move 1.07 GB in 203 us, 5.3 TB/s (a large copy: 4.9), 64 requests
-// take 56 us.
+// 128 x 128 move 1.07 GB in 202 us, 5.3 TB/s (a copy of as many bytes: 5.3), 64
+// requests take 56 us.
 // State rows pass the caches (nontemporal): a step reads a line once and the
 // next step comes after a model's other layers.  221 us with plain accesses for
 // 256 requests, 62 for 64; a batch that stays in the caches between calls would

@@ -13,7 +13,7 @@
 // scans the slice sums and reads one slice again, into registers).
 // 64 requests of 131072 entries: 13 us for the sums, which read 67 MB
 // (5.2 TB/s), and 7 us to pick: three dependent reads and as many scans, about
-// what any workgroup takes for them.  256 requests without draft rows: 22 and
+// what any workgroup takes for them.  256 requests without draft rows: 20 and
 // 8 us.  (Reading the rows past the caches is worth 1 % either way.)
 #include "gdr_params.h"
 #include "sconv_device.h"
