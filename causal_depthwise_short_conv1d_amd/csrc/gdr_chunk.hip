@@ -77,8 +77,8 @@ __device__ __forceinline__ constexpr int tri_tile(int mt, int tt) { return mt < 
 constexpr int kTriTiles = 6;
 
 // What decays between two tokens is small, and fp16 has no step below 2^-24: the triangles are held times powers of two.  A
-// and T, 4 at most where the rule contracts, have steps of 2^-30 so (and 2^10 is left above them where it hardly does); P,
-// at most 2.25, of 2^-38.
+// and T, 4 at most where the rule contracts, then have steps of 2^-30 (and may reach 1023); P, at most 2, of 2^-38.  Without,
+// a state that decays by 2^-17 inside a chunk was off by 2^-23 of the chunk's largest value.
 constexpr float kTriScale = 1 << kTriExp, kTriInv = 1.0f / kTriScale;
 constexpr float kPScale = 1 << 14;
 
