@@ -17,6 +17,9 @@ Entry points (same names as the C ABI):
   gdr_fwd_varlen       -- the gated delta rule over a packed varlen batch
   gdr_update           -- its decode update, with the speculative options
   sconv_verify_drafts  -- which drafted tokens stand (num_accepted_tokens)
+  ssm_fwd_varlen       -- the selective state space scan over a packed varlen batch
+  ssm_update           -- its decode update, with the speculative options
+  sconv_group_norm     -- the norm of channel groups, with a gate or activation
 bind_fwd_varlen and bind_update_decode marshal a forward or a decode step
 once for repeated launches.
 """
@@ -31,6 +34,7 @@ import torch
 __all__ = ["conv1d_fwd_varlen", "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
            "sconv_paged_fused_multi", "sconv_seq_metadata", "new_output", "bind_fwd_varlen",
            "bind_update_decode", "gdr_fwd_varlen", "gdr_update", "sconv_verify_drafts",
+           "ssm_fwd_varlen", "ssm_update", "sconv_group_norm",
            "SconvError", "library_path", "load_library", "exported_symbols",
            "version", "status_string"]
 
@@ -98,8 +102,15 @@ def load_library(path: str | None = None):
         *([P, I64, I64, I64, I64] * 3), *([P, I64, I64, I64] * 2), P, P, P, I64, I64, I64, I64, I64,
         P, I64, I64, I32, P, P, I64, I64, I32, I32, I32, I32, I32, I32, F32, I32, I32,
         P, I64, I64, I64, I64, P]
+    lib.ssm_fwd_varlen.argtypes = [
+        *([P, I64, I64, I64] * 2), I32, *([P, I64, I64, I64] * 3), P, I64, I64, P, I64, I64, I64, P, I64, I64, I32, F32, F32,
+        P, I64, I64, I64, I64, I64, P, P, P, I32, I64, I32, I32, I32, I32, I32, P, I64, I64, I64, P, I64, P]
+    lib.ssm_update.argtypes = [
+        *([P, I64, I64, I64, I64] * 2), I32, P, I64, I64, I64, *([P, I64, I64, I64, I64] * 2), P, I64, I64,
+        P, I64, I64, I64, I64, P, I64, I64, I32, F32, F32, P, I64, I64, I64, I64, I64, P, I64, I64, I32, P, P, I64, I64,
+        I32, I32, I32, I32, I32, I32, I32, P, I64, I64, I64, I64, P]
     packed = {}
-    for f in (lib.gdr_fwd_varlen, lib.gdr_update):
+    for f in (lib.gdr_fwd_varlen, lib.gdr_update, lib.ssm_fwd_varlen, lib.ssm_update):
         words = getattr(lib, f.__name__ + "_packed")
         words.argtypes, words.restype = [ctypes.c_char_p], ctypes.c_int
         # the words of a call as bytes: a float is the low half of its word
@@ -109,9 +120,12 @@ def load_library(path: str | None = None):
         P, P, P, I64, P, I64, P, P, I32, I32, I32, I32, P, I64, P, P, I64, P]
     lib.sconv_verify_workspace_bytes.argtypes = [I32, I32]
     lib.sconv_verify_workspace_bytes.restype = I64
+    lib.sconv_group_norm.argtypes = [
+        *([P, I64, I64, I64] * 2), P, I64, P, I64, I32, I64, I32, I32, I32, I32, I32, F32, P, I64, I64, I64, P]
     for f in (lib.conv1d_fwd_varlen, lib.conv1d_update_decode, lib.conv1d_update,
               lib.sconv_paged_fused, lib.sconv_paged_fused_multi, lib.sconv_seq_metadata,
-              lib.gdr_fwd_varlen, lib.gdr_update, lib.sconv_verify_drafts):
+              lib.gdr_fwd_varlen, lib.gdr_update, lib.sconv_verify_drafts, lib.ssm_fwd_varlen, lib.ssm_update,
+              lib.sconv_group_norm):
         f.restype = ctypes.c_int
     if path is None:
         _packed.update(packed)        # before _lib: another thread's call looks there once it finds the library
@@ -124,7 +138,8 @@ def exported_symbols() -> list[str]:
             "conv1d_update_decode", "conv1d_update", "sconv_paged_fused",
             "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen",
             "gdr_fwd_varlen_packed", "gdr_fwd_workspace_bytes", "gdr_update", "gdr_update_packed",
-            "sconv_verify_workspace_bytes", "sconv_verify_drafts"]
+            "sconv_verify_workspace_bytes", "sconv_verify_drafts", "ssm_fwd_varlen", "ssm_fwd_varlen_packed",
+            "ssm_update", "ssm_update_packed", "sconv_group_norm"]
 
 
 def version() -> tuple[int, int]:
@@ -807,3 +822,234 @@ def sconv_verify_drafts(draft_tokens, draft_start_loc, target_probs, draft_probs
         _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch), ws.data_ptr(),
         ws_bytes))
     return tokens, num_accepted_tokens
+
+
+# ------------------------------------------------- selective state space scan --
+
+_INF = float("inf")
+
+
+def _ssm_tensors(x, dt, A, B, C, D, z, dt_bias, state, out, dev, index, lead):
+    """Checks and marshals what prefill and decode share.  `lead`: x's leading dimensions (tokens, or entries and maybe
+    tokens).  Returns the sizes (heads, groups, head_dim, state_dim), the tensors (x, dt), A, (B, C), D, z, dt_bias, state and
+    out, each as its address and strides (the leading dimensions' first), and whether dt is fp32."""
+    n = len(lead)
+    a_shape, xs, bs = A.shape, x.shape, B.shape
+    if C.shape != bs or bs[:n] != lead:
+        raise ValueError("B and C need one shape, and x's tokens")
+    if out.shape != xs or (z is not None and z.shape != xs):
+        raise ValueError("out and z must have x's shape")
+    rest = xs[n:]
+    if len(a_shape) == 1:              # one decay a head
+        if len(rest) != 2 or a_shape[0] != rest[0] or len(bs) != n + 2:
+            raise ValueError("A (heads,) needs x (.., heads, head_dim) and B, C (.., groups, state_dim)")
+        H, P = rest
+        G, N = bs[n:]
+        of = (H,)                      # what has a step size
+        a_str, d_str = (A.stride(0), 0, 0), (0,)
+        whole = (H, P)
+    elif len(a_shape) == 2:            # one a channel and state
+        if len(rest) != 1 or a_shape[0] != rest[0] or len(bs) not in (n + 1, n + 2) or bs[-1] != a_shape[1]:
+            raise ValueError("A (dim, state_dim) needs x (.., dim) and B, C (.., [groups,] state_dim)")
+        dim, N = a_shape
+        H = G = bs[n] if len(bs) == n + 2 else 1
+        if G < 1 or dim % G:
+            raise ValueError("dim must be a multiple of B's groups")
+        P = dim // G
+        of = whole = (dim,)
+        a0, a1 = A.stride()
+        a_str = (P * a0, a0, a1)
+    else:
+        raise ValueError("A must be (heads,) or (dim, state_dim)")
+    heads = len(a_shape) == 1
+    if H < 1 or G < 1 or H % G:
+        raise ValueError("x's heads must be a multiple of B's groups")
+    if dt.shape != (*lead, *of):
+        raise ValueError("dt needs one value per token and head, or per token and channel where A has one decay a channel")
+
+    def weight(t, name):
+        if t is None:
+            return 0, 0, 0
+        if t.shape != of and t.shape != whole:
+            raise ValueError(f"{name} must be ({'heads,) or (heads, head_dim' if name == 'D' and heads else 'heads,' if heads else 'dim,'})")
+        st = t.stride()
+        return (_ptr(t, _F32, name, dev, index), *((st[0], 0) if t.dim() == 1 else st)) if heads else (
+            _ptr(t, _F32, name, dev, index), P * st[0], st[0])
+
+    def rows(t):                       # x, z, out
+        st = t.stride()
+        return st if heads else (*st[:-1], P * st[-1], st[-1])
+
+    if dt_bias is not None and dt_bias.shape != of:
+        raise ValueError("dt_bias needs one value per step size of a token")
+    if state is None:
+        st = (0, 0, 0, 0, 0, 0)
+    else:
+        ss = state.shape
+        if ss[1:] != (*whole, N):
+            raise ValueError("state must be (lines, heads, head_dim, state_dim), or (lines, dim, state_dim)")
+        s4 = state.stride()
+        st = (_ptr(state, _F32, "state", dev, index), *(s4 if heads else (s4[0], P * s4[1], s4[1], s4[2])), ss[0])
+    dt_fp32 = dt.dtype is _F32
+    if not (index >= 0 and x.dtype is B.dtype is C.dtype is out.dtype is _BF16 and A.dtype is _F32 and
+            (dt_fp32 or dt.dtype is _BF16) and (z is None or (z.dtype is _BF16 and z.get_device() == index)) and
+            index == B.get_device() == C.get_device() == dt.get_device() == A.get_device() == out.get_device()):
+        for t, dtype, name in ((x, _BF16, "x"), (B, _BF16, "B"), (C, _BF16, "C"), (z, _BF16, "z"), (out, _BF16, "out"),
+                               (A, _F32, "A"), (dt, _F32 if dt_fp32 else _BF16, "dt")):
+            _dev(t, dtype, name, dev)
+    d_st = dt.stride()
+    d_st = (*d_st, 0) if heads else (*d_st[:-1], P * d_st[-1], d_st[-1])
+    b_st, c_st = B.stride(), C.stride()
+    if len(bs) == n + 1:
+        b_st, c_st = (*b_st[:-1], 0, b_st[-1]), (*c_st[:-1], 0, c_st[-1])
+    return ((H, G, P, N), ((x.data_ptr(), *rows(x)), (dt.data_ptr(), *d_st)), (A.data_ptr(), *a_str),
+            ((B.data_ptr(), *b_st), (C.data_ptr(), *c_st)), weight(D, "D"),
+            (0,) * (n + 3) if z is None else (z.data_ptr(), *rows(z)), weight(dt_bias, "dt_bias"), st,
+            (out.data_ptr(), *rows(out)), dt_fp32)
+
+
+def _limits(dt_limit):
+    if dt_limit is None:
+        return -_INF, _INF
+    lo, hi = dt_limit
+    return float(lo), float(hi)
+
+
+def ssm_fwd_varlen(x, dt, A, B, C, state, query_start_loc, cache_indices=None, has_initial_state=None, D=None, z=None,
+                   dt_bias=None, dt_softplus: bool = False, dt_limit=None, pad_slot_id: int = -1, out=None):
+    """The selective state space scan over a packed varlen batch: per channel and token,
+    S <- e^(d A) S + d x B; out = (S . C + D x) silu(z), with d = clamp([softplus](dt + dt_bias)).
+
+    One decay a head: A (heads,), x (T, heads, head_dim), dt (T, heads), B, C (T, groups, state_dim), state
+    (lines, heads, head_dim, state_dim), D (heads,) or (heads, head_dim), dt_bias (heads,).  One a channel and state:
+    A (dim, state_dim), x (T, dim), dt (T, dim), B, C (T, [groups,] state_dim), state (lines, dim, state_dim), D and dt_bias
+    (dim,).  x, B, C and z bf16, any strides (views of a convolution's (T, dim) output take the vector loads); dt bf16 or
+    fp32; A, D, dt_bias and state fp32; D, z (like x), dt_bias and state may be None.  dt_limit: (least, largest) step size.
+    A decay d A above 0 counts as 0.  query_start_loc int32 (batch+1,), cache_indices int32 (batch,) or None,
+    has_initial_state bool (batch,) or None: as for conv1d_fwd_varlen.  state is updated in place.  Returns out, like x;
+    rows of padded sequences are left as they are."""
+    dev = x.device
+    index = x.get_device()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    (H, G, P, N), (xa, da), a, (ba, ca), d, za, bias, st, o, dt_fp32 = _ssm_tensors(
+        x, dt, A, B, C, D, z, dt_bias, state, out, dev, index, x.shape[:1])
+    lo, hi = _limits(dt_limit)
+    batch = query_start_loc.numel() - 1
+    total = x.shape[0]
+    _launch_packed("ssm_fwd_varlen", dev, (
+        *xa, *da, dt_fp32, *a, *ba, *ca, *d, *za, *bias, 1 if dt_softplus else 0, lo, hi, *st,
+        _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
+        _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),
+        _vec(query_start_loc, _I32, "query_start_loc", dev, index, 1),
+        batch, total, H, G, P, N, pad_slot_id, *o, 0, 0))
+    return out
+
+
+def ssm_update(x, dt, A, B, C, state, cache_indices=None, num_accepted_tokens=None, output_state_indices=None, D=None,
+               z=None, dt_bias=None, dt_softplus: bool = False, dt_limit=None, pad_slot_id: int = -1, out=None):
+    """Decode update of the selective state space scan: x, dt, B, C and z as for ssm_fwd_varlen with (batch,) or
+    (batch, seqlen) in place of the tokens, state updated in place.  cache_indices, num_accepted_tokens and
+    output_state_indices: as for gdr_update.  Returns out, shaped like x."""
+    dev = x.device
+    index = x.get_device()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    n = x.dim() - (2 if A.dim() == 1 else 1)
+    if n not in (1, 2):
+        raise ValueError("x must be (batch, [seqlen,] heads, head_dim), or (batch, [seqlen,] dim)")
+    if state is None:
+        raise ValueError("state is required")
+    batch, seqlen = x.shape[0], x.shape[1] if n == 2 else 1
+    ci, ci_seq, ci_step, steps, wide = cache_indices, 0, 0, 1, False
+    if ci is not None:
+        cs = ci.shape
+        wide = len(cs) == 2
+        if not (wide or len(cs) == 1) or cs[0] < batch:
+            raise ValueError("cache_indices must be (batch,) or (batch, steps)")
+        if wide:
+            steps = cs[1]
+            ci_seq, ci_step = ci.stride()
+        else:
+            ci_seq = ci.stride(0)
+    if num_accepted_tokens is not None and not wide:
+        raise ValueError("num_accepted_tokens needs cache_indices of (batch, steps)")
+    osi, osi_seq, osi_step = output_state_indices, 0, 0
+    if osi is not None:
+        if osi.dim() != 2 or osi.shape[0] < batch or osi.shape[1] < seqlen:
+            raise ValueError("output_state_indices must be (batch, >= seqlen)")
+        osi_seq, osi_step = osi.stride()
+    (H, G, P, N), (xa, da), a, (ba, ca), d, za, bias, st, o, dt_fp32 = _ssm_tensors(
+        x, dt, A, B, C, D, z, dt_bias, state, out, dev, index, x.shape[:n])
+    if n == 1:                         # (a token dimension of stride 0)
+        xa, da, ba, ca, za, o = ((*t[:2], 0, *t[2:]) for t in (xa, da, ba, ca, za, o))
+    lo, hi = _limits(dt_limit)
+    _launch_packed("ssm_update", dev, (
+        *xa, *da, dt_fp32, *a, *ba, *ca, *d, *za, *bias, 1 if dt_softplus else 0, lo, hi, *st,
+        _ptr(ci, _I32, "cache_indices", dev, index), ci_seq, ci_step, steps,
+        _vec(num_accepted_tokens, _I32, "num_accepted_tokens", dev, index, batch),
+        _ptr(osi, _I32, "output_state_indices", dev, index), osi_seq, osi_step,
+        batch, seqlen, H, G, P, N, pad_slot_id, *o))
+    return out
+
+
+# -------------------------------------------------------------- group norm --
+
+_NORMS = {"rms": 0, "layer": 1}
+_NORM_ACTS = {None: 0, "silu": 1, "swish": 1, "sigmoid": 2}
+
+
+def sconv_group_norm(x, group_size: int | None = None, weight=None, bias=None, z=None, eps: float = 1e-5,
+                     norm: str = "rms", activation=None, gate_first: bool = False, out=None):
+    """The norm of every group of channels of every row, with the layer's gate or activation.
+
+    x (rows, channels) bf16 in groups of group_size channels (default: all of them), or (rows, heads, head_dim) with a group a
+    head; z like x, or None; weight and bias bf16 or fp32 (one type), of all the channels or of one group (shared by the
+    groups), or None.  v = x act(z) with gate_first, else x; v = norm(v) weight + bias over each group ("rms": by its root
+    mean square; "layer": its mean is taken out first); then v act(z), or act(v) without z, or v with gate_first.
+    activation: None, "silu" or "sigmoid".  Returns out, which may be x or z itself."""
+    dev, index = x.device, x.get_device()
+    xs = x.shape
+    if len(xs) == 3:
+        rows, groups, size = xs
+        if group_size is not None and group_size != size:
+            raise ValueError("x of heads is normalised by heads: group_size must be head_dim")
+    elif len(xs) == 2:
+        rows, channels = xs
+        size = channels if group_size is None else group_size
+        if size < 1 or channels % size:
+            if channels:
+                raise ValueError("channels must be a multiple of group_size")
+            size = 1
+        groups = channels // size
+    else:
+        raise ValueError("x must be (rows, channels) or (rows, heads, head_dim)")
+    if out is None:
+        out = torch.empty(xs, dtype=x.dtype, device=dev)
+    if out.shape != xs or (z is not None and z.shape != xs):
+        raise ValueError("out and z must have x's shape")
+    if norm not in _NORMS or activation not in _NORM_ACTS:
+        raise ValueError(f"unsupported norm {norm!r} or activation {activation!r}")
+    if gate_first and z is None:
+        raise ValueError("gate_first needs z")
+    first = bias if weight is None else weight
+    w_type, ws = _F32 if first is not None and first.dtype is _F32 else _BF16, []
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            ws += (0, 0)
+            continue
+        n = t.numel()
+        if n not in (size, groups * size) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of all the channels or of one group's")
+        ws += (_ptr(t, w_type, name, dev, index), size if n != size else 0)
+
+    def strides(t):
+        st = t.stride()
+        return st if len(st) == 3 else (st[0], size * st[1], st[1])
+
+    _launch("sconv_group_norm", dev, (
+        _ptr(x, _BF16, "x", dev, index), *strides(x),
+        *((_ptr(z, _BF16, "z", dev, index), *strides(z)) if z is not None else (0, 0, 0, 0)), *ws, w_type is _F32,
+        rows, groups, size, _NORMS[norm], _NORM_ACTS[activation], 1 if gate_first else 0, eps,
+        _ptr(out, _BF16, "out", dev, index), *strides(out)))
+    return out

@@ -2,9 +2,6 @@
 // launches.  Nothing here touches device memory or synchronises.
 #include <math.h>
 #include <stdint.h>
-#include <string.h>
-
-#include <utility>
 
 #include "gdr_params.h"
 #include "sconv.h"
@@ -13,24 +10,6 @@
 using namespace sconv;
 
 namespace {
-
-bool negative(std::initializer_list<int64_t> v) {
-    for (int64_t x : v)
-        if (x < 0) return true;
-    return false;
-}
-
-// Every stride a multiple of n elements (dimensions of one element aside) and
-// the base aligned to n elements of `elem` bytes.
-bool groups_of(const void *p, int n, int elem, std::initializer_list<int64_t> sizes,
-               std::initializer_list<int64_t> strides) {
-    auto st = strides.begin();
-    for (int64_t s : sizes) {
-        const int64_t d = *st++;
-        if (s > 1 && d % n) return false;
-    }
-    return aligned(p, uintptr_t(n) * uintptr_t(elem));
-}
 
 Span span_of_out(const GdrParams &p, int64_t B, int64_t T) {
     return span_of(p.out, {B, T, p.Hv, p.Dv}, {p.os.sb, p.os.st, p.os.sh, p.os.sd});
@@ -103,24 +82,6 @@ int32_t verify_slice(int64_t batch, int64_t vocab) {
     int64_t s = (batch * vocab + 2047) / 2048;
     s = (s + 255) / 256 * 256;
     return int32_t(s < 1024 ? 1024 : (s > kVfMaxSlice ? kVfMaxSlice : s));
-}
-
-// The word that holds an argument, as that argument.
-template <class A>
-A from_word(const unsigned char *w) {
-    static_assert(sizeof(A) == 4 || sizeof(A) == 8, "an argument fits a word");
-    A a;                               // (little endian: a shorter one is the low half)
-    memcpy(&a, w, sizeof(A));
-    return a;
-}
-template <class... A, size_t... I>
-int call_words(int (*f)(A...), const unsigned char *w, std::index_sequence<I...>) {
-    return f(from_word<A>(w + 8 * I)...);
-}
-template <class... A>
-int call_words(int (*f)(A...), const void *words) {
-    if (!words) return SCONV_ERR_NULL;
-    return call_words(f, static_cast<const unsigned char *>(words), std::index_sequence_for<A...>{});
 }
 
 }  // namespace

@@ -3,7 +3,9 @@
 #pragma once
 
 #include <stdint.h>
+#include <string.h>
 #include <initializer_list>
+#include <utility>
 #include <hip/hip_runtime_api.h>
 
 #include "sconv.h"
@@ -59,6 +61,42 @@ inline bool non_overlapping(std::initializer_list<int64_t> sizes, std::initializ
         span += st[i] * (n[i] - 1);
     }
     return true;
+}
+
+inline bool negative(std::initializer_list<int64_t> v) {
+    for (int64_t x : v)
+        if (x < 0) return true;
+    return false;
+}
+
+// Every stride a multiple of n elements (dimensions of one element aside) and
+// the base aligned to n elements of `elem` bytes.
+inline bool groups_of(const void *p, int n, int elem, std::initializer_list<int64_t> sizes,
+                      std::initializer_list<int64_t> strides) {
+    auto st = strides.begin();
+    for (int64_t s : sizes) {
+        const int64_t d = *st++;
+        if (s > 1 && d % n) return false;
+    }
+    return aligned(p, uintptr_t(n) * uintptr_t(elem));
+}
+
+// The word that holds an argument, as that argument.
+template <class A>
+A from_word(const unsigned char *w) {
+    static_assert(sizeof(A) == 4 || sizeof(A) == 8, "an argument fits a word");
+    A a;                               // (little endian: a shorter one is the low half)
+    memcpy(&a, w, sizeof(A));
+    return a;
+}
+template <class... A, size_t... I>
+int call_words(int (*f)(A...), const unsigned char *w, std::index_sequence<I...>) {
+    return f(from_word<A>(w + 8 * I)...);
+}
+template <class... A>
+int call_words(int (*f)(A...), const void *words) {
+    if (!words) return SCONV_ERR_NULL;
+    return call_words(f, static_cast<const unsigned char *>(words), std::index_sequence_for<A...>{});
 }
 
 inline int launch_status(hipError_t e) { return e == hipSuccess ? SCONV_OK : SCONV_ERR_LAUNCH; }

@@ -1,0 +1,58 @@
+// Device helpers of the state space kernels.
+#pragma once
+
+#include "gdr_device.h"
+#include "ssm_params.h"
+
+namespace sconv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The step size of head h, channel c at element offset `at` of dt (channel included).
+__device__ __forceinline__ float ssm_step(const SsmParams &p, int64_t at, float bias) {
+    float d = p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
+    d += bias;
+    if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
+    d = d < p.dt_min ? p.dt_min : d;   // (NaN stays)
+    return d > p.dt_max ? p.dt_max : d;
+}
+
+// e^(d A), at most 1 (NaN stays).  The argument's rounding moves the result by |d A| e^(d A) 2^-24, which is below 2^-25:
+// what a state keeps is right to that share of the state.
+__device__ __forceinline__ float ssm_decay(float d, float A) {
+    const float g = d * A;
+    return __builtin_amdgcn_exp2f((g > 0.0f ? 0.0f : g) * kLog2e);
+}
+
+// y silu(z).
+__device__ __forceinline__ float ssm_gate(float y, float z) { return y * act<true>(z); }
+
+// Sequence b's (or entry b's) rows and line; false when nothing is to be done for it.
+struct SsmSpan { int64_t t0, n, line; bool init; };
+__device__ __forceinline__ bool ssm_span(const SsmParams &p, int32_t b, SsmSpan &sp) {
+    sp.t0 = 0;
+    sp.n = p.seqlen;
+    sp.line = b;
+    sp.init = p.state != nullptr;
+    if (p.qsl) {
+        int64_t a = p.qsl[b], e = p.qsl[b + 1];
+        a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
+        e = e < a ? a : (e > p.total_T ? p.total_T : e);
+        sp.t0 = a;
+        sp.n = e - a;
+        sp.init = p.state && p.has_init && p.has_init[b] != 0;
+    }
+    if (sp.n == 0) return false;
+    if (p.ci) {
+        int32_t step = 0;
+        if (p.accepted) {
+            step = p.accepted[b] - 1;
+            if (step < 0 || step >= p.ci_steps) return false;
+        }
+        sp.line = p.ci[b * p.ci_sb + step * p.ci_ss];
+        if (sp.line == p.pad_slot_id) return false;
+    }
+    return !(p.state && (sp.line < 0 || sp.line >= p.num_lines));
+}
+
+}  // namespace sconv

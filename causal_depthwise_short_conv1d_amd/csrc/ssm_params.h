@@ -1,0 +1,80 @@
+// Kernel parameters of the selective state space scan and of the group norm,
+// shared by the host checks and the kernels.
+#pragma once
+
+#include <stdint.h>
+#include <hip/hip_runtime_api.h>
+
+#include "gdr_params.h"                // GdrTensor, kMaxThreads
+
+namespace sconv {
+
+// One tensor of the layer's weights: (head, channel, state), fp32.
+struct SsmWeight {
+    const float *p;                    // or null
+    int64_t sh, sd, sn;
+};
+
+struct SsmParams {
+    const uint16_t *x, *B, *C, *z;     // z may be null
+    uint16_t *out;
+    GdrTensor xs, bs, cs, zs, os;      // of B and C: (sequence, token, group, state)
+    const void *dt;                    // fp32 or bf16
+    GdrTensor ds;
+    int32_t dt_fp32, softplus;
+    float dt_min, dt_max;
+    SsmWeight A, D, bias;              // D and bias may be null
+    float *state;                      // [lines][H][P][N] or null
+    int64_t s_sl, s_sh, s_sp, s_sn;
+    int64_t num_lines;
+    int32_t batch;
+    int32_t H, G, P, N;                // heads, groups, channels a head, states a channel
+    int32_t per_group;                 // heads of a group
+    int32_t pad_slot_id;
+    // packed prefill (qsl) or fixed-length entries (seqlen)
+    const int32_t *qsl;
+    const uint8_t *has_init;
+    int64_t total_T;
+    int32_t seqlen;
+    // decode: the line that an entry reads, and those that its steps write
+    const int32_t *ci;
+    int64_t ci_sb, ci_ss;
+    int32_t ci_steps;
+    const int32_t *accepted;
+    const int32_t *osi;
+    int64_t osi_sb, osi_ss;
+};
+
+struct NormParams {
+    const uint16_t *x, *z;             // z may be null
+    uint16_t *out;
+    int64_t x_sr, x_sg, x_sc, z_sr, z_sg, z_sc, o_sr, o_sg, o_sc;    // (row, group, channel)
+    const void *w, *b;                 // fp32 or bf16, or null
+    int64_t w_sg, b_sg;                // (group) strides; channels are contiguous
+    int32_t w_fp32;                    // of both
+    int64_t rows;
+    int32_t groups, size;
+    int32_t layer;                     // the mean is taken out first
+    int32_t act, gate_first;
+    float eps;
+};
+
+constexpr int kSsmMaxState = 256;      // states a channel
+constexpr int kNormBlock = 256;        // threads of a workgroup of the norm
+constexpr int kNormMaxVec = 64 * kNormBlock;     // channels of a group that a workgroup holds in registers
+// Threads that share a group of `size` channels, eight channels each at a time.
+inline int norm_threads(int32_t size) {
+    if (size > 2048) return kNormBlock;
+    int n = 8;
+    while (n < 64 && n * 8 < size) n *= 2;
+    return n;
+}
+
+// Launchers: each enqueues its kernels and returns hipGetLastError().
+// `head`: one step size and one decay a head.  `vec`: unit strides of B, C and the
+// state, and every base and stride of theirs keeps four elements together.
+hipError_t launch_ssm_recurrent(const SsmParams &p, bool head, bool vec, hipStream_t s);
+// `vec`: unit channel strides, every base and stride of 8 elements.
+hipError_t launch_group_norm(const NormParams &p, bool vec, hipStream_t s);
+
+}  // namespace sconv

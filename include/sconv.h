@@ -89,6 +89,9 @@ typedef enum sconv_status {
 #define SCONV_MAX_PAGED_STREAMS 8   /* conv streams of one sconv_paged_fused_multi call */
 #define SCONV_ACT_NONE 0
 #define SCONV_ACT_SILU 1
+#define SCONV_ACT_SIGMOID 2          /* sconv_group_norm only */
+#define SCONV_NORM_RMS 0
+#define SCONV_NORM_LAYER 1
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *sconv_status_string(int status);
@@ -577,6 +580,134 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
                         int32_t batch, int32_t num_drafts, int32_t vocab, int32_t max_drafts,
                         int32_t *tokens, int64_t t_stride_row, int32_t *num_accepted_tokens,
                         void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The selective state space scan -- ssm_fwd_varlen (prefill) and ssm_update
+ * (decode).
+ *
+ * For channel p of head h (group h / (num_heads / num_groups)) with states
+ * S[state_dim] in fp32, per token:
+ *     d = dt + dt_bias;  d = softplus(d) when dt_softplus is non-zero;
+ *     d = min(max(d, dt_min), dt_max)
+ *     S <- e^(d A) S + d x B;   y = sum S C + D x;   y <- y silu(z)
+ * d A is at most 0; a larger value counts as 0.  Two forms, told apart by
+ * strides: one step size and one decay a head (dt, dt_bias and A of channel
+ * stride 0, A of state stride 0), or one step size a channel and one decay a
+ * channel and state.  Steps, decays, the state and all sums are in fp32 or
+ * more, and y is rounded to bf16.
+ *
+ * x, z, out    logical [.. tokens][num_heads][head_dim] bf16; z may be NULL (no
+ *              gate).  x, b and c may be views of one buffer, e.g. the rows of
+ *              a convolution's (T, dim) output.  out may overlap no input.
+ * dt           logical [.. tokens][num_heads][head_dim], bf16, or fp32 when
+ *              dt_fp32 is non-zero.
+ * b, c         logical [.. tokens][num_groups][state_dim] bf16.
+ * a            logical [num_heads][head_dim][state_dim] fp32.
+ * d, dt_bias   logical [num_heads][head_dim] fp32, or NULL (0).
+ * dt_min, dt_max  limits of the step size (-INFINITY and INFINITY: none).
+ * state        logical [num_cache_lines][num_heads][head_dim][state_dim] fp32,
+ *              any strides without two elements at one address.
+ * num_heads must be a multiple of num_groups and state_dim at most 256 (else
+ *   SCONV_ERR_SHAPE), total_tokens at most 2^31 - 257, and a call's rows of
+ *   state (entries x num_heads x head_dim) below about 2^29.
+ * Layouts and speed (results agree to rounding): unit strides of b, c and the
+ *   state, state_dim a multiple of 4 and rows aligned to 16 bytes take the
+ *   vector loads; every other layout loads by elements.
+ * Errors: a NULL tensor -> SCONV_ERR_NULL; bad sizes -> SCONV_ERR_SHAPE; a
+ *   negative stride, or out / state with two elements at one address ->
+ *   SCONV_ERR_STRIDE; a pointer not aligned to its elements ->
+ *   SCONV_ERR_ALIGN; dt_min above dt_max, or NaN -> SCONV_ERR_ARG; out or
+ *   state overlapping an input or each other -> SCONV_ERR_ALIAS.
+ */
+
+/*
+ * ssm_fwd_varlen -- the scan over a packed batch of variable-length sequences.
+ * cache_indices, has_initial_state, query_start_loc, pad_slot_id and
+ * total_tokens: as for conv1d_fwd_varlen.  The state of a sequence starts from
+ * its line when has_initial_state is set, else from zero, and is written back
+ * to its line (a sequence of no tokens writes nothing).  state may be NULL:
+ * zero states, none written.  Rows of skipped sequences and rows behind the
+ * last sequence are left untouched.
+ * workspace, workspace_bytes: reserved; NULL and 0.
+ */
+int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,
+                   const void *dt, int64_t dt_stride_tok, int64_t dt_stride_head, int64_t dt_stride_dim, int32_t dt_fp32,
+                   const float *a, int64_t a_stride_head, int64_t a_stride_dim, int64_t a_stride_state,
+                   const void *b, int64_t b_stride_tok, int64_t b_stride_group, int64_t b_stride_state,
+                   const void *c, int64_t c_stride_tok, int64_t c_stride_group, int64_t c_stride_state,
+                   const float *d, int64_t d_stride_head, int64_t d_stride_dim,
+                   const void *z, int64_t z_stride_tok, int64_t z_stride_head, int64_t z_stride_dim,
+                   const float *dt_bias, int64_t dtb_stride_head, int64_t dtb_stride_dim,
+                   int32_t dt_softplus, float dt_min, float dt_max,
+                   float *state, int64_t s_stride_line, int64_t s_stride_head, int64_t s_stride_dim,
+                   int64_t s_stride_state, int64_t num_cache_lines,
+                   const int32_t *cache_indices, const uint8_t *has_initial_state, const int32_t *query_start_loc,
+                   int32_t batch, int64_t total_tokens, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                   int32_t state_dim, int32_t pad_slot_id,
+                   void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
+                   void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ssm_update -- decode: each of `batch` entries feeds `seqlen` tokens, from the
+ * state of its line.  cache_indices, num_accepted_tokens, output_state_indices:
+ * as for gdr_update.
+ */
+int ssm_update(const void *x, int64_t x_stride_seq, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,
+               const void *dt, int64_t dt_stride_seq, int64_t dt_stride_tok, int64_t dt_stride_head, int64_t dt_stride_dim,
+               int32_t dt_fp32,
+               const float *a, int64_t a_stride_head, int64_t a_stride_dim, int64_t a_stride_state,
+               const void *b, int64_t b_stride_seq, int64_t b_stride_tok, int64_t b_stride_group, int64_t b_stride_state,
+               const void *c, int64_t c_stride_seq, int64_t c_stride_tok, int64_t c_stride_group, int64_t c_stride_state,
+               const float *d, int64_t d_stride_head, int64_t d_stride_dim,
+               const void *z, int64_t z_stride_seq, int64_t z_stride_tok, int64_t z_stride_head, int64_t z_stride_dim,
+               const float *dt_bias, int64_t dtb_stride_head, int64_t dtb_stride_dim,
+               int32_t dt_softplus, float dt_min, float dt_max,
+               float *state, int64_t s_stride_line, int64_t s_stride_head, int64_t s_stride_dim, int64_t s_stride_state,
+               int64_t num_cache_lines,
+               const int32_t *cache_indices, int64_t ci_stride_seq, int64_t ci_stride_step, int32_t ci_steps,
+               const int32_t *num_accepted_tokens,
+               const int32_t *output_state_indices, int64_t osi_stride_seq, int64_t osi_stride_step,
+               int32_t batch, int32_t seqlen, int32_t num_heads, int32_t num_groups, int32_t head_dim, int32_t state_dim,
+               int32_t pad_slot_id,
+               void *out, int64_t o_stride_seq, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
+               hipStream_t stream);
+
+/* The two calls with their arguments in one array of words, as gdr_fwd_varlen_packed. */
+int ssm_fwd_varlen_packed(const void *words);
+int ssm_update_packed(const void *words);
+
+/*
+ * sconv_group_norm -- the norm of every group of channels of every row, with the
+ * gate or activation of the layer, in one launch.  In fp32, per row and group:
+ *     v = x act(z) when gate_first is non-zero, else x
+ *     v <- v - mean(v)                        (SCONV_NORM_LAYER)
+ *     v <- v / sqrt(mean(v^2) + eps);   v <- v weight + bias
+ *     v <- v act(z) (z given, gate_first zero), act(v) (no z), else v
+ * and one rounding to bf16.  The squares of a group have to sum up within fp32.
+ *
+ * x, z, out    logical [rows][num_groups][group_size] bf16, any strides; z may be
+ *              NULL.  out may be exactly x or exactly z (same pointer and
+ *              strides); any other overlap is SCONV_ERR_ALIAS.
+ * weight, bias logical [num_groups][group_size], channel stride 1, bf16 or (both)
+ *              fp32 when weights_fp32 is non-zero; a group stride of 0 shares
+ *              them; NULL: 1 and 0.
+ * norm         SCONV_NORM_RMS or SCONV_NORM_LAYER.
+ * activation   SCONV_ACT_NONE, SCONV_ACT_SILU or SCONV_ACT_SIGMOID.
+ * Layouts and speed: unit channel strides, rows and groups aligned to 16 bytes and
+ *   group_size a multiple of 8, at most 16384, take the vector kernel, which
+ *   reads and writes everything once; others are read by elements, three times.
+ * Errors: NULL x or out -> SCONV_ERR_NULL; a bad size -> SCONV_ERR_SHAPE; a
+ *   negative stride, or out with two elements at one address ->
+ *   SCONV_ERR_STRIDE; a misaligned pointer -> SCONV_ERR_ALIGN; a bad norm or
+ *   activation, an eps that is negative or not finite, or gate_first without z
+ *   -> SCONV_ERR_ARG.
+ */
+int sconv_group_norm(const void *x, int64_t x_stride_row, int64_t x_stride_group, int64_t x_stride_dim,
+                     const void *z, int64_t z_stride_row, int64_t z_stride_group, int64_t z_stride_dim,
+                     const void *weight, int64_t w_stride_group, const void *bias, int64_t b_stride_group,
+                     int32_t weights_fp32, int64_t rows, int32_t num_groups, int32_t group_size, int32_t norm,
+                     int32_t activation, int32_t gate_first, float eps,
+                     void *out, int64_t o_stride_row, int64_t o_stride_group, int64_t o_stride_dim, hipStream_t stream);
 
 #ifdef __cplusplus
 }
