@@ -109,6 +109,8 @@ def load_library(path: str | None = None):
         *([P, I64, I64, I64, I64] * 2), I32, P, I64, I64, I64, *([P, I64, I64, I64, I64] * 2), P, I64, I64,
         P, I64, I64, I64, I64, P, I64, I64, I32, F32, F32, P, I64, I64, I64, I64, I64, P, I64, I64, I32, P, P, I64, I64,
         I32, I32, I32, I32, I32, I32, I32, P, I64, I64, I64, I64, P]
+    lib.ssm_fwd_workspace_bytes.argtypes = [I32, I64, I32, I32, I32, I32, I32]
+    lib.ssm_fwd_workspace_bytes.restype = I64
     packed = {}
     for f in (lib.gdr_fwd_varlen, lib.gdr_update, lib.ssm_fwd_varlen, lib.ssm_update):
         words = getattr(lib, f.__name__ + "_packed")
@@ -139,6 +141,7 @@ def exported_symbols() -> list[str]:
             "sconv_paged_fused_multi", "sconv_seq_metadata", "gdr_fwd_varlen",
             "gdr_fwd_varlen_packed", "gdr_fwd_workspace_bytes", "gdr_update", "gdr_update_packed",
             "sconv_verify_workspace_bytes", "sconv_verify_drafts", "ssm_fwd_varlen", "ssm_fwd_varlen_packed",
+            "ssm_fwd_workspace_bytes",
             "ssm_update", "ssm_update_packed", "sconv_group_norm"]
 
 
@@ -937,12 +940,18 @@ def ssm_fwd_varlen(x, dt, A, B, C, state, query_start_loc, cache_indices=None, h
     lo, hi = _limits(dt_limit)
     batch = query_start_loc.numel() - 1
     total = x.shape[0]
+    need = load_library().ssm_fwd_workspace_bytes(batch, total, H, G, P, N, A.dim() == 2)
+    # the workspace is this stream's until the launch is made: whoever gets its memory next comes after it
+    try:
+        ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
+    except torch.OutOfMemoryError:
+        need = 0                  # (the forms that take none are slower, and right)
     _launch_packed("ssm_fwd_varlen", dev, (
         *xa, *da, dt_fp32, *a, *ba, *ca, *d, *za, *bias, 1 if dt_softplus else 0, lo, hi, *st,
         _vec(cache_indices, _I32, "cache_indices", dev, index, batch),
         _vec(has_initial_state, torch.bool, "has_initial_state", dev, index, batch),
         _vec(query_start_loc, _I32, "query_start_loc", dev, index, 1),
-        batch, total, H, G, P, N, pad_slot_id, *o, 0, 0))
+        batch, total, H, G, P, N, pad_slot_id, *o, ws.data_ptr() if need else 0, need))
     return out
 
 

@@ -75,6 +75,30 @@ int check_ssm(const SsmParams &p, int64_t B, int64_t T, Layout *layout) {
 
 }  // namespace
 
+namespace sconv {
+
+SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int32_t N, bool workspace) {
+    SsmPlan plan = {};
+    plan.nt = N <= 32 ? 1 : (N <= 64 ? 2 : 4);
+    const int64_t units = int64_t(H / G) * ((int64_t(P) + 31) / 32);         // of a group, a wave each
+    plan.waves = units > 4 ? 8 : (units > 2 ? 4 : 2);
+    plan.groups = G * ((units + plan.waves - 1) / plan.waves);
+    // a place takes a CU a workgroup: segments, until there is one for each of 256
+    const int64_t chunks = T / kSsmChunk + batch, mean = T / kSsmChunk / batch;
+    if (workspace && batch * plan.groups < 192 && mean >= 4) {
+        int64_t seg = (chunks * plan.groups + 255) / 256;
+        if (seg < 2) seg = 2;
+        if (seg < mean) {
+            plan.seg = int32_t(seg);
+            plan.slots = T / (kSsmChunk * seg) + batch + 1;
+            plan.bytes = plan.slots * G * units * (plan.nt * 1024 + 1) * 4;
+        }
+    }
+    return plan;
+}
+
+}  // namespace sconv
+
 extern "C" {
 
 int ssm_fwd_varlen_packed(const void *words) { return call_words(ssm_fwd_varlen, words); }
@@ -142,7 +166,38 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
     const int rc = check_ssm(p, 1, total_tokens, &layout);
     if (rc != SCONV_OK) return rc;
     p.per_group = p.H / p.G;
+    const int64_t T = total_tokens;
+    if (layout.head && p.N <= kSsmMaxChunkN) {
+        const SsmPlan plan = ssm_plan(T, batch, p.H, p.G, p.P, p.N, workspace != nullptr);
+        const int64_t places = (plan.seg ? plan.slots : batch) + 7;
+        if (places <= kMaxThreads / (64 * plan.waves) / plan.groups && plan.groups <= INT32_MAX) {
+            if (plan.bytes) {
+                if (!aligned(workspace, 16)) return SCONV_ERR_ALIGN;
+                if (workspace_bytes < plan.bytes) return SCONV_ERR_SHAPE;
+                const Span sw = span_of(workspace, {plan.bytes}, {1}, 1);
+                if (overlap(sw, span_of_out(p, 1, T)) || overlap(sw, span_of_state(p)) || overlaps_input(p, 1, T, sw))
+                    return SCONV_ERR_ALIAS;
+            }
+            const auto rows = [&](const void *a, const GdrTensor &t, int32_t heads) {
+                return !a || (t.sd == 1 && groups_of(a, 8, 2, {T, heads}, {t.st, t.sh}));
+            };
+            const bool vec = p.P % 8 == 0 && p.N % 8 == 0 && rows(p.x, p.xs, p.H) && rows(p.z, p.zs, p.H) &&
+                             rows(p.out, p.os, p.H) && rows(p.B, p.bs, p.G) && rows(p.C, p.cs, p.G);
+            const bool svec = p.state && p.N % 4 == 0 && p.s_sn == 1 &&
+                              groups_of(p.state, 4, 4, {p.num_lines, p.H, p.P}, {p.s_sl, p.s_sh, p.s_sp});
+            return launch_status(launch_ssm_chunk(p, vec, svec, plan, workspace, stream));
+        }
+    }
     return launch_status(launch_ssm_recurrent(p, layout.head, layout.vec, stream));
+}
+
+int64_t ssm_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                                int32_t state_dim, int32_t per_channel) {
+    if (batch < 1 || total_tokens < 1 || num_heads < 1 || num_groups < 1 || num_heads % num_groups || head_dim < 1 ||
+        state_dim < 1 || total_tokens > INT32_MAX - 256)
+        return 0;
+    if (per_channel || state_dim > kSsmMaxChunkN) return 0;
+    return ssm_plan(total_tokens, batch, num_heads, num_groups, head_dim, state_dim, true).bytes;
 }
 
 int ssm_update(const void *x, int64_t x_stride_seq, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,

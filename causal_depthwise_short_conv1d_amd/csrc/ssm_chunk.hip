@@ -1,0 +1,703 @@
+// The selective state space scan of the head form over 64-token chunks: prefill
+// on the matrix cores.
+//
+// With d_j the step sizes, G the running sum of the log decay d A inside a chunk
+// and S the state before it:
+//   y_i = e^G_i (S C_i) + sum_(j <= i) e^(G_i - G_j) d_j (B_j . C_i) x_j + D x_i
+//   S <- e^G_last S + sum_j (e^(G_last - G_j) d_j x_j) B_j^T
+//
+// A wave owns 32 channels of one head: their states in its registers, the chunk's
+// x in a piece of LDS of its own.  The waves of a workgroup belong to one group
+// and share its B and C, which come to LDS a chunk ahead, without passing
+// registers (two buffers, one barrier a chunk).
+//
+// Operands.  v_mfma_f32_32x32x16_bf16: a result has its column in the lane and
+// rows (q % 4) + 8 (q / 4) + 4 (l / 32) in its registers q; an operand has its row
+// or column in the lane and 8 contracted places 8 (l / 32) .. in its registers.
+// Since the order of a contracted index is free, a result is the next product's
+// operand as it lies: the scores P^T[j][i] meet x^T[p][j], the states S^T[n][p]
+// meet C.  What is contracted over tokens comes transposed out of LDS
+// (ds_read_b64_tr_b16).  Rows of S and of y are taken in the order n = r with bits
+// 2 and 3 swapped, so that a lane holds 8 neighbours: 16-byte reads and writes.
+//
+// Precision.  x, B and C are bf16 and enter as they are; every other operand is
+// split into bf16 parts, which have fp32's range: e^(..) d x, which feeds the
+// state, into three (24 bits); S and the scores, which only feed the bf16
+// output, into two (17 bits, 2^-18 of each).  All sums are fp32, G is fp64.
+#include "ssm_device.h"
+
+namespace sconv {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kC = kSsmChunk;          // tokens per chunk
+constexpr int kPW = 32;                // channels a wave
+
+// A head's factors of a chunk, per token, in the LDS of its wave.
+struct alignas(16) Factors {
+    float eG[kC];                      // e^G
+    float w[kC];                       // e^(G_last - G) d
+    float u[kC];                       // e^(G - R), R: G at the start of the token's half
+    float v[kC];                       // e^(R - G) d
+    float vx[kC / 2];                  // e^(R_1 - G) d of the first half
+    float relh[kC], rell[kC], d[kC];   // G - R in two parts, in powers of 2, and the step
+};
+
+// Rows of U 16-byte units in LDS, unit u of row r at u ^ swz(r): 8 neighbouring rows' like units lie in different banks, and so
+// do 4 neighbouring rows' pairs of units.
+template <int U>
+__device__ __forceinline__ int swz(int r) {
+    return U >= 8 ? ((r & 3) << 1 | ((r >> 2) & 1)) : (((r >> 1) & 1) << 1 | ((r >> 2) & 1));
+}
+
+typedef __attribute__((address_space(3))) void LdsVoid;
+typedef const __attribute__((address_space(1))) void GlobalVoid;
+
+// 16 bytes a lane from memory to lds + 16 lane, past the registers.
+__device__ __forceinline__ void to_lds(const void *g, void *lds) {
+    __builtin_amdgcn_global_load_lds((GlobalVoid *)g, (LdsVoid *)lds, 16, 0, 0);
+}
+// What this wave has on its way to LDS is there.
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ bf16x8 read16(const uint16_t *lds) { return *reinterpret_cast<const bf16x8 *>(lds); }
+__device__ __forceinline__ f32x4 row4(const float *v) { return *reinterpret_cast<const f32x4 *>(v); }
+
+// Transposed: lane l gets column l % 16 of its 16 lanes' 4 rows; it names row (l % 16) / 4, columns 4 (l % 4) ..
+__device__ __forceinline__ s16x4 read_tr(const uint16_t *lds) {
+    typedef __attribute__((address_space(3))) s16x4 L;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)lds);
+}
+// 16 tokens from t0 on (contracted: 8 (e / 4) + 4 (l / 32) + e % 4) of the 32 columns from unit u0 on, a column (bits 2 and 3
+// swapped) a lane.
+template <int U>
+__device__ __forceinline__ bf16x8 read_cols(const uint16_t *lds, int t0, int u0, int lane) {
+    const int r = ((lane & 15) >> 2) + 4 * (lane >> 5), c = lane & 3;
+    const int u = u0 + 2 * ((lane >> 4) & 1) + (c & 1), o = 4 * (c >> 1);
+    union { s16x4 s[2]; bf16x8 b; } x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = t0 + 8 * i + r;
+        x.s[i] = read_tr(lds + (t * U + (u ^ swz<U>(t))) * 8 + o);
+    }
+    return x.b;
+}
+
+__device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f32x16 &c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0}; }
+
+__device__ __forceinline__ bf16x8 as_bf16(const uint32_t (&w)[4]) { return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}); }
+
+// x = hi + lo to 2^-18 of it.
+__device__ __forceinline__ void split2(const float (&x)[8], bf16x8 &hi, bf16x8 &lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        l[i] = pack_bf16x2(x[2 * i] - bf_lo(h[i]), x[2 * i + 1] - bf_hi(h[i]));
+    }
+    hi = as_bf16(h);
+    lo = as_bf16(l);
+}
+// ... in three parts, to the last bit.
+__device__ __forceinline__ void split3(const float (&x)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+    uint32_t h[4], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        const float a = x[2 * i] - bf_lo(h[i]), b = x[2 * i + 1] - bf_hi(h[i]);
+        m[i] = pack_bf16x2(a, b);
+        l[i] = pack_bf16x2(a - bf_lo(m[i]), b - bf_hi(m[i]));
+    }
+    hi = as_bf16(h);
+    mid = as_bf16(m);
+    lo = as_bf16(l);
+}
+
+// x + the value that lane CTRL's pattern moves here (fp64, 0 where it moves none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, uint32_t(u), CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, uint32_t(u >> 32), CTRL, ROWS, 0xf, false);
+    return x + __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+template <int LANE>
+__device__ __forceinline__ double lane64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, uint64_t(uint32_t(__builtin_amdgcn_readlane(int(u >> 32), LANE))) << 32 |
+                                          uint32_t(__builtin_amdgcn_readlane(int(u), LANE)));
+}
+
+// Eight elements of a row by elements, zero past n.
+__device__ __forceinline__ u32x4 load8(const uint16_t *row, int64_t sd, int c, int32_t n) {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = c + i < n ? row[(c + i) * sd] : 0u;
+    u32x4 r;
+    r.x = e[0] | e[1] << 16; r.y = e[2] | e[3] << 16;
+    r.z = e[4] | e[5] << 16; r.w = e[6] | e[7] << 16;
+    return r;
+}
+
+// What a workgroup does: chunks [c0, c1) of sequence b, for the heads of `group` from unit u0 on.
+struct Job {
+    int32_t group, u0;
+    int32_t t0, n;                     // the sequence's first row and length
+    int32_t c0, c1;
+};
+
+enum Mode { kWhole, kStates, kSegment };
+
+template <int NT, bool VEC>
+struct Wave {
+    static constexpr int U = 4 * NT;   // units of a row of B and C
+    const SsmParams &p;
+    const Job job;
+    const int lane;
+    const int32_t h, pb;               // head, block of 32 channels
+    const float A, bias;
+    uint16_t *xl;                      // [kC][kPW], this wave's
+    Factors &f;
+    f32x16 S[NT];                      // S^T: n = 32 nt + 16 (q / 8) + 8 (l / 32) + q % 8 of channel chan()
+    float dt;                          // of the next chunk, a token a lane
+
+    __device__ __forceinline__ int32_t chan() const {
+        const int r = lane & 31;
+        return kPW * pb + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) S[i] = zero16();
+    }
+    template <class F>
+    __device__ __forceinline__ void state_rows(F fn) {
+        const int hh = lane >> 5;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) fn(i, 4 * k, 32 * i + 16 * (k >> 1) + 8 * hh + 4 * (k & 1));
+    }
+    __device__ __forceinline__ void load(const float *rows, bool svec) {
+        const int32_t c = chan();
+        zero();
+        if (c >= p.P) return;
+        const float *row = rows + c * p.s_sp;
+        state_rows([&](int i, int q, int n) {
+            if (svec) {
+                if (n < p.N) {
+                    const f32x4 v = row4(row + n);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[i][q + e] = v[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) S[i][q + e] = row[(n + e) * p.s_sn];
+            }
+        });
+    }
+    __device__ __forceinline__ void save(float *rows, bool svec) {
+        const int32_t c = chan();
+        if (c >= p.P) return;
+        float *row = rows + c * p.s_sp;
+        state_rows([&](int i, int q, int n) {
+            if (svec) {
+                if (n < p.N) *reinterpret_cast<f32x4 *>(row + n) = f32x4{S[i][q], S[i][q + 1], S[i][q + 2], S[i][q + 3]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < p.N) row[(n + e) * p.s_sn] = S[i][q + e];
+            }
+        });
+    }
+    // As the registers lie: 16 bytes a lane, 4 NT pieces.
+    __device__ __forceinline__ void load_raw(const float *at) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const f32x4 v = row4(at + ((4 * i + k) * 64 + lane) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[i][4 * k + e] = v[e];
+            }
+    }
+    __device__ __forceinline__ void save_raw(float *at) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<f32x4 *>(at + ((4 * i + k) * 64 + lane) * 4) =
+                    f32x4{S[i][4 * k], S[i][4 * k + 1], S[i][4 * k + 2], S[i][4 * k + 3]};
+    }
+
+    // The row of a chunk's token; behind the sequence's end its last one, whose step counts as 0.
+    __device__ __forceinline__ int64_t row_of(int32_t c, int t) const {
+        const int32_t r = c * kC + t;
+        return int64_t(job.t0) + (r < job.n ? r : job.n - 1);
+    }
+    __device__ __forceinline__ void fetch_dt(int32_t c) {
+        const int64_t at = row_of(c, lane) * p.ds.st + h * p.ds.sh;
+        dt = p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
+    }
+    // The wave's x of a chunk on its way to LDS.
+    __device__ __forceinline__ void fetch_x(int32_t c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = 64 * k + lane, t = at >> 2, u = (at & 3) ^ swz<4>(t);
+            const int ch = kPW * pb + 8 * u;
+            const uint16_t *row = p.x + row_of(c, t) * p.xs.st + h * p.xs.sh;
+            if constexpr (VEC) {
+                if (ch < p.P) to_lds(row + ch, xl + 64 * 8 * k);
+            } else {
+                *reinterpret_cast<u32x4 *>(xl + at * 8) = load8(row, p.xs.sd, ch, p.P);
+            }
+        }
+    }
+
+    // The factors of chunk c from its dt; returns e^G_last, and whether the halves' decays are small enough for products.
+    __device__ __forceinline__ float factors(int32_t c, bool &plain, double &total) {
+        float d = dt + bias;
+        if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
+        d = d < p.dt_min ? p.dt_min : d;
+        d = d > p.dt_max ? p.dt_max : d;
+        if (c * kC + lane >= job.n) d = 0.0f;
+        float g = d * A;
+        g = g > 0.0f ? 0.0f : (g < -200.0f ? -200.0f : g);         // e^-200 is 0, as of anything below
+        double G = double(g) * 1.4426950408889634;
+        G = dpp_add64<0x111, 0xf>(G);                  // row_shr 1, 2, 4, 8, then the rows' last values
+        G = dpp_add64<0x112, 0xf>(G);
+        G = dpp_add64<0x114, 0xf>(G);
+        G = dpp_add64<0x118, 0xf>(G);
+        G = dpp_add64<0x142, 0xa>(G);
+        G = dpp_add64<0x143, 0xc>(G);
+        const double last = lane64<63>(G), mid = lane64<31>(G);
+        const double rel = G - (lane < 32 ? 0.0 : mid);
+        const float r = float(rel);
+        f.eG[lane] = __builtin_amdgcn_exp2f(float(G));
+        f.w[lane] = d * __builtin_amdgcn_exp2f(float(last - G));
+        f.u[lane] = __builtin_amdgcn_exp2f(r);
+        f.v[lane] = d * __builtin_amdgcn_exp2f(-r);
+        if (lane < 32) f.vx[lane] = d * __builtin_amdgcn_exp2f(float(mid - G));
+        plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
+        if (!plain) {
+            f.relh[lane] = r;
+            f.rell[lane] = float(rel - double(r));
+            f.d[lane] = d;
+        }
+        total += last;
+        return __builtin_amdgcn_exp2f(float(last));
+    }
+
+    // x^T: channel chan() a lane, 16 tokens each.
+    __device__ __forceinline__ void read_x(bf16x8 (&x)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = read_cols<4>(xl, 16 * k, 0, lane);
+    }
+
+    // S <- e^G_last S + sum_j w_j x_j B_j^T
+    __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], float keep) {
+        const int hh = lane >> 5;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) S[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const f32x4 w0 = row4(f.w + 16 * k + 4 * hh), w1 = row4(f.w + 16 * k + 8 + 4 * hh);
+            const u32x4 xr = __builtin_bit_cast(u32x4, x[k]);
+            float xw[8];
+            unpack8(xr, xw);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { xw[e] *= w0[e]; xw[4 + e] *= w1[e]; }
+            bf16x8 hi, mid, lo;
+            split3(xw, hi, mid, lo);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const bf16x8 b = read_cols<U>(B, 16 * k, 4 * i, lane);
+                S[i] = mfma(b, hi, S[i]);
+                S[i] = mfma(b, mid, S[i]);
+                S[i] = mfma(b, lo, S[i]);
+            }
+        }
+    }
+
+    // A tile of scores to the two operands of their product with x.  DIAG: tokens of one half (masked, D on the diagonal).
+    template <bool DIAG>
+    __device__ __forceinline__ void weigh(f32x16 &s, int half, bool plain, float D, bf16x8 (&hi)[2], bf16x8 (&lo)[2]) {
+        const int n = lane & 31, hh = lane >> 5;
+        const float ui = f.u[32 * (DIAG ? half : 1) + n];
+        float v[16];
+        if (DIAG && !plain) {
+            const float ih = f.relh[32 * half + n], il = f.rell[32 * half + n];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 32 * half + 8 * k + 4 * hh;
+                const f32x4 jh = row4(f.relh + j), jl = row4(f.rell + j), d = row4(f.d + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = (ih - jh[e]) + (il - jl[e]);
+                    v[4 * k + e] = s[4 * k + e] * (d[e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const f32x4 vj = row4((DIAG ? f.v + 32 * half : f.vx) + 8 * k + 4 * hh);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * k + e] = s[4 * k + e] * ui * vj[e];
+            }
+        }
+        if constexpr (DIAG) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int j = (q & 3) + 8 * (q >> 2) + 4 * hh;
+                v[q] = j < n ? v[q] : (j == n ? v[q] + D : 0.0f);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = v[8 * k + e];
+            split2(t, hi[k], lo[k]);
+        }
+    }
+
+    // The outputs of a chunk, from the state before it.  D: of the head, 0 where it is per channel.
+    __device__ __forceinline__ void emit(int32_t c, const uint16_t *B, const uint16_t *C, const bf16x8 (&x)[4], bool plain, float D) {
+        const int n = lane & 31, hh = lane >> 5;
+        f32x16 y0 = zero16(), y1 = zero16(), s00 = zero16(), s01 = zero16(), s11 = zero16();
+#pragma unroll
+        for (int k = 0; k < 2 * NT; ++k) {
+            const int u = (2 * k + hh) ^ swz<U>(n);    // (rows n and n + 32 are swizzled alike)
+            const bf16x8 b0 = read16(B + (n * U + u) * 8), b1 = read16(B + ((n + 32) * U + u) * 8);
+            const bf16x8 c0 = read16(C + (n * U + u) * 8), c1 = read16(C + ((n + 32) * U + u) * 8);
+            float t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = S[k >> 1][8 * (k & 1) + e];
+            bf16x8 hi, lo;
+            split2(t, hi, lo);
+            s00 = mfma(b0, c0, s00);
+            s01 = mfma(b0, c1, s01);
+            s11 = mfma(b1, c1, s11);
+            y0 = mfma(hi, c0, y0);
+            y1 = mfma(hi, c1, y1);
+            y0 = mfma(lo, c0, y0);
+            y1 = mfma(lo, c1, y1);
+        }
+        y0 *= f.eG[n];
+        y1 *= f.eG[32 + n];
+        bf16x8 hi[2], lo[2];
+        weigh<true>(s00, 0, plain, D, hi, lo);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            y0 = mfma(x[k], hi[k], y0);
+            y0 = mfma(x[k], lo[k], y0);
+        }
+        weigh<false>(s01, 1, plain, D, hi, lo);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            y1 = mfma(x[k], hi[k], y1);
+            y1 = mfma(x[k], lo[k], y1);
+        }
+        weigh<true>(s11, 1, plain, D, hi, lo);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            y1 = mfma(x[2 + k], hi[k], y1);
+            y1 = mfma(x[2 + k], lo[k], y1);
+        }
+        store(c, n, y0);
+        store(c, 32 + n, y1);
+    }
+
+    // Token t's 16 outputs of this lane: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the block.
+    __device__ __forceinline__ void store(int32_t c, int t, const f32x16 &y) {
+        const int32_t r = c * kC + t;
+        if (r >= job.n) return;
+        const int64_t row = int64_t(job.t0) + r;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int32_t ch = kPW * pb + 16 * k + 8 * (lane >> 5);
+            if (ch >= p.P) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = y[8 * k + e];
+            if (p.D.p && p.D.sd != 0) {
+                float xf[8];
+                const uint16_t *xr = p.x + row * p.xs.st + h * p.xs.sh;
+                unpack8(VEC ? ld16(xr + ch) : load8(xr, p.xs.sd, ch, p.P), xf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (ch + e < p.P) v[e] = fmaf(p.D.p[h * p.D.sh + (ch + e) * p.D.sd], xf[e], v[e]);
+            }
+            if (p.z) {
+                float zf[8];
+                const uint16_t *zr = p.z + row * p.zs.st + h * p.zs.sh;
+                unpack8(VEC ? ld16(zr + ch) : load8(zr, p.zs.sd, ch, p.P), zf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = ssm_gate(v[e], zf[e]);
+            }
+            uint16_t *o = p.out + row * p.os.st + h * p.os.sh;
+            if constexpr (VEC) {
+                st16(o + ch, pack8(v));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (ch + e < p.P) o[(ch + e) * p.os.sd] = to_bf16(v[e]);
+            }
+        }
+    }
+};
+
+// B and C of a chunk on their way to LDS, by all of a workgroup's waves.
+template <int NT, int W, bool VEC>
+__device__ __forceinline__ void fetch_bc(const SsmParams &p, const Job &job, int32_t c, uint16_t *B, uint16_t *C, bool with_c) {
+    constexpr int U = 4 * NT, kPieces = kC * U / 64;               // a wave brings 64 units at a time
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < (kPieces + W - 1) / W; ++k) {
+        if (kPieces % W != 0 && wave + k * W >= kPieces) break;
+        const int first = (wave + k * W) * 64, at = first + lane, t = at / U, u = (at % U) ^ swz<U>(t);
+        const int32_t r = c * kC + t;
+        const int64_t row = int64_t(job.t0) + (r < job.n ? r : job.n - 1);
+        const uint16_t *br = p.B + row * p.bs.st + job.group * p.bs.sh, *cr = p.C + row * p.cs.st + job.group * p.cs.sh;
+        if constexpr (VEC) {
+            if (8 * u < p.N) {
+                to_lds(br + 8 * u, B + first * 8);
+                if (with_c) to_lds(cr + 8 * u, C + first * 8);
+            }
+        } else {
+            *reinterpret_cast<u32x4 *>(B + at * 8) = load8(br, p.bs.sd, 8 * u, p.N);
+            if (with_c) *reinterpret_cast<u32x4 *>(C + at * 8) = load8(cr, p.cs.sd, 8 * u, p.N);
+        }
+    }
+}
+
+constexpr int kMaxRanked = 256;
+
+// The sequence that is r-th by length, the longest first: a workgroup takes as long as its sequence, and one that starts late with a
+// long one leaves the chip idle behind it.  More sequences than kMaxRanked stay in order.
+template <int THREADS>
+__device__ __forceinline__ int32_t ranked(const SsmParams &p, int32_t r, int32_t *len) {
+    if (p.batch > kMaxRanked) return r;
+    int32_t *out = len + kMaxRanked;
+    for (int t = threadIdx.x; t < p.batch; t += THREADS) {
+        SsmSpan sp;
+        len[t] = ssm_span(p, t, sp) ? int32_t(sp.n) : 0;
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.batch; t += THREADS) {
+        const int32_t n = len[t];
+        int32_t before = 0;
+        for (int32_t i = 0; i < p.batch; ++i) before += len[i] > n || (len[i] == n && i < t);
+        if (before == r) *out = t;
+    }
+    __syncthreads();
+    return *out;
+}
+
+// Segments of `seg` chunks: segment k of sequence i has slot floor(start_i / (64 seg)) + i + k.  No two share one, and
+// floor(T / (64 seg)) + batch + 1 are enough for any offsets, so no kernel has to count them.
+__device__ __forceinline__ int64_t first_slot(const SsmParams &p, int32_t b, int32_t seg) {
+    int64_t a = p.qsl[b];
+    a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
+    return a / (int64_t(kC) * seg) + b;
+}
+
+struct alignas(16) Raw { float v[4]; };
+
+template <int NT, int W, bool VEC, Mode MODE>
+__global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
+                                                                          int64_t places, int32_t seg, float *states, float *decays,
+                                                                          bool svec) {
+    constexpr int U = 4 * NT, kBC = kC * U * 8;
+    __shared__ alignas(16) uint16_t B[2][kBC], C[MODE == kStates ? 1 : 2][MODE == kStates ? 8 : kBC];
+    __shared__ alignas(16) uint16_t xl[W][kC * kPW];
+    __shared__ Factors factors[W];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+
+    // Blocks go to the 8 XCDs in turn: those of one place and group, which read the same B and C, follow each other on one.
+    const int64_t at = blockIdx.x >> 3, pg = at / blocks * 8 + (blockIdx.x & 7);
+    const int32_t block = int32_t(at % blocks);
+    if (pg >= places * p.G) return;
+    const int64_t place = pg / p.G;
+    Job job;
+    job.group = int32_t(pg - place * p.G);
+    job.u0 = block * W;
+    SsmSpan sp;
+    int64_t slot = 0;
+    int32_t b = int32_t(place);
+    if constexpr (MODE == kWhole) {
+        b = __builtin_amdgcn_readfirstlane(ranked<64 * W>(p, b, reinterpret_cast<int32_t *>(&xl[0][0])));
+        __syncthreads();
+    } else {
+        slot = place;
+        int32_t lo = 0, hi = p.batch - 1;                          // the last sequence whose slots start at or before
+        while (lo < hi) {
+            const int32_t m = (lo + hi + 1) >> 1;
+            if (first_slot(p, m, seg) <= slot) lo = m; else hi = m - 1;
+        }
+        b = lo;
+    }
+    if (!ssm_span(p, b, sp)) return;
+    job.t0 = int32_t(sp.t0);
+    job.n = int32_t(sp.n);
+    const int32_t nc = int32_t((sp.n + kC - 1) / kC);
+    job.c0 = 0;
+    job.c1 = nc;
+    if constexpr (MODE != kWhole) {
+        const int64_t k = slot - first_slot(p, b, seg);
+        if (k < 0 || k * seg >= nc) return;
+        if (MODE == kStates && (k + 1) * seg >= nc) return;        // the last segment's end is no one's start
+        job.c0 = int32_t(k * seg);
+        job.c1 = job.c0 + seg < nc ? job.c0 + seg : nc;
+    }
+
+    // columns that no row has stay zero
+    if (8 * U > p.N || p.P % kPW != 0) {
+        for (int i = threadIdx.x; i < 2 * kBC / 8; i += 64 * W) {
+            reinterpret_cast<u32x4 *>(&B[0][0])[i] = u32x4{0, 0, 0, 0};
+            if (MODE != kStates) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
+        }
+        for (int i = threadIdx.x; i < W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0])[i] = u32x4{0, 0, 0, 0};
+        __syncthreads();
+    }
+
+    const int32_t unit = job.u0 + wave;
+    const bool work = unit < units;
+    const int32_t h = job.group * p.per_group + (work ? unit / pbs : 0), pb = work ? unit % pbs : 0;
+    Wave<NT, VEC> wv{p, job, lane, h, pb, p.A.p[h * p.A.sh], p.bias.p ? p.bias.p[h * p.bias.sh] : 0.0f, xl[wave], factors[wave]};
+    float *rows = p.state ? p.state + sp.line * p.s_sl + h * p.s_sh : nullptr;
+    const int64_t per_slot = int64_t(p.G) * units;
+    const int64_t piece = job.group * units + unit;
+    wv.zero();
+    if (work) {
+        if (MODE != kStates && job.c0 == 0) {
+            if (sp.init) wv.load(rows, svec);
+        } else if (MODE == kSegment) {
+            wv.load_raw(states + ((slot - 1) * per_slot + piece) * (NT * 1024));
+        }
+        wv.fetch_dt(job.c0);
+        wv.fetch_x(job.c0);
+    }
+    fetch_bc<NT, W, VEC>(p, job, job.c0, B[0], C[0], MODE != kStates);
+    const float D = MODE != kStates && p.D.p && p.D.sd == 0 ? p.D.p[h * p.D.sh] : 0.0f;
+    double total = 0.0;
+    landed();
+    __syncthreads();
+    for (int32_t c = job.c0; c < job.c1; ++c) {
+        const int cur = (c - job.c0) & 1;
+        const bool more = c + 1 < job.c1;
+        bf16x8 x[4];
+        bool plain = true;
+        float keep = 1.0f;
+        if (work) {
+            wv.read_x(x);
+            keep = wv.factors(c, plain, total);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // x is in registers: its place is free
+        if (more) {
+            if (work) {
+                wv.fetch_dt(c + 1);
+                wv.fetch_x(c + 1);
+            }
+            fetch_bc<NT, W, VEC>(p, job, c + 1, B[cur ^ 1], MODE == kStates ? C[0] : C[cur ^ 1], MODE != kStates);
+        }
+        if (work) {
+            if constexpr (MODE != kStates) wv.emit(c, B[cur], C[cur], x, plain, D);
+            wv.advance(B[cur], x, keep);
+        }
+        landed();
+        __syncthreads();
+    }
+    if (!work) return;
+    if constexpr (MODE == kStates) {
+        wv.save_raw(states + (slot * per_slot + piece) * (NT * 1024));
+        if (lane == 0) decays[slot * per_slot + piece] = __builtin_amdgcn_exp2f(float(total));
+    } else {
+        if (p.state && job.c1 == nc) wv.save(rows, svec);
+    }
+}
+
+// From each segment's own states to the states that the next one starts from, in place: a thread takes 4 of them through a
+// sequence's segments.
+template <int NT>
+__global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t units, int32_t pbs, int32_t seg, float *states,
+                                                       const float *decays, bool svec) {
+    const int64_t per_slot = int64_t(p.G) * units;
+    const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / (NT * 256);
+    if (id >= int64_t(p.batch) * per_slot) return;
+    const int32_t b = int32_t(id / per_slot);
+    const int64_t piece = id - b * per_slot;
+    const int quad = threadIdx.x + 256 * (blockIdx.x % NT), lane = quad & 63, k = quad >> 6;
+    SsmSpan sp;
+    if (!ssm_span(p, b, sp)) return;
+    const int32_t nc = int32_t((sp.n + kC - 1) / kC), ns = (nc + seg - 1) / seg;
+    if (ns < 2) return;
+    const int32_t group = int32_t(piece / units), unit = int32_t(piece - int64_t(group) * units);
+    const int32_t h = group * p.per_group + unit / pbs, r = lane & 31;
+    const int32_t ch = kPW * (unit % pbs) + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
+    const int32_t n = 32 * (k >> 2) + 16 * ((k >> 1) & 1) + 8 * (lane >> 5) + 4 * (k & 1);
+    f32x4 S = {0, 0, 0, 0};
+    if (sp.init && ch < p.P) {
+        const float *row = p.state + sp.line * p.s_sl + h * p.s_sh + ch * p.s_sp;
+        if (svec) {
+            if (n < p.N) S = row4(row + n);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) S[e] = row[(n + e) * p.s_sn];
+        }
+    }
+    const int64_t first = first_slot(p, b, seg) * per_slot + piece;
+    for (int32_t i = 0; i + 1 < ns; ++i) {
+        const int64_t at = first + i * per_slot;
+        f32x4 *s = reinterpret_cast<f32x4 *>(states + at * (NT * 1024) + quad * 4);
+        S = S * decays[at] + *s;
+        *s = S;
+    }
+}
+
+template <int NT, int W, bool VEC>
+hipError_t launch_w(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
+    const int32_t pbs = (p.P + kPW - 1) / kPW, units = p.per_group * pbs, blocks = (units + W - 1) / W;
+    const auto grid = [&](int64_t places) { return dim3(uint32_t((places * p.G + 7) / 8 * 8 * blocks)); };
+    if (!plan.seg) {
+        ssm_chunk_kernel<NT, W, VEC, kWhole>
+            <<<grid(p.batch), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, p.batch, 0, nullptr, nullptr, svec);
+        return hipGetLastError();
+    }
+    float *states = static_cast<float *>(workspace);
+    const int64_t pieces = int64_t(p.G) * units;
+    float *decays = states + plan.slots * pieces * (NT * 1024);
+    ssm_chunk_kernel<NT, W, VEC, kStates>
+        <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
+    ssm_pass_kernel<NT><<<dim3(uint32_t(p.batch * pieces * NT)), dim3(256), 0, s>>>(p, units, pbs, plan.seg, states, decays, svec);
+    ssm_chunk_kernel<NT, W, VEC, kSegment>
+        <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
+    return hipGetLastError();
+}
+
+template <int NT, bool VEC>
+hipError_t launch_nt(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
+    if (plan.waves == 8) return launch_w<NT, 8, VEC>(p, svec, plan, workspace, s);
+    return plan.waves == 4 ? launch_w<NT, 4, VEC>(p, svec, plan, workspace, s) : launch_w<NT, 2, VEC>(p, svec, plan, workspace, s);
+}
+
+}  // namespace
+
+hipError_t launch_ssm_chunk(const SsmParams &p, bool vec, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
+    switch (plan.nt) {
+        case 1: return vec ? launch_nt<1, true>(p, svec, plan, workspace, s) : launch_nt<1, false>(p, svec, plan, workspace, s);
+        case 2: return vec ? launch_nt<2, true>(p, svec, plan, workspace, s) : launch_nt<2, false>(p, svec, plan, workspace, s);
+        default: return vec ? launch_nt<4, true>(p, svec, plan, workspace, s) : launch_nt<4, false>(p, svec, plan, workspace, s);
+    }
+}
+
+}  // namespace sconv

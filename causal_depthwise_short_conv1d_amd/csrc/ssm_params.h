@@ -70,10 +70,28 @@ inline int norm_threads(int32_t size) {
     return n;
 }
 
+constexpr int kSsmChunk = 64;          // tokens of a chunk
+constexpr int kSsmMaxChunkN = 128;     // states a channel of the chunked kernel
+
+// How the chunked kernel takes a call: its shapes, and whether sequences are cut into segments of `seg` chunks (0: they
+// are not) that are walked at once.
+struct SsmPlan {
+    int32_t nt;                        // 32-state tiles: 1, 2 or 4
+    int32_t waves;                     // a workgroup
+    int32_t seg;
+    int64_t slots;                     // of segments
+    int64_t groups;                    // workgroups of a place (a sequence or slot)
+    int64_t bytes;                     // workspace
+};
+SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int32_t N, bool workspace);
+
 // Launchers: each enqueues its kernels and returns hipGetLastError().
 // `head`: one step size and one decay a head.  `vec`: unit strides of B, C and the
 // state, and every base and stride of theirs keeps four elements together.
 hipError_t launch_ssm_recurrent(const SsmParams &p, bool head, bool vec, hipStream_t s);
+// `vec`: unit strides of x, B, C, z and out, every base and stride of 8 elements; `svec`: the state's rows in 16-byte
+// pieces.  The head form, up to kSsmMaxChunkN states.
+hipError_t launch_ssm_chunk(const SsmParams &p, bool vec, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s);
 // `vec`: unit channel strides, every base and stride of 8 elements.
 hipError_t launch_group_norm(const NormParams &p, bool vec, hipStream_t s);
 

@@ -628,7 +628,14 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  * to its line (a sequence of no tokens writes nothing).  state may be NULL:
  * zero states, none written.  Rows of skipped sequences and rows behind the
  * last sequence are left untouched.
- * workspace, workspace_bytes: reserved; NULL and 0.
+ * Heads with one decay and up to 128 states a channel are processed in chunks of
+ * 64 tokens on the matrix cores.  In a chunk an infinity or NaN in a token's x may
+ * reach the other tokens of its chunk, sequence and head, earlier ones too.
+ * workspace    device memory, 16-byte aligned, in use until the call's work is
+ *              done, or NULL.  With ssm_fwd_workspace_bytes() bytes of it, calls
+ *              of few heads and long sequences take three kernels that walk all
+ *              segments of their sequences at once.  Smaller than asked for ->
+ *              SCONV_ERR_SHAPE.
  */
 int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,
                    const void *dt, int64_t dt_stride_tok, int64_t dt_stride_head, int64_t dt_stride_dim, int32_t dt_fp32,
@@ -646,6 +653,11 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
                    int32_t state_dim, int32_t pad_slot_id,
                    void *out, int64_t o_stride_tok, int64_t o_stride_head, int64_t o_stride_dim,
                    void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that ssm_fwd_varlen makes use of (0: none).  per_channel:
+ * one step size a channel and one decay a channel and state. */
+int64_t ssm_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                                int32_t state_dim, int32_t per_channel);
 
 /*
  * ssm_update -- decode: each of `batch` entries feeds `seqlen` tokens, from the
