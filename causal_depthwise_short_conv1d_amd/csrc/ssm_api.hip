@@ -80,9 +80,11 @@ namespace sconv {
 SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int32_t N, bool workspace) {
     SsmPlan plan = {};
     plan.nt = N <= 32 ? 1 : (N <= 64 ? 2 : 4);
-    const int64_t units = int64_t(H / G) * ((int64_t(P) + 31) / 32);         // of a group, a wave each
-    plan.waves = units > 4 ? 8 : (units > 2 ? 4 : 2);
-    plan.groups = G * ((units + plan.waves - 1) / plan.waves);
+    plan.pair = P > 32;
+    const int64_t units = int64_t(H / G) * (plan.pair ? (int64_t(P) + 63) / 64 : 1);       // of a group
+    const int64_t waves = units * (plan.pair ? 2 : 1);
+    plan.waves = waves > 2 ? 8 : 2;
+    plan.groups = G * ((waves + plan.waves - 1) / plan.waves);
     // a place takes a CU a workgroup: segments, until there is one for each of 256
     const int64_t chunks = T / kSsmChunk + batch, mean = T / kSsmChunk / batch;
     if (workspace && batch * plan.groups < 192 && mean >= 4) {
@@ -91,7 +93,7 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
         if (seg < mean) {
             plan.seg = int32_t(seg);
             plan.slots = T / (kSsmChunk * seg) + batch + 1;
-            plan.bytes = plan.slots * G * units * (plan.nt * 1024 + 1) * 4;
+            plan.bytes = plan.slots * G * waves * (plan.nt * 1024 + 1) * 4;
         }
     }
     return plan;
@@ -178,11 +180,12 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
                 if (overlap(sw, span_of_out(p, 1, T)) || overlap(sw, span_of_state(p)) || overlaps_input(p, 1, T, sw))
                     return SCONV_ERR_ALIAS;
             }
-            const auto rows = [&](const void *a, const GdrTensor &t, int32_t heads) {
-                return !a || (t.sd == 1 && groups_of(a, 8, 2, {T, heads}, {t.st, t.sh}));
+            // rows longer than what is read of them, a chunk's within the 31 bits of a descriptor's offsets
+            const auto rows = [&](const void *a, const GdrTensor &t, int32_t heads, int32_t n) {
+                return !a || (t.sd == 1 && n % 8 == 0 && n <= t.st && t.st < (1 << 23) && groups_of(a, 8, 2, {T, heads}, {t.st, t.sh}));
             };
-            const bool vec = p.P % 8 == 0 && p.N % 8 == 0 && rows(p.x, p.xs, p.H) && rows(p.z, p.zs, p.H) &&
-                             rows(p.out, p.os, p.H) && rows(p.B, p.bs, p.G) && rows(p.C, p.cs, p.G);
+            const bool vec = rows(p.x, p.xs, p.H, p.P) && rows(p.z, p.zs, p.H, p.P) && rows(p.out, p.os, p.H, p.P) &&
+                             rows(p.B, p.bs, p.G, p.N) && rows(p.C, p.cs, p.G, p.N);
             const bool svec = p.state && p.N % 4 == 0 && p.s_sn == 1 &&
                               groups_of(p.state, 4, 4, {p.num_lines, p.H, p.P}, {p.s_sl, p.s_sh, p.s_sp});
             return launch_status(launch_ssm_chunk(p, vec, svec, plan, workspace, stream));

@@ -9,7 +9,8 @@
 // A wave owns 32 channels of one head: their states in its registers, the chunk's
 // x in a piece of LDS of its own.  The waves of a workgroup belong to one group
 // and share its B and C, which come to LDS a chunk ahead, without passing
-// registers (two buffers, one barrier a chunk).
+// registers.  Two waves (w and w + W / 2, on one SIMD) hold 64 channels of a head:
+// one prepares the decays and a third of the scores, the other the rest.
 //
 // Operands.  v_mfma_f32_32x32x16_bf16: a result has its column in the lane and
 // rows (q % 4) + 8 (q / 4) + 4 (l / 32) in its registers q; an operand has its row
@@ -45,6 +46,8 @@ struct alignas(16) Factors {
     float v[kC];                       // e^(R - G) d
     float vx[kC / 2];                  // e^(R_1 - G) d of the first half
     float relh[kC], rell[kC], d[kC];   // G - R in two parts, in powers of 2, and the step
+    float keep, last;                  // e^G_last, G_last in powers of 2
+    int plain;                         // e^(R - G) does not pass 2^64
 };
 
 // Rows of U 16-byte units in LDS, unit u of row r at u ^ swz(r): 8 neighbouring rows' like units lie in different banks, and so
@@ -55,16 +58,15 @@ __device__ __forceinline__ int swz(int r) {
 }
 
 typedef __attribute__((address_space(3))) void LdsVoid;
-typedef const __attribute__((address_space(1))) void GlobalVoid;
 
-// 16 bytes a lane from memory to lds + 16 lane, past the registers.
-__device__ __forceinline__ void to_lds(const void *g, void *lds) {
-    __builtin_amdgcn_global_load_lds((GlobalVoid *)g, (LdsVoid *)lds, 16, 0, 0);
+// 16 bytes a lane from byte `at` of r to lds + 16 lane, past the registers.  What lies past r's end may or may not be written
+// as zero: those places hold zeros or an earlier chunk's rows.
+__device__ __forceinline__ void to_lds(Rsrc r, uint32_t at, void *lds) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsVoid *)lds, 16, at, 0, 0, 0);
 }
 // What this wave has on its way to LDS is there.
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-__device__ __forceinline__ bf16x8 read16(const uint16_t *lds) { return *reinterpret_cast<const bf16x8 *>(lds); }
 __device__ __forceinline__ f32x4 row4(const float *v) { return *reinterpret_cast<const f32x4 *>(v); }
 
 // Transposed: lane l gets column l % 16 of its 16 lanes' 4 rows; it names row (l % 16) / 4, columns 4 (l % 4) ..
@@ -72,19 +74,23 @@ __device__ __forceinline__ s16x4 read_tr(const uint16_t *lds) {
     typedef __attribute__((address_space(3))) s16x4 L;
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((L *)lds);
 }
-// 16 tokens from t0 on (contracted: 8 (e / 4) + 4 (l / 32) + e % 4) of the 32 columns from unit u0 on, a column (bits 2 and 3
+// 16 tokens from t0 on (contracted: 8 (e / 4) + 4 (l / 32) + e % 4) of the 32 columns of tile i, a column (bits 2 and 3
 // swapped) a lane.
 template <int U>
-__device__ __forceinline__ bf16x8 read_cols(const uint16_t *lds, int t0, int u0, int lane) {
-    const int r = ((lane & 15) >> 2) + 4 * (lane >> 5), c = lane & 3;
-    const int u = u0 + 2 * ((lane >> 4) & 1) + (c & 1), o = 4 * (c >> 1);
+__device__ __forceinline__ bf16x8 read_cols(const uint16_t *lds, int t0, int i, int lane) {
+    const int r = ((lane & 15) >> 2) + 4 * (lane >> 5), c = lane & 3;          // (t0 is a multiple of 16: swz goes by r)
+    const int u = (2 * ((lane >> 4) & 1) + (c & 1)) ^ swz<U>(r), o = 4 * (c >> 1);
+    const uint16_t *base = lds + (r * U + (u ^ (4 * (i & 1)))) * 8 + o;
     union { s16x4 s[2]; bf16x8 b; } x;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int t = t0 + 8 * i + r;
-        x.s[i] = read_tr(lds + (t * U + (u ^ swz<U>(t))) * 8 + o);
-    }
+    x.s[0] = read_tr(base + t0 * U * 8 + 64 * (i >> 1));
+    x.s[1] = read_tr(base + (t0 + 8) * U * 8 + 64 * (i >> 1));
     return x.b;
+}
+// Rows r0 + l % 32, columns 16 k + 8 (l / 32) ..
+template <int U>
+__device__ __forceinline__ bf16x8 read_rows(const uint16_t *lds, int r0, int k, int lane) {
+    const int n = lane & 31, u = ((lane >> 5) ^ swz<U>(n)) ^ (2 * (k & 3));
+    return *reinterpret_cast<const bf16x8 *>(lds + (n * U + u) * 8 + r0 * U * 8 + 64 * (k >> 2));
 }
 
 __device__ __forceinline__ f32x16 mfma(const bf16x8 &a, const bf16x8 &b, const f32x16 &c) {
@@ -146,38 +152,50 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *row, int64_t sd, int c, i
     return r;
 }
 
-// What a workgroup does: chunks [c0, c1) of sequence b, for the heads of `group` from unit u0 on.
+// What a workgroup does: chunks [c0, c1) of a sequence, for a group's heads.
 struct Job {
-    int32_t group, u0;
+    int32_t group;
     int32_t t0, n;                     // the sequence's first row and length
     int32_t c0, c1;
 };
 
+// Rows of a chunk from the sequence's row c * kC on, through a descriptor that ends behind the sequence's last row.
+__device__ __forceinline__ Rsrc chunk_rsrc(const uint16_t *t, int64_t st, const Job &job, int32_t c) {
+    const int32_t left = job.n - c * kC < kC ? job.n - c * kC : kC;
+    return make_rsrc(t + (int64_t(job.t0) + c * kC) * st, left * st * 2);
+}
+
 enum Mode { kWhole, kStates, kSegment };
+
+// A tile of scores as an operand of its product with x: two steps of 16 tokens, high and low parts.
+struct Scores { bf16x8 hi[2], lo[2]; };
 
 template <int NT, bool VEC>
 struct Wave {
     static constexpr int U = 4 * NT;   // units of a row of B and C
     const SsmParams &p;
     const Job job;
-    const int lane;
-    const int32_t h, pb;               // head, block of 32 channels
-    const float A, bias;
+    const int lane0;
+    const int32_t h, ch0;              // head, first channel
     uint16_t *xl;                      // [kC][kPW], this wave's
-    Factors &f;
     f32x16 S[NT];                      // S^T: n = 32 nt + 16 (q / 8) + 8 (l / 32) + q % 8 of channel chan()
-    float dt;                          // of the next chunk, a token a lane
 
-    __device__ __forceinline__ int32_t chan() const {
+    // The lane number anew, as a value that the compiler takes for unknown: addresses computed from it stay in their phase.
+    __device__ __forceinline__ int fresh() const {
+        int lane = lane0;
+        asm volatile("" : "+v"(lane));
+        return lane;
+    }
+    __device__ __forceinline__ int32_t chan(int lane) const {
         const int r = lane & 31;
-        return kPW * pb + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
+        return ch0 + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < NT; ++i) S[i] = zero16();
     }
     template <class F>
-    __device__ __forceinline__ void state_rows(F fn) {
+    __device__ __forceinline__ void state_rows(int lane, F fn) {
         const int hh = lane >> 5;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -185,11 +203,12 @@ struct Wave {
             for (int k = 0; k < 4; ++k) fn(i, 4 * k, 32 * i + 16 * (k >> 1) + 8 * hh + 4 * (k & 1));
     }
     __device__ __forceinline__ void load(const float *rows, bool svec) {
-        const int32_t c = chan();
+        const int lane = fresh();
+        const int32_t c = chan(lane);
         zero();
         if (c >= p.P) return;
         const float *row = rows + c * p.s_sp;
-        state_rows([&](int i, int q, int n) {
+        state_rows(lane, [&](int i, int q, int n) {
             if (svec) {
                 if (n < p.N) {
                     const f32x4 v = row4(row + n);
@@ -204,10 +223,11 @@ struct Wave {
         });
     }
     __device__ __forceinline__ void save(float *rows, bool svec) {
-        const int32_t c = chan();
+        const int lane = fresh();
+        const int32_t c = chan(lane);
         if (c >= p.P) return;
         float *row = rows + c * p.s_sp;
-        state_rows([&](int i, int q, int n) {
+        state_rows(lane, [&](int i, int q, int n) {
             if (svec) {
                 if (n < p.N) *reinterpret_cast<f32x4 *>(row + n) = f32x4{S[i][q], S[i][q + 1], S[i][q + 2], S[i][q + 3]};
             } else {
@@ -219,6 +239,7 @@ struct Wave {
     }
     // As the registers lie: 16 bytes a lane, 4 NT pieces.
     __device__ __forceinline__ void load_raw(const float *at) {
+        const int lane = fresh();
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -229,6 +250,7 @@ struct Wave {
             }
     }
     __device__ __forceinline__ void save_raw(float *at) {
+        const int lane = fresh();
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -237,32 +259,36 @@ struct Wave {
                     f32x4{S[i][4 * k], S[i][4 * k + 1], S[i][4 * k + 2], S[i][4 * k + 3]};
     }
 
-    // The row of a chunk's token; behind the sequence's end its last one, whose step counts as 0.
-    __device__ __forceinline__ int64_t row_of(int32_t c, int t) const {
-        const int32_t r = c * kC + t;
-        return int64_t(job.t0) + (r < job.n ? r : job.n - 1);
-    }
-    __device__ __forceinline__ void fetch_dt(int32_t c) {
-        const int64_t at = row_of(c, lane) * p.ds.st + h * p.ds.sh;
-        dt = p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
+    // The step size's input of a chunk's token, a token a lane; behind the sequence's end its last one (which counts as 0).
+    __device__ __forceinline__ float fetch_dt(int32_t c) const {
+        const int32_t r = c * kC + lane0;
+        const int64_t at = (int64_t(job.t0) + (r < job.n ? r : job.n - 1)) * p.ds.st + h * p.ds.sh;
+        return p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
     }
     // The wave's x of a chunk on its way to LDS.
     __device__ __forceinline__ void fetch_x(int32_t c) {
+        const int lane = fresh(), t0 = lane >> 2, u = (lane & 3) ^ swz<4>(t0);
+        const int32_t ch = ch0 + 8 * u;
+        if constexpr (VEC) {
+            const Rsrc r = chunk_rsrc(p.x + h * p.xs.sh, p.xs.st, job, c);
+            const uint32_t row = uint32_t(p.xs.st) * 2, at = t0 * row + uint32_t(ch) * 2;
+            if (ch < p.P) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = 64 * k + lane, t = at >> 2, u = (at & 3) ^ swz<4>(t);
-            const int ch = kPW * pb + 8 * u;
-            const uint16_t *row = p.x + row_of(c, t) * p.xs.st + h * p.xs.sh;
-            if constexpr (VEC) {
-                if (ch < p.P) to_lds(row + ch, xl + 64 * 8 * k);
-            } else {
-                *reinterpret_cast<u32x4 *>(xl + at * 8) = load8(row, p.xs.sd, ch, p.P);
+                for (int k = 0; k < 4; ++k) to_lds(r, at + 16 * k * row, xl + 512 * k);
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int32_t t = c * kC + 16 * k + t0;
+                const int64_t row = int64_t(job.t0) + (t < job.n ? t : job.n - 1);
+                *reinterpret_cast<u32x4 *>(xl + (64 * k + lane) * 8) = load8(p.x + row * p.xs.st + h * p.xs.sh, p.xs.sd, ch, p.P);
             }
         }
     }
 
-    // The factors of chunk c from its dt; returns e^G_last, and whether the halves' decays are small enough for products.
-    __device__ __forceinline__ float factors(int32_t c, bool &plain, double &total) {
+    // The factors of chunk c from its dt.
+    __device__ __forceinline__ void factors(int32_t c, float dt, float A, float bias, Factors &f) {
+        const int lane = fresh();
         float d = dt + bias;
         if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
         d = d < p.dt_min ? p.dt_min : d;
@@ -285,54 +311,64 @@ struct Wave {
         f.u[lane] = __builtin_amdgcn_exp2f(r);
         f.v[lane] = d * __builtin_amdgcn_exp2f(-r);
         if (lane < 32) f.vx[lane] = d * __builtin_amdgcn_exp2f(float(mid - G));
-        plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
-        if (!plain) {
-            f.relh[lane] = r;
-            f.rell[lane] = float(rel - double(r));
-            f.d[lane] = d;
+        const bool plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
+        f.relh[lane] = r;
+        f.rell[lane] = float(rel - double(r));
+        f.d[lane] = d;
+        if (lane == 0) {
+            f.keep = __builtin_amdgcn_exp2f(float(last));
+            f.last = float(last);
+            f.plain = plain;
         }
-        total += last;
-        return __builtin_amdgcn_exp2f(float(last));
     }
 
     // x^T: channel chan() a lane, 16 tokens each.
     __device__ __forceinline__ void read_x(bf16x8 (&x)[4]) {
+        const int lane = fresh();
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = read_cols<4>(xl, 16 * k, 0, lane);
     }
 
     // S <- e^G_last S + sum_j w_j x_j B_j^T
-    __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], float keep) {
-        const int hh = lane >> 5;
+    __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], const Factors &f) {
+        const int lane = fresh(), hh = lane >> 5;
+        const float keep = f.keep;
 #pragma unroll
         for (int i = 0; i < NT; ++i) S[i] *= keep;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const f32x4 w0 = row4(f.w + 16 * k + 4 * hh), w1 = row4(f.w + 16 * k + 8 + 4 * hh);
-            const u32x4 xr = __builtin_bit_cast(u32x4, x[k]);
             float xw[8];
-            unpack8(xr, xw);
+            unpack8(__builtin_bit_cast(u32x4, x[k]), xw);
 #pragma unroll
             for (int e = 0; e < 4; ++e) { xw[e] *= w0[e]; xw[4 + e] *= w1[e]; }
-            bf16x8 hi, mid, lo;
+            bf16x8 hi, mid, lo, b[NT];
             split3(xw, hi, mid, lo);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const bf16x8 b = read_cols<U>(B, 16 * k, 4 * i, lane);
-                S[i] = mfma(b, hi, S[i]);
-                S[i] = mfma(b, mid, S[i]);
-                S[i] = mfma(b, lo, S[i]);
-            }
+            for (int i = 0; i < NT; ++i) b[i] = read_cols<U>(B, 16 * k, i, lane);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], hi, S[i]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], mid, S[i]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], lo, S[i]);
         }
     }
 
-    // A tile of scores to the two operands of their product with x.  DIAG: tokens of one half (masked, D on the diagonal).
+    // B_j . C_i of a tile, j = 32 jt .., i = 32 it ..
+    __device__ __forceinline__ f32x16 score(const uint16_t *B, const uint16_t *C, int jt, int it) {
+        const int lane = fresh();
+        f32x16 s = zero16();
+#pragma unroll
+        for (int k = 0; k < 2 * NT; ++k) s = mfma(read_rows<U>(B, 32 * jt, k, lane), read_rows<U>(C, 32 * it, k, lane), s);
+        return s;
+    }
+    // ... times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).
     template <bool DIAG>
-    __device__ __forceinline__ void weigh(f32x16 &s, int half, bool plain, float D, bf16x8 (&hi)[2], bf16x8 (&lo)[2]) {
-        const int n = lane & 31, hh = lane >> 5;
-        const float ui = f.u[32 * (DIAG ? half : 1) + n];
+    __device__ __forceinline__ Scores weigh(const f32x16 &s, int half, const Factors &f, float D) {
+        const int lane = fresh(), n = lane & 31, hh = lane >> 5;
         float v[16];
-        if (DIAG && !plain) {
+        if (DIAG && !__builtin_amdgcn_readfirstlane(f.plain)) {
             const float ih = f.relh[32 * half + n], il = f.rell[32 * half + n];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -345,6 +381,7 @@ struct Wave {
                 }
             }
         } else {
+            const float ui = f.u[32 * half + n];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const f32x4 vj = row4((DIAG ? f.v + 32 * half : f.vx) + 8 * k + 4 * hh);
@@ -359,32 +396,42 @@ struct Wave {
                 v[q] = j < n ? v[q] : (j == n ? v[q] + D : 0.0f);
             }
         }
+        Scores r;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = v[8 * k + e];
-            split2(t, hi[k], lo[k]);
+            split2(t, r.hi[k], r.lo[k]);
         }
+        return r;
+    }
+    static __device__ __forceinline__ void put(const Scores &s, uint16_t *at, int lane) {
+        bf16x8 *o = reinterpret_cast<bf16x8 *>(at) + lane;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) { o[128 * k] = s.hi[k]; o[128 * k + 64] = s.lo[k]; }
+    }
+    static __device__ __forceinline__ Scores get(const uint16_t *at, int lane) {
+        const bf16x8 *o = reinterpret_cast<const bf16x8 *>(at) + lane;
+        Scores s;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) { s.hi[k] = o[128 * k]; s.lo[k] = o[128 * k + 64]; }
+        return s;
     }
 
-    // The outputs of a chunk, from the state before it.  D: of the head, 0 where it is per channel.
-    __device__ __forceinline__ void emit(int32_t c, const uint16_t *B, const uint16_t *C, const bf16x8 (&x)[4], bool plain, float D) {
-        const int n = lane & 31, hh = lane >> 5;
-        f32x16 y0 = zero16(), y1 = zero16(), s00 = zero16(), s01 = zero16(), s11 = zero16();
+    // y = e^G_i (S C_i), tokens 32 it + l % 32 a lane
+    __device__ __forceinline__ void from_state(const uint16_t *C, const Factors &f, f32x16 &y0, f32x16 &y1) {
+        const int lane = fresh(), n = lane & 31;
+        y0 = zero16();
+        y1 = zero16();
 #pragma unroll
         for (int k = 0; k < 2 * NT; ++k) {
-            const int u = (2 * k + hh) ^ swz<U>(n);    // (rows n and n + 32 are swizzled alike)
-            const bf16x8 b0 = read16(B + (n * U + u) * 8), b1 = read16(B + ((n + 32) * U + u) * 8);
-            const bf16x8 c0 = read16(C + (n * U + u) * 8), c1 = read16(C + ((n + 32) * U + u) * 8);
+            const bf16x8 c0 = read_rows<U>(C, 0, k, lane), c1 = read_rows<U>(C, 32, k, lane);
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = S[k >> 1][8 * (k & 1) + e];
             bf16x8 hi, lo;
             split2(t, hi, lo);
-            s00 = mfma(b0, c0, s00);
-            s01 = mfma(b0, c1, s01);
-            s11 = mfma(b1, c1, s11);
             y0 = mfma(hi, c0, y0);
             y1 = mfma(hi, c1, y1);
             y0 = mfma(lo, c0, y0);
@@ -392,37 +439,23 @@ struct Wave {
         }
         y0 *= f.eG[n];
         y1 *= f.eG[32 + n];
-        bf16x8 hi[2], lo[2];
-        weigh<true>(s00, 0, plain, D, hi, lo);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            y0 = mfma(x[k], hi[k], y0);
-            y0 = mfma(x[k], lo[k], y0);
-        }
-        weigh<false>(s01, 1, plain, D, hi, lo);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            y1 = mfma(x[k], hi[k], y1);
-            y1 = mfma(x[k], lo[k], y1);
-        }
-        weigh<true>(s11, 1, plain, D, hi, lo);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            y1 = mfma(x[2 + k], hi[k], y1);
-            y1 = mfma(x[2 + k], lo[k], y1);
-        }
-        store(c, n, y0);
-        store(c, 32 + n, y1);
+    }
+    static __device__ __forceinline__ void add(f32x16 &y, const bf16x8 &xa, const bf16x8 &xb, const Scores &s) {
+        y = mfma(xa, s.hi[0], y);
+        y = mfma(xb, s.hi[1], y);
+        y = mfma(xa, s.lo[0], y);
+        y = mfma(xb, s.lo[1], y);
     }
 
-    // Token t's 16 outputs of this lane: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the block.
-    __device__ __forceinline__ void store(int32_t c, int t, const f32x16 &y) {
-        const int32_t r = c * kC + t;
+    // Outputs of the lane's token of half `it`: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the wave's.
+    __device__ __forceinline__ void store(int32_t c, int it, const f32x16 &y) {
+        const int lane = fresh();
+        const int32_t r = c * kC + 32 * it + (lane & 31);
         if (r >= job.n) return;
         const int64_t row = int64_t(job.t0) + r;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int32_t ch = kPW * pb + 16 * k + 8 * (lane >> 5);
+            const int32_t ch = ch0 + 16 * k + 8 * (lane >> 5);
             if (ch >= p.P) continue;
             float v[8];
 #pragma unroll
@@ -454,26 +487,26 @@ struct Wave {
     }
 };
 
-// B and C of a chunk on their way to LDS, by all of a workgroup's waves.
+// Rows of B or C of a chunk on their way to LDS, by all of a workgroup's waves.
 template <int NT, int W, bool VEC>
-__device__ __forceinline__ void fetch_bc(const SsmParams &p, const Job &job, int32_t c, uint16_t *B, uint16_t *C, bool with_c) {
-    constexpr int U = 4 * NT, kPieces = kC * U / 64;               // a wave brings 64 units at a time
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+__device__ __forceinline__ void fetch_rows(const uint16_t *t, const GdrTensor &ts, int32_t N, const Job &job, int32_t c,
+                                           uint16_t *lds, int wave, int lane) {
+    constexpr int U = 4 * NT, kPieces = kC * U / 64, kRows = 64 / U;           // a piece: 64 units, kRows rows
+    asm volatile("" : "+v"(lane));
+    const uint32_t row = uint32_t(ts.st) * 2;
+    const uint16_t *base = t + job.group * ts.sh;
+    const Rsrc r = chunk_rsrc(base, ts.st, job, c);
 #pragma unroll
     for (int k = 0; k < (kPieces + W - 1) / W; ++k) {
-        if (kPieces % W != 0 && wave + k * W >= kPieces) break;
-        const int first = (wave + k * W) * 64, at = first + lane, t = at / U, u = (at % U) ^ swz<U>(t);
-        const int32_t r = c * kC + t;
-        const int64_t row = int64_t(job.t0) + (r < job.n ? r : job.n - 1);
-        const uint16_t *br = p.B + row * p.bs.st + job.group * p.bs.sh, *cr = p.C + row * p.cs.st + job.group * p.cs.sh;
+        const int piece = wave + k * W;
+        if (kPieces % W != 0 && piece >= kPieces) break;
+        const int tt = piece * kRows + lane / U, u = (lane % U) ^ swz<U>(tt);
         if constexpr (VEC) {
-            if (8 * u < p.N) {
-                to_lds(br + 8 * u, B + first * 8);
-                if (with_c) to_lds(cr + 8 * u, C + first * 8);
-            }
+            if (8 * u < N) to_lds(r, tt * row + 16 * u, lds + piece * 512);
         } else {
-            *reinterpret_cast<u32x4 *>(B + at * 8) = load8(br, p.bs.sd, 8 * u, p.N);
-            if (with_c) *reinterpret_cast<u32x4 *>(C + at * 8) = load8(cr, p.cs.sd, 8 * u, p.N);
+            const int32_t at = c * kC + tt;
+            const int64_t rr = int64_t(job.t0) + (at < job.n ? at : job.n - 1);
+            *reinterpret_cast<u32x4 *>(lds + (piece * 64 + lane) * 8) = load8(base + rr * ts.st, ts.sd, 8 * u, N);
         }
     }
 }
@@ -511,24 +544,26 @@ __device__ __forceinline__ int64_t first_slot(const SsmParams &p, int32_t b, int
 
 struct alignas(16) Raw { float v[4]; };
 
-template <int NT, int W, bool VEC, Mode MODE>
+// PAIR: two waves a block of 64 channels of a head, which share its scores; otherwise a wave for up to 32 channels.
+template <int NT, int W, bool PAIR, bool VEC, Mode MODE>
 __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
                                                                           int64_t places, int32_t seg, float *states, float *decays,
                                                                           bool svec) {
-    constexpr int U = 4 * NT, kBC = kC * U * 8;
-    __shared__ alignas(16) uint16_t B[2][kBC], C[MODE == kStates ? 1 : 2][MODE == kStates ? 8 : kBC];
+    constexpr int U = 4 * NT, kBC = kC * U * 8, kUnits = PAIR ? W / 2 : W;
+    constexpr bool kOut = MODE != kStates;
+    __shared__ alignas(16) uint16_t B[2][kBC], C[kOut ? 2 : 1][kOut ? kBC : 8];
     __shared__ alignas(16) uint16_t xl[W][kC * kPW];
-    __shared__ Factors factors[W];
+    __shared__ alignas(16) uint16_t scores[kOut && PAIR ? kUnits : 1][kOut && PAIR ? 3 * 2048 : 8];
+    __shared__ Factors factors[kUnits][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
 
     // Blocks go to the 8 XCDs in turn: those of one place and group, which read the same B and C, follow each other on one.
-    const int64_t at = blockIdx.x >> 3, pg = at / blocks * 8 + (blockIdx.x & 7);
-    const int32_t block = int32_t(at % blocks);
-    if (pg >= places * p.G) return;
-    const int64_t place = pg / p.G;
+    const uint32_t at = blockIdx.x >> 3, pg = at / uint32_t(blocks) * 8 + (blockIdx.x & 7);
+    const int32_t block = int32_t(at % uint32_t(blocks));
+    const uint32_t place = pg / uint32_t(p.G);
+    if (place >= places) return;
     Job job;
-    job.group = int32_t(pg - place * p.G);
-    job.u0 = block * W;
+    job.group = int32_t(pg - place * uint32_t(p.G));
     SsmSpan sp;
     int64_t slot = 0;
     int32_t b = int32_t(place);
@@ -558,60 +593,90 @@ __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmPa
         job.c1 = job.c0 + seg < nc ? job.c0 + seg : nc;
     }
 
-    // columns that no row has stay zero
-    if (8 * U > p.N || p.P % kPW != 0) {
-        for (int i = threadIdx.x; i < 2 * kBC / 8; i += 64 * W) {
-            reinterpret_cast<u32x4 *>(&B[0][0])[i] = u32x4{0, 0, 0, 0};
-            if (MODE != kStates) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
-        }
-        for (int i = threadIdx.x; i < W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0])[i] = u32x4{0, 0, 0, 0};
-        __syncthreads();
+    // columns and rows that a chunk may lack
+    for (int i = threadIdx.x; i < 2 * kBC / 8; i += 64 * W) {
+        reinterpret_cast<u32x4 *>(&B[0][0])[i] = u32x4{0, 0, 0, 0};
+        if (kOut) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
     }
+    for (int i = threadIdx.x; i < W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0])[i] = u32x4{0, 0, 0, 0};
+    __syncthreads();
 
-    const int32_t unit = job.u0 + wave;
-    const bool work = unit < units;
+    const int half = PAIR ? wave / kUnits : 0, own = PAIR ? wave % kUnits : wave;
+    const int32_t unit = block * kUnits + own;
+    const bool work = unit < units, first = half == 0, second = !PAIR || half == 1;
     const int32_t h = job.group * p.per_group + (work ? unit / pbs : 0), pb = work ? unit % pbs : 0;
-    Wave<NT, VEC> wv{p, job, lane, h, pb, p.A.p[h * p.A.sh], p.bias.p ? p.bias.p[h * p.bias.sh] : 0.0f, xl[wave], factors[wave]};
+    Wave<NT, VEC> wv{p, job, lane, h, (PAIR ? 64 : 32) * pb + 32 * half, xl[wave]};
+    uint16_t *sc = scores[kOut && PAIR ? own : 0];
     float *rows = p.state ? p.state + sp.line * p.s_sl + h * p.s_sh : nullptr;
-    const int64_t per_slot = int64_t(p.G) * units;
-    const int64_t piece = job.group * units + unit;
+    const int64_t per_slot = int64_t(p.G) * units * (PAIR ? 2 : 1);
+    const int64_t piece = (int64_t(job.group) * units + unit) * (PAIR ? 2 : 1) + half;
+    const float A = p.A.p[h * p.A.sh], bias = p.bias.p ? p.bias.p[h * p.bias.sh] : 0.0f;
+    const float D = kOut && p.D.p && p.D.sd == 0 ? p.D.p[h * p.D.sh] : 0.0f;
+    float dt = 0.0f;
     wv.zero();
+    fetch_rows<NT, W, VEC>(p.B, p.bs, p.N, job, job.c0, B[0], wave, lane);
+    if (kOut) fetch_rows<NT, W, VEC>(p.C, p.cs, p.N, job, job.c0, C[0], wave, lane);
     if (work) {
+        wv.fetch_x(job.c0);
         if (MODE != kStates && job.c0 == 0) {
             if (sp.init) wv.load(rows, svec);
         } else if (MODE == kSegment) {
             wv.load_raw(states + ((slot - 1) * per_slot + piece) * (NT * 1024));
         }
-        wv.fetch_dt(job.c0);
-        wv.fetch_x(job.c0);
+        if (first) wv.factors(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
     }
-    fetch_bc<NT, W, VEC>(p, job, job.c0, B[0], C[0], MODE != kStates);
-    const float D = MODE != kStates && p.D.p && p.D.sd == 0 ? p.D.p[h * p.D.sh] : 0.0f;
-    double total = 0.0;
+    float total = 0.0f;
     landed();
     __syncthreads();
     for (int32_t c = job.c0; c < job.c1; ++c) {
         const int cur = (c - job.c0) & 1;
         const bool more = c + 1 < job.c1;
+        const Factors &f = factors[own][cur];
         bf16x8 x[4];
-        bool plain = true;
-        float keep = 1.0f;
-        if (work) {
-            wv.read_x(x);
-            keep = wv.factors(c, plain, total);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (work) wv.read_x(x);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // x is in registers: its place is free
         if (more) {
             if (work) {
-                wv.fetch_dt(c + 1);
+                if (first) dt = wv.fetch_dt(c + 1);
                 wv.fetch_x(c + 1);
             }
-            fetch_bc<NT, W, VEC>(p, job, c + 1, B[cur ^ 1], MODE == kStates ? C[0] : C[cur ^ 1], MODE != kStates);
+            fetch_rows<NT, W, VEC>(p.B, p.bs, p.N, job, c + 1, B[cur ^ 1], wave, lane);
+            if (kOut) fetch_rows<NT, W, VEC>(p.C, p.cs, p.N, job, c + 1, C[kOut ? cur ^ 1 : 0], wave, lane);
+        }
+        if constexpr (kOut) {
+            f32x16 y0, y1;
+            const uint16_t *Bc = B[cur], *Cc = C[cur];
+            if constexpr (PAIR) {
+                if (work) {
+                    if (first) {
+                        wv.put(wv.template weigh<true>(wv.score(Bc, Cc, 0, 0), 0, f, D), sc, lane);
+                    } else {
+                        wv.put(wv.template weigh<false>(wv.score(Bc, Cc, 0, 1), 1, f, D), sc + 2048, lane);
+                        wv.put(wv.template weigh<true>(wv.score(Bc, Cc, 1, 1), 1, f, D), sc + 4096, lane);
+                    }
+                    wv.from_state(Cc, f, y0, y1);
+                }
+                __syncthreads();
+                if (work) {
+                    wv.add(y0, x[0], x[1], wv.get(sc, lane));
+                    wv.add(y1, x[0], x[1], wv.get(sc + 2048, lane));
+                    wv.add(y1, x[2], x[3], wv.get(sc + 4096, lane));
+                }
+            } else if (work) {
+                wv.from_state(Cc, f, y0, y1);
+                wv.add(y0, x[0], x[1], wv.template weigh<true>(wv.score(Bc, Cc, 0, 0), 0, f, D));
+                wv.add(y1, x[0], x[1], wv.template weigh<false>(wv.score(Bc, Cc, 0, 1), 1, f, D));
+                wv.add(y1, x[2], x[3], wv.template weigh<true>(wv.score(Bc, Cc, 1, 1), 1, f, D));
+            }
+            if (work) {
+                wv.store(c, 0, y0);
+                wv.store(c, 1, y1);
+            }
         }
         if (work) {
-            if constexpr (MODE != kStates) wv.emit(c, B[cur], C[cur], x, plain, D);
-            wv.advance(B[cur], x, keep);
+            if (more && first) wv.factors(c + 1, dt, A, bias, factors[own][cur ^ 1]);
+            wv.advance(B[cur], x, f);
+            if (MODE == kStates) total += f.last;
         }
         landed();
         __syncthreads();
@@ -619,7 +684,7 @@ __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmPa
     if (!work) return;
     if constexpr (MODE == kStates) {
         wv.save_raw(states + (slot * per_slot + piece) * (NT * 1024));
-        if (lane == 0) decays[slot * per_slot + piece] = __builtin_amdgcn_exp2f(float(total));
+        if (lane == 0) decays[slot * per_slot + piece] = __builtin_amdgcn_exp2f(total);
     } else {
         if (p.state && job.c1 == nc) wv.save(rows, svec);
     }
@@ -630,6 +695,7 @@ __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmPa
 template <int NT>
 __global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t units, int32_t pbs, int32_t seg, float *states,
                                                        const float *decays, bool svec) {
+    // units and pbs count 32-channel pieces here
     const int64_t per_slot = int64_t(p.G) * units;
     const int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / (NT * 256);
     if (id >= int64_t(p.batch) * per_slot) return;
@@ -664,30 +730,35 @@ __global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t unit
     }
 }
 
-template <int NT, int W, bool VEC>
+template <int NT, int W, bool PAIR, bool VEC>
 hipError_t launch_w(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
-    const int32_t pbs = (p.P + kPW - 1) / kPW, units = p.per_group * pbs, blocks = (units + W - 1) / W;
+    const int32_t pbs = PAIR ? (p.P + 63) / 64 : 1, units = p.per_group * pbs, per = PAIR ? W / 2 : W;
+    const int32_t blocks = (units + per - 1) / per, halves = PAIR ? 2 : 1;
     const auto grid = [&](int64_t places) { return dim3(uint32_t((places * p.G + 7) / 8 * 8 * blocks)); };
     if (!plan.seg) {
-        ssm_chunk_kernel<NT, W, VEC, kWhole>
+        ssm_chunk_kernel<NT, W, PAIR, VEC, kWhole>
             <<<grid(p.batch), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, p.batch, 0, nullptr, nullptr, svec);
         return hipGetLastError();
     }
     float *states = static_cast<float *>(workspace);
-    const int64_t pieces = int64_t(p.G) * units;
+    const int64_t pieces = int64_t(p.G) * units * halves;
     float *decays = states + plan.slots * pieces * (NT * 1024);
-    ssm_chunk_kernel<NT, W, VEC, kStates>
+    ssm_chunk_kernel<NT, W, PAIR, VEC, kStates>
         <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
-    ssm_pass_kernel<NT><<<dim3(uint32_t(p.batch * pieces * NT)), dim3(256), 0, s>>>(p, units, pbs, plan.seg, states, decays, svec);
-    ssm_chunk_kernel<NT, W, VEC, kSegment>
+    ssm_pass_kernel<NT><<<dim3(uint32_t(p.batch * pieces * NT)), dim3(256), 0, s>>>(p, units * halves, pbs * halves, plan.seg, states,
+                                                                                    decays, svec);
+    ssm_chunk_kernel<NT, W, PAIR, VEC, kSegment>
         <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
     return hipGetLastError();
 }
 
 template <int NT, bool VEC>
 hipError_t launch_nt(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
-    if (plan.waves == 8) return launch_w<NT, 8, VEC>(p, svec, plan, workspace, s);
-    return plan.waves == 4 ? launch_w<NT, 4, VEC>(p, svec, plan, workspace, s) : launch_w<NT, 2, VEC>(p, svec, plan, workspace, s);
+    if (plan.pair)
+        return plan.waves == 8 ? launch_w<NT, 8, true, VEC>(p, svec, plan, workspace, s)
+                               : launch_w<NT, 2, true, VEC>(p, svec, plan, workspace, s);
+    return plan.waves == 8 ? launch_w<NT, 8, false, VEC>(p, svec, plan, workspace, s)
+                           : launch_w<NT, 2, false, VEC>(p, svec, plan, workspace, s);
 }
 
 }  // namespace

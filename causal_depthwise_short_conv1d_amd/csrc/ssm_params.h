@@ -78,6 +78,7 @@ constexpr int kSsmMaxChunkN = 128;     // states a channel of the chunked kernel
 struct SsmPlan {
     int32_t nt;                        // 32-state tiles: 1, 2 or 4
     int32_t waves;                     // a workgroup
+    bool pair;                         // two waves a block of 64 channels of a head, else one for up to 32
     int32_t seg;
     int64_t slots;                     // of segments
     int64_t groups;                    // workgroups of a place (a sequence or slot)
