@@ -83,8 +83,7 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
     plan.pair = P > 32;
     const int64_t units = int64_t(H / G) * (plan.pair ? (int64_t(P) + 63) / 64 : 1);       // of a group
     const int64_t waves = units * (plan.pair ? 2 : 1);
-    plan.waves = waves > 2 ? 8 : 2;
-    plan.groups = G * ((waves + plan.waves - 1) / plan.waves);
+    plan.groups = G * ((waves + kSsmWaves - 1) / kSsmWaves);
     // a place takes a CU a workgroup: segments, until there is one for each of 256
     const int64_t chunks = T / kSsmChunk + batch, mean = T / kSsmChunk / batch;
     if (workspace && batch * plan.groups < 192 && mean >= 4) {
@@ -172,7 +171,7 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
     if (layout.head && p.N <= kSsmMaxChunkN) {
         const SsmPlan plan = ssm_plan(T, batch, p.H, p.G, p.P, p.N, workspace != nullptr);
         const int64_t places = (plan.seg ? plan.slots : batch) + 7;
-        if (places <= kMaxThreads / (64 * plan.waves) / plan.groups && plan.groups <= INT32_MAX) {
+        if (places <= kMaxThreads / (64 * kSsmWaves) / plan.groups && plan.groups <= INT32_MAX) {
             if (plan.bytes) {
                 if (!aligned(workspace, 16)) return SCONV_ERR_ALIGN;
                 if (workspace_bytes < plan.bytes) return SCONV_ERR_SHAPE;

@@ -57,15 +57,34 @@ __device__ __forceinline__ int swz(int r) {
     return U >= 8 ? ((r & 3) << 1 | ((r >> 2) & 1)) : (((r >> 1) & 1) << 1 | ((r >> 2) & 1));
 }
 
-typedef __attribute__((address_space(3))) void LdsVoid;
-
-// 16 bytes a lane from byte `at` of r to lds + 16 lane, past the registers.  What lies past r's end may or may not be written
-// as zero: those places hold zeros or an earlier chunk's rows.
-__device__ __forceinline__ void to_lds(Rsrc r, uint32_t at, void *lds) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsVoid *)lds, 16, at, 0, 0, 0);
+// A descriptor's words, in scalar registers.
+__device__ __forceinline__ u32x4 make_words(const void *base, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    u32x4 r;
+    r.x = __builtin_amdgcn_readfirstlane(uint32_t(a));
+    r.y = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32) & 0xffffu);
+    r.z = __builtin_amdgcn_readfirstlane(uint32_t(bytes < 0x7fffffff ? bytes : 0x7fffffff));
+    r.w = 0x00020000u;
+    return r;
 }
+// 16 bytes a lane from byte `at` of r to lds + 16 lane, past the registers.  What lies past r's end may or may not be written
+// as zero: those places hold zeros or an earlier chunk's rows.  Written as an instruction (it has no register to be written
+// late): the builtin makes the compiler wait for it before the next read of the same array, the other buffer's included, which
+// is a trip to memory in every chunk.  landed() waits for it; no other
+// instruction here goes by m0.
+__device__ __forceinline__ void to_lds(const u32x4 &r, uint32_t at, void *lds) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>(lds)));   // (its place in the LDS)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(r), "s"(to) : "memory");
+}
+// A barrier for what waves exchange through ds_write: what is on its way to LDS past the registers stays on its way.
+__device__ __forceinline__ void exchange() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// Reads that were written before it are issued before what comes after it.
+__device__ __forceinline__ void issued() { __builtin_amdgcn_sched_barrier(0); }
 // What this wave has on its way to LDS is there.
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void landed() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);        // vmcnt(0), as an instruction that the compiler knows: its own loads are over too
+    asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ f32x4 row4(const float *v) { return *reinterpret_cast<const f32x4 *>(v); }
 
@@ -160,9 +179,9 @@ struct Job {
 };
 
 // Rows of a chunk from the sequence's row c * kC on, through a descriptor that ends behind the sequence's last row.
-__device__ __forceinline__ Rsrc chunk_rsrc(const uint16_t *t, int64_t st, const Job &job, int32_t c) {
+__device__ __forceinline__ u32x4 chunk_rsrc(const uint16_t *t, int64_t st, const Job &job, int32_t c) {
     const int32_t left = job.n - c * kC < kC ? job.n - c * kC : kC;
-    return make_rsrc(t + (int64_t(job.t0) + c * kC) * st, left * st * 2);
+    return make_words(t + (int64_t(job.t0) + c * kC) * st, left * st * 2);
 }
 
 enum Mode { kWhole, kStates, kSegment };
@@ -259,18 +278,21 @@ struct Wave {
                     f32x4{S[i][4 * k], S[i][4 * k + 1], S[i][4 * k + 2], S[i][4 * k + 3]};
     }
 
-    // The step size's input of a chunk's token, a token a lane; behind the sequence's end its last one (which counts as 0).
-    __device__ __forceinline__ float fetch_dt(int32_t c) const {
-        const int32_t r = c * kC + lane0;
+    // The bits of the step size's input of a chunk's token, a token a lane (behind the sequence's end anything), loaded without
+    // a branch: a bf16 is the high half.
+    struct Step { uint32_t lo, hi; };
+    __device__ __forceinline__ Step fetch_dt(int32_t c) const {
+        const int32_t r = c * kC + lane0, w = p.dt_fp32 ? 2 : 1;
         const int64_t at = (int64_t(job.t0) + (r < job.n ? r : job.n - 1)) * p.ds.st + h * p.ds.sh;
-        return p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
+        const uint16_t *e = static_cast<const uint16_t *>(p.dt) + at * w;
+        return {e[0], e[w - 1]};
     }
     // The wave's x of a chunk on its way to LDS.
     __device__ __forceinline__ void fetch_x(int32_t c) {
         const int lane = fresh(), t0 = lane >> 2, u = (lane & 3) ^ swz<4>(t0);
         const int32_t ch = ch0 + 8 * u;
         if constexpr (VEC) {
-            const Rsrc r = chunk_rsrc(p.x + h * p.xs.sh, p.xs.st, job, c);
+            const u32x4 r = chunk_rsrc(p.x + h * p.xs.sh, p.xs.st, job, c);
             const uint32_t row = uint32_t(p.xs.st) * 2, at = t0 * row + uint32_t(ch) * 2;
             if (ch < p.P) {
 #pragma unroll
@@ -287,9 +309,9 @@ struct Wave {
     }
 
     // The factors of chunk c from its dt.
-    __device__ __forceinline__ void factors(int32_t c, float dt, float A, float bias, Factors &f) {
+    __device__ __forceinline__ void factors(int32_t c, const Step &dt, float A, float bias, Factors &f) {
         const int lane = fresh();
-        float d = dt + bias;
+        float d = __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias;
         if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
         d = d < p.dt_min ? p.dt_min : d;
         d = d > p.dt_max ? p.dt_max : d;
@@ -333,35 +355,66 @@ struct Wave {
     __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], const Factors &f) {
         const int lane = fresh(), hh = lane >> 5;
         const float keep = f.keep;
+        f32x4 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = row4(f.w + 8 * k + 4 * hh);
+        bf16x8 b[2][NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) b[0][i] = read_cols<U>(B, 0, i, lane);
+        issued();
 #pragma unroll
         for (int i = 0; i < NT; ++i) S[i] *= keep;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const f32x4 w0 = row4(f.w + 16 * k + 4 * hh), w1 = row4(f.w + 16 * k + 8 + 4 * hh);
             float xw[8];
             unpack8(__builtin_bit_cast(u32x4, x[k]), xw);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { xw[e] *= w0[e]; xw[4 + e] *= w1[e]; }
-            bf16x8 hi, mid, lo, b[NT];
+            for (int e = 0; e < 8; ++e) xw[e] *= w[2 * k + (e >> 2)][e & 3];
+            bf16x8 hi, mid, lo;
             split3(xw, hi, mid, lo);
+            if (k < 3) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) b[i] = read_cols<U>(B, 16 * k, i, lane);
+                for (int i = 0; i < NT; ++i) b[(k + 1) & 1][i] = read_cols<U>(B, 16 * k + 16, i, lane);
+                issued();
+            }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], hi, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], hi, S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], mid, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], mid, S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[i], lo, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], lo, S[i]);
         }
     }
 
-    // B_j . C_i of a tile, j = 32 jt .., i = 32 it ..
-    __device__ __forceinline__ f32x16 score(const uint16_t *B, const uint16_t *C, int jt, int it) {
+    // B_j . C_i of NJ tiles, j = 32 (jt + 0, 1) .., i = 32 it ..; four steps' operands are read before the last four's products.
+    template <int NJ>
+    __device__ __forceinline__ void score(const uint16_t *B, const uint16_t *C, int jt, int it, f32x16 (&s)[NJ]) {
+        constexpr int kGroup = 2 * NT < 4 ? 2 * NT : 4, kN = 2 * NT / kGroup;
         const int lane = fresh();
-        f32x16 s = zero16();
+        bf16x8 b[2][NJ][kGroup], c[2][kGroup];
+        const auto fetch = [&](int g) {
 #pragma unroll
-        for (int k = 0; k < 2 * NT; ++k) s = mfma(read_rows<U>(B, 32 * jt, k, lane), read_rows<U>(C, 32 * it, k, lane), s);
-        return s;
+            for (int k = 0; k < kGroup; ++k) {
+                c[g & 1][k] = read_rows<U>(C, 32 * it, g * kGroup + k, lane);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) b[g & 1][j][k] = read_rows<U>(B, 32 * (jt + j), g * kGroup + k, lane);
+            }
+        };
+        fetch(0);
+        issued();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s[j] = zero16();
+#pragma unroll
+        for (int g = 0; g < kN; ++g) {
+            if (g + 1 < kN) {
+                fetch(g + 1);
+                issued();
+            }
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) s[j] = mfma(b[g & 1][j][k], c[g & 1][k], s[j]);
+        }
     }
     // ... times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).
     template <bool DIAG>
@@ -422,23 +475,42 @@ struct Wave {
     // y = e^G_i (S C_i), tokens 32 it + l % 32 a lane
     __device__ __forceinline__ void from_state(const uint16_t *C, const Factors &f, f32x16 &y0, f32x16 &y1) {
         const int lane = fresh(), n = lane & 31;
+        const float e0 = f.eG[n], e1 = f.eG[32 + n];
+        bf16x8 c[2][2][2];
+        const auto fetch = [&](int g) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) c[g & 1][k][i] = read_rows<U>(C, 32 * i, 2 * g + k, lane);
+        };
+        fetch(0);
+        issued();
         y0 = zero16();
         y1 = zero16();
 #pragma unroll
-        for (int k = 0; k < 2 * NT; ++k) {
-            const bf16x8 c0 = read_rows<U>(C, 0, k, lane), c1 = read_rows<U>(C, 32, k, lane);
-            float t[8];
+        for (int g = 0; g < NT; ++g) {
+            bf16x8 hi[2], lo[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = S[k >> 1][8 * (k & 1) + e];
-            bf16x8 hi, lo;
-            split2(t, hi, lo);
-            y0 = mfma(hi, c0, y0);
-            y1 = mfma(hi, c1, y1);
-            y0 = mfma(lo, c0, y0);
-            y1 = mfma(lo, c1, y1);
+            for (int k = 0; k < 2; ++k) {
+                float t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = S[g][8 * k + e];
+                split2(t, hi[k], lo[k]);
+            }
+            if (g + 1 < NT) {
+                fetch(g + 1);
+                issued();
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                y0 = mfma(hi[k], c[g & 1][k][0], y0);
+                y1 = mfma(hi[k], c[g & 1][k][1], y1);
+                y0 = mfma(lo[k], c[g & 1][k][0], y0);
+                y1 = mfma(lo[k], c[g & 1][k][1], y1);
+            }
         }
-        y0 *= f.eG[n];
-        y1 *= f.eG[32 + n];
+        y0 *= e0;
+        y1 *= e1;
     }
     static __device__ __forceinline__ void add(f32x16 &y, const bf16x8 &xa, const bf16x8 &xb, const Scores &s) {
         y = mfma(xa, s.hi[0], y);
@@ -495,7 +567,7 @@ __device__ __forceinline__ void fetch_rows(const uint16_t *t, const GdrTensor &t
     asm volatile("" : "+v"(lane));
     const uint32_t row = uint32_t(ts.st) * 2;
     const uint16_t *base = t + job.group * ts.sh;
-    const Rsrc r = chunk_rsrc(base, ts.st, job, c);
+    const u32x4 r = chunk_rsrc(base, ts.st, job, c);
 #pragma unroll
     for (int k = 0; k < (kPieces + W - 1) / W; ++k) {
         const int piece = wave + k * W;
@@ -546,7 +618,7 @@ struct alignas(16) Raw { float v[4]; };
 
 // PAIR: two waves a block of 64 channels of a head, which share its scores; otherwise a wave for up to 32 channels.
 template <int NT, int W, bool PAIR, bool VEC, Mode MODE>
-__global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
+__global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
                                                                           int64_t places, int32_t seg, float *states, float *decays,
                                                                           bool svec) {
     constexpr int U = 4 * NT, kBC = kC * U * 8, kUnits = PAIR ? W / 2 : W;
@@ -612,7 +684,7 @@ __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmPa
     const int64_t piece = (int64_t(job.group) * units + unit) * (PAIR ? 2 : 1) + half;
     const float A = p.A.p[h * p.A.sh], bias = p.bias.p ? p.bias.p[h * p.bias.sh] : 0.0f;
     const float D = kOut && p.D.p && p.D.sd == 0 ? p.D.p[h * p.D.sh] : 0.0f;
-    float dt = 0.0f;
+    typename Wave<NT, VEC>::Step dt = {0, 0};
     wv.zero();
     fetch_rows<NT, W, VEC>(p.B, p.bs, p.N, job, job.c0, B[0], wave, lane);
     if (kOut) fetch_rows<NT, W, VEC>(p.C, p.cs, p.N, job, job.c0, C[0], wave, lane);
@@ -649,24 +721,33 @@ __global__ __launch_bounds__(64 * W, W >= 8 ? 2 : 1) void ssm_chunk_kernel(SsmPa
             if constexpr (PAIR) {
                 if (work) {
                     if (first) {
-                        wv.put(wv.template weigh<true>(wv.score(Bc, Cc, 0, 0), 0, f, D), sc, lane);
+                        f32x16 s[1];
+                        wv.template score<1>(Bc, Cc, 0, 0, s);
+                        wv.put(wv.template weigh<true>(s[0], 0, f, D), sc, lane);
                     } else {
-                        wv.put(wv.template weigh<false>(wv.score(Bc, Cc, 0, 1), 1, f, D), sc + 2048, lane);
-                        wv.put(wv.template weigh<true>(wv.score(Bc, Cc, 1, 1), 1, f, D), sc + 4096, lane);
+                        f32x16 s[2];
+                        wv.template score<2>(Bc, Cc, 0, 1, s);
+                        wv.put(wv.template weigh<false>(s[0], 1, f, D), sc + 2048, lane);
+                        wv.put(wv.template weigh<true>(s[1], 1, f, D), sc + 4096, lane);
                     }
                     wv.from_state(Cc, f, y0, y1);
                 }
-                __syncthreads();
+                exchange();
                 if (work) {
-                    wv.add(y0, x[0], x[1], wv.get(sc, lane));
-                    wv.add(y1, x[0], x[1], wv.get(sc + 2048, lane));
-                    wv.add(y1, x[2], x[3], wv.get(sc + 4096, lane));
+                    const Scores s00 = wv.get(sc, lane), s01 = wv.get(sc + 2048, lane), s11 = wv.get(sc + 4096, lane);
+                    issued();
+                    wv.add(y0, x[0], x[1], s00);
+                    wv.add(y1, x[0], x[1], s01);
+                    wv.add(y1, x[2], x[3], s11);
                 }
             } else if (work) {
                 wv.from_state(Cc, f, y0, y1);
-                wv.add(y0, x[0], x[1], wv.template weigh<true>(wv.score(Bc, Cc, 0, 0), 0, f, D));
-                wv.add(y1, x[0], x[1], wv.template weigh<false>(wv.score(Bc, Cc, 0, 1), 1, f, D));
-                wv.add(y1, x[2], x[3], wv.template weigh<true>(wv.score(Bc, Cc, 1, 1), 1, f, D));
+                f32x16 s[1], t[2];
+                wv.template score<1>(Bc, Cc, 0, 0, s);
+                wv.add(y0, x[0], x[1], wv.template weigh<true>(s[0], 0, f, D));
+                wv.template score<2>(Bc, Cc, 0, 1, t);
+                wv.add(y1, x[0], x[1], wv.template weigh<false>(t[0], 1, f, D));
+                wv.add(y1, x[2], x[3], wv.template weigh<true>(t[1], 1, f, D));
             }
             if (work) {
                 wv.store(c, 0, y0);
@@ -754,11 +835,8 @@ hipError_t launch_w(const SsmParams &p, bool svec, const SsmPlan &plan, void *wo
 
 template <int NT, bool VEC>
 hipError_t launch_nt(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
-    if (plan.pair)
-        return plan.waves == 8 ? launch_w<NT, 8, true, VEC>(p, svec, plan, workspace, s)
-                               : launch_w<NT, 2, true, VEC>(p, svec, plan, workspace, s);
-    return plan.waves == 8 ? launch_w<NT, 8, false, VEC>(p, svec, plan, workspace, s)
-                           : launch_w<NT, 2, false, VEC>(p, svec, plan, workspace, s);
+    return plan.pair ? launch_w<NT, kSsmWaves, true, VEC>(p, svec, plan, workspace, s)
+                     : launch_w<NT, kSsmWaves, false, VEC>(p, svec, plan, workspace, s);
 }
 
 }  // namespace

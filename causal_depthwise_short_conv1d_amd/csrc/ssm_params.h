@@ -71,13 +71,13 @@ inline int norm_threads(int32_t size) {
 }
 
 constexpr int kSsmChunk = 64;          // tokens of a chunk
+constexpr int kSsmWaves = 8;           // a workgroup of the chunked kernel
 constexpr int kSsmMaxChunkN = 128;     // states a channel of the chunked kernel
 
 // How the chunked kernel takes a call: its shapes, and whether sequences are cut into segments of `seg` chunks (0: they
 // are not) that are walked at once.
 struct SsmPlan {
     int32_t nt;                        // 32-state tiles: 1, 2 or 4
-    int32_t waves;                     // a workgroup
     bool pair;                         // two waves a block of 64 channels of a head, else one for up to 32
     int32_t seg;
     int64_t slots;                     // of segments
