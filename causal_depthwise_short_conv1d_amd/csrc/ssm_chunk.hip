@@ -24,7 +24,7 @@
 // Precision.  x, B and C are bf16 and enter as they are; every other operand is
 // split into bf16 parts, which have fp32's range: e^(..) d x, which feeds the
 // state, into three (24 bits); S and the scores, which only feed the bf16
-// output, into two (17 bits, 2^-18 of each).  All sums are fp32, G is fp64.
+// output, into two (to 2^-17 of each).  All sums are fp32, G is fp64.
 #include "ssm_device.h"
 
 namespace sconv {
@@ -57,16 +57,6 @@ __device__ __forceinline__ int swz(int r) {
     return U >= 8 ? ((r & 3) << 1 | ((r >> 2) & 1)) : (((r >> 1) & 1) << 1 | ((r >> 2) & 1));
 }
 
-// A descriptor's words, in scalar registers.
-__device__ __forceinline__ u32x4 make_words(const void *base, int64_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    u32x4 r;
-    r.x = __builtin_amdgcn_readfirstlane(uint32_t(a));
-    r.y = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32) & 0xffffu);
-    r.z = __builtin_amdgcn_readfirstlane(uint32_t(bytes < 0x7fffffff ? bytes : 0x7fffffff));
-    r.w = 0x00020000u;
-    return r;
-}
 // 16 bytes a lane from byte `at` of r to lds + 16 lane, past the registers.  What lies past r's end may or may not be written
 // as zero: those places hold zeros or an earlier chunk's rows.  Written as an instruction (it has no register to be written
 // late): the builtin makes the compiler wait for it before the next read of the same array, the other buffer's included, which
@@ -80,9 +70,21 @@ __device__ __forceinline__ void to_lds(const u32x4 &r, uint32_t at, void *lds) {
 __device__ __forceinline__ void exchange() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // Reads that were written before it are issued before what comes after it.
 __device__ __forceinline__ void issued() { __builtin_amdgcn_sched_barrier(0); }
-// What this wave has on its way to LDS is there.
+// N matrix products with 6 vector instructions behind each, which take no longer than it.
+template <int N>
+__device__ __forceinline__ void interleave() {
+    if constexpr (N > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+        interleave<N - 1>();
+    }
+}
+// All but this wave's last N reads and writes of memory are done, those on their way to LDS among them.  As an instruction that
+// the compiler knows: it takes its own loads for done too.
+template <int N>
 __device__ __forceinline__ void landed() {
-    __builtin_amdgcn_s_waitcnt(0x0f70);        // vmcnt(0), as an instruction that the compiler knows: its own loads are over too
+    static_assert(N < 16, "the low bits of the counter");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | N);
     asm volatile("" ::: "memory");
 }
 
@@ -119,26 +121,32 @@ __device__ __forceinline__ f32x16 zero16() { return f32x16{0, 0, 0, 0, 0, 0, 0, 
 
 __device__ __forceinline__ bf16x8 as_bf16(const uint32_t (&w)[4]) { return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}); }
 
-// x = hi + lo to 2^-18 of it.
+// The upper halves of two floats: their bf16 parts, cut off.
+__device__ __forceinline__ uint32_t upper(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// x = hi + lo to 2^-17 of it.  (Cut off, not rounded: a conversion takes 6.5 cycles where a logical instruction takes 4, and
+// a dot product with (-1, 0) in place of the two for what is left takes 8 beside another wave's matrix products.)
 __device__ __forceinline__ void split2(const float (&x)[8], bf16x8 &hi, bf16x8 &lo) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        l[i] = pack_bf16x2(x[2 * i] - bf_lo(h[i]), x[2 * i + 1] - bf_hi(h[i]));
+        h[i] = upper(x[2 * i], x[2 * i + 1]);
+        l[i] = pack_bf16x2(below(x[2 * i]), below(x[2 * i + 1]));
     }
     hi = as_bf16(h);
     lo = as_bf16(l);
 }
-// ... in three parts, to the last bit.
+// ... in three parts, to 2^-24.
 __device__ __forceinline__ void split3(const float (&x)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
     uint32_t h[4], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        const float a = x[2 * i] - bf_lo(h[i]), b = x[2 * i + 1] - bf_hi(h[i]);
-        m[i] = pack_bf16x2(a, b);
-        l[i] = pack_bf16x2(a - bf_lo(m[i]), b - bf_hi(m[i]));
+        h[i] = upper(x[2 * i], x[2 * i + 1]);
+        const float a = below(x[2 * i]), b = below(x[2 * i + 1]);
+        m[i] = upper(a, b);
+        l[i] = upper(below(a), below(b));
     }
     hi = as_bf16(h);
     mid = as_bf16(m);
@@ -178,11 +186,22 @@ struct Job {
     int32_t c0, c1;
 };
 
-// Rows of a chunk from the sequence's row c * kC on, through a descriptor that ends behind the sequence's last row.
-__device__ __forceinline__ u32x4 chunk_rsrc(const uint16_t *t, int64_t st, const Job &job, int32_t c) {
-    const int32_t left = job.n - c * kC < kC ? job.n - c * kC : kC;
-    return make_words(t + (int64_t(job.t0) + c * kC) * st, left * st * 2);
-}
+// A wave-uniform tensor's rows from a chunk's first on; next() goes to the next chunk's.
+struct Rows {
+    const char *at;
+    uint32_t row;                      // bytes
+    __device__ __forceinline__ Rows(const uint16_t *t, int64_t st, int64_t first) {
+        at = reinterpret_cast<const char *>(t + first * st);
+        row = uint32_t(st) * 2;
+    }
+    __device__ __forceinline__ void next() { at += uint64_t(row) * kC; }
+    // A descriptor that ends behind the `left`-th row (at most a chunk's).
+    __device__ __forceinline__ u32x4 words(int32_t left) const {
+        const uint64_t a = reinterpret_cast<uint64_t>(at);
+        return u32x4{uint32_t(a), uint32_t(a >> 32) & 0xffffu, uint32_t(left < kC ? left : kC) * row, 0x00020000u};
+    }
+    __device__ __forceinline__ Rsrc rsrc(int32_t left) const { return make_rsrc(at, int64_t(left < kC ? left : kC) * row); }
+};
 
 enum Mode { kWhole, kStates, kSegment };
 
@@ -196,7 +215,7 @@ struct Wave {
     const Job job;
     const int lane0;
     const int32_t h, ch0;              // head, first channel
-    uint16_t *xl;                      // [kC][kPW], this wave's
+    uint32_t xo, oo[2];                // the lane's offsets in a chunk's rows of x, and of out
     f32x16 S[NT];                      // S^T: n = 32 nt + 16 (q / 8) + 8 (l / 32) + q % 8 of channel chan()
 
     // The lane number anew, as a value that the compiler takes for unknown: addresses computed from it stay in their phase.
@@ -287,23 +306,29 @@ struct Wave {
         const uint16_t *e = static_cast<const uint16_t *>(p.dt) + at * w;
         return {e[0], e[w - 1]};
     }
-    // The wave's x of a chunk on its way to LDS.
-    __device__ __forceinline__ void fetch_x(int32_t c) {
-        const int lane = fresh(), t0 = lane >> 2, u = (lane & 3) ^ swz<4>(t0);
+    __device__ __forceinline__ void offsets(uint32_t xrow, uint32_t orow) {
+        const int t = lane0 >> 2, u = (lane0 & 3) ^ swz<4>(t);
         const int32_t ch = ch0 + 8 * u;
-        if constexpr (VEC) {
-            const u32x4 r = chunk_rsrc(p.x + h * p.xs.sh, p.xs.st, job, c);
-            const uint32_t row = uint32_t(p.xs.st) * 2, at = t0 * row + uint32_t(ch) * 2;
-            if (ch < p.P) {
+        xo = ch < p.P ? t * xrow + uint32_t(ch) * 2 : kOob;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) to_lds(r, at + 16 * k * row, xl + 512 * k);
-            }
+        for (int k = 0; k < 2; ++k) {
+            const int32_t o = ch0 + 16 * k + 8 * (lane0 >> 5);
+            oo[k] = o < p.P ? (lane0 & 31) * orow + uint32_t(o) * 2 : kOob;
+        }
+    }
+    // Pieces [k0, k1) of the wave's x of chunk c, 16 rows each, on their way to LDS.  r: that chunk's rows.
+    __device__ __forceinline__ void fetch_x(const Rows &r, int32_t c, uint16_t *to, int k0, int k1) {
+        if constexpr (VEC) {
+            const u32x4 words = r.words(job.n - c * kC);
+#pragma unroll
+            for (int k = k0; k < k1; ++k) to_lds(words, xo + 16 * k * r.row, to + 512 * k);
         } else {
+            const int lane = fresh(), t0 = lane >> 2, ch = ch0 + 8 * ((lane & 3) ^ swz<4>(t0));
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
+            for (int k = k0; k < k1; ++k) {
                 const int32_t t = c * kC + 16 * k + t0;
                 const int64_t row = int64_t(job.t0) + (t < job.n ? t : job.n - 1);
-                *reinterpret_cast<u32x4 *>(xl + (64 * k + lane) * 8) = load8(p.x + row * p.xs.st + h * p.xs.sh, p.xs.sd, ch, p.P);
+                *reinterpret_cast<u32x4 *>(to + (64 * k + lane) * 8) = load8(p.x + row * p.xs.st + h * p.xs.sh, p.xs.sd, ch, p.P);
             }
         }
     }
@@ -345,7 +370,7 @@ struct Wave {
     }
 
     // x^T: channel chan() a lane, 16 tokens each.
-    __device__ __forceinline__ void read_x(bf16x8 (&x)[4]) {
+    __device__ __forceinline__ void read_x(const uint16_t *xl, bf16x8 (&x)[4]) {
         const int lane = fresh();
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = read_cols<4>(xl, 16 * k, 0, lane);
@@ -358,31 +383,36 @@ struct Wave {
         f32x4 w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = row4(f.w + 8 * k + 4 * hh);
-        bf16x8 b[2][NT];
+        bf16x8 b[2][NT], hi[2], mid[2], lo[2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) b[0][i] = read_cols<U>(B, 0, i, lane);
         issued();
-#pragma unroll
-        for (int i = 0; i < NT; ++i) S[i] *= keep;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        const auto split = [&](int k) {
             float xw[8];
             unpack8(__builtin_bit_cast(u32x4, x[k]), xw);
 #pragma unroll
             for (int e = 0; e < 8; ++e) xw[e] *= w[2 * k + (e >> 2)][e & 3];
-            bf16x8 hi, mid, lo;
-            split3(xw, hi, mid, lo);
+            split3(xw, hi[k & 1], mid[k & 1], lo[k & 1]);
+        };
+        split(0);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) S[i] *= keep;
+        // The next 16 tokens' operands are read and split between this step's products.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
             if (k < 3) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) b[(k + 1) & 1][i] = read_cols<U>(B, 16 * k + 16, i, lane);
                 issued();
+                split(k + 1);
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], hi, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], hi[k & 1], S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], mid, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], mid[k & 1], S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], lo, S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], lo[k & 1], S[i]);
+            if (k < 3) interleave<3 * NT>();
         }
     }
 
@@ -416,12 +446,24 @@ struct Wave {
                 for (int j = 0; j < NJ; ++j) s[j] = mfma(b[g & 1][j][k], c[g & 1][k], s[j]);
         }
     }
-    // ... times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).
+    // What the scores of half `half` against their own tokens (DIAG), or against the first half's, are multiplied by: u_i v_j.
+    struct Weights { float u; f32x4 v[4]; };
     template <bool DIAG>
-    __device__ __forceinline__ Scores weigh(const f32x16 &s, int half, const Factors &f, float D) {
+    __device__ __forceinline__ Weights weights(int half, const Factors &f) {
+        const int lane = fresh();
+        Weights r;
+        r.u = f.u[32 * half + (lane & 31)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r.v[k] = row4((DIAG ? f.v + 32 * half : f.vx) + 8 * k + 4 * (lane >> 5));
+        return r;
+    }
+    // The scores times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).
+    template <bool DIAG>
+    __device__ __forceinline__ Scores weigh(const f32x16 &s, int half, const Weights &g, bool plain, const Factors &f, float D) {
         const int lane = fresh(), n = lane & 31, hh = lane >> 5;
         float v[16];
-        if (DIAG && !__builtin_amdgcn_readfirstlane(f.plain)) {
+        const int i = n - 4 * hh;                      // (token j of register q is token i at j = (q % 4) + 8 (q / 4))
+        if (DIAG && !plain) {
             const float ih = f.relh[32 * half + n], il = f.rell[32 * half + n];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -429,25 +471,20 @@ struct Wave {
                 const f32x4 jh = row4(f.relh + j), jl = row4(f.rell + j), d = row4(f.d + j);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = (ih - jh[e]) + (il - jl[e]);
-                    v[4 * k + e] = s[4 * k + e] * (d[e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a));
+                    const float a = (ih - jh[e]) + (il - jl[e]), g = d[e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a);
+                    v[4 * k + e] = s[4 * k + e] * (8 * k + e <= i ? g : 0.0f);
                 }
             }
         } else {
-            const float ui = f.u[32 * half + n];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const f32x4 vj = row4((DIAG ? f.v + 32 * half : f.vx) + 8 * k + 4 * hh);
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * k + e] = s[4 * k + e] * ui * vj[e];
-            }
+                for (int e = 0; e < 4; ++e)
+                    v[4 * k + e] = s[4 * k + e] * g.u * (!DIAG || 8 * k + e <= i ? g.v[k][e] : 0.0f);
         }
         if constexpr (DIAG) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int j = (q & 3) + 8 * (q >> 2) + 4 * hh;
-                v[q] = j < n ? v[q] : (j == n ? v[q] + D : 0.0f);
-            }
+            for (int q = 0; q < 16; ++q) v[q] += 8 * (q >> 2) + (q & 3) == i ? D : 0.0f;
         }
         Scores r;
 #pragma unroll
@@ -485,33 +522,39 @@ struct Wave {
         };
         fetch(0);
         issued();
-        y0 = zero16();
-        y1 = zero16();
-#pragma unroll
-        for (int g = 0; g < NT; ++g) {
-            bf16x8 hi[2], lo[2];
+        bf16x8 hi[2][2], lo[2][2];
+        const auto split = [&](int g) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float t[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = S[g][8 * k + e];
-                split2(t, hi[k], lo[k]);
+                split2(t, hi[g & 1][k], lo[g & 1][k]);
             }
+        };
+        split(0);
+        y0 = zero16();
+        y1 = zero16();
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
             if (g + 1 < NT) {
                 fetch(g + 1);
                 issued();
+                split(g + 1);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                y0 = mfma(hi[k], c[g & 1][k][0], y0);
-                y1 = mfma(hi[k], c[g & 1][k][1], y1);
-                y0 = mfma(lo[k], c[g & 1][k][0], y0);
-                y1 = mfma(lo[k], c[g & 1][k][1], y1);
+                y0 = mfma(hi[g & 1][k], c[g & 1][k][0], y0);
+                y1 = mfma(hi[g & 1][k], c[g & 1][k][1], y1);
+                y0 = mfma(lo[g & 1][k], c[g & 1][k][0], y0);
+                y1 = mfma(lo[g & 1][k], c[g & 1][k][1], y1);
             }
+            if (g + 1 < NT) interleave<8>();
         }
         y0 *= e0;
         y1 *= e1;
     }
+    // y += P x of a tile
     static __device__ __forceinline__ void add(f32x16 &y, const bf16x8 &xa, const bf16x8 &xb, const Scores &s) {
         y = mfma(xa, s.hi[0], y);
         y = mfma(xb, s.hi[1], y);
@@ -519,20 +562,29 @@ struct Wave {
         y = mfma(xb, s.lo[1], y);
     }
 
-    // Outputs of the lane's token of half `it`: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the wave's.
-    __device__ __forceinline__ void store(int32_t c, int it, const f32x16 &y) {
-        const int lane = fresh();
-        const int32_t r = c * kC + 32 * it + (lane & 31);
-        if (r >= job.n) return;
-        const int64_t row = int64_t(job.t0) + r;
+    // Outputs of the lane's token of half `it`: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the wave's.  VEC: two writes,
+    // whatever of them exists (landed() counts them).  r: out's rows of the chunk.
+    __device__ __forceinline__ void store(const Rows &r, int32_t c, int it, const f32x16 &y, bool plain) {
+        const Rsrc to = r.rsrc(job.n - c * kC);
+        if (VEC && plain) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = y[8 * k + e];
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, oo[k] + 32 * it * r.row, 0, 0);
+            }
+            return;
+        }
+        const int lane = fresh(), t = c * kC + 32 * it + (lane & 31);
+        const int64_t row = int64_t(job.t0) + (t < job.n ? t : job.n - 1);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int32_t ch = ch0 + 16 * k + 8 * (lane >> 5);
-            if (ch >= p.P) continue;
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = y[8 * k + e];
-            if (p.D.p && p.D.sd != 0) {
+            if (p.D.p && p.D.sd != 0 && ch < p.P) {
                 float xf[8];
                 const uint16_t *xr = p.x + row * p.xs.st + h * p.xs.sh;
                 unpack8(VEC ? ld16(xr + ch) : load8(xr, p.xs.sd, ch, p.P), xf);
@@ -540,42 +592,47 @@ struct Wave {
                 for (int e = 0; e < 8; ++e)
                     if (ch + e < p.P) v[e] = fmaf(p.D.p[h * p.D.sh + (ch + e) * p.D.sd], xf[e], v[e]);
             }
-            if (p.z) {
+            if (p.z && ch < p.P) {
                 float zf[8];
                 const uint16_t *zr = p.z + row * p.zs.st + h * p.zs.sh;
                 unpack8(VEC ? ld16(zr + ch) : load8(zr, p.zs.sd, ch, p.P), zf);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = ssm_gate(v[e], zf[e]);
             }
-            uint16_t *o = p.out + row * p.os.st + h * p.os.sh;
             if constexpr (VEC) {
-                st16(o + ch, pack8(v));
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, oo[k] + 32 * it * r.row, 0, 0);
             } else {
+                uint16_t *o = p.out + row * p.os.st + h * p.os.sh;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (ch + e < p.P) o[(ch + e) * p.os.sd] = to_bf16(v[e]);
+                    if (t < job.n && ch + e < p.P) o[(ch + e) * p.os.sd] = to_bf16(v[e]);
             }
         }
     }
 };
 
-// Rows of B or C of a chunk on their way to LDS, by all of a workgroup's waves.
+// Rows of B or C of chunk c on their way to LDS, by all of a workgroup's waves: each brings pieces of 64 units.  `off`: the
+// lane's offset in its wave's first piece.
+template <int NT, int W>
+__device__ __forceinline__ uint32_t piece_offset(uint32_t row, int32_t N, int wave, int lane) {
+    constexpr int U = 4 * NT;
+    const int t = wave * (64 / U) + lane / U, u = (lane % U) ^ swz<U>(t);
+    return 8 * u < N ? t * row + 16 * u : kOob;
+}
 template <int NT, int W, bool VEC>
-__device__ __forceinline__ void fetch_rows(const uint16_t *t, const GdrTensor &ts, int32_t N, const Job &job, int32_t c,
-                                           uint16_t *lds, int wave, int lane) {
-    constexpr int U = 4 * NT, kPieces = kC * U / 64, kRows = 64 / U;           // a piece: 64 units, kRows rows
-    asm volatile("" : "+v"(lane));
-    const uint32_t row = uint32_t(ts.st) * 2;
-    const uint16_t *base = t + job.group * ts.sh;
-    const u32x4 r = chunk_rsrc(base, ts.st, job, c);
+__device__ __forceinline__ void fetch_rows(const Rows &r, uint32_t off, const uint16_t *base, const GdrTensor &ts, int32_t N,
+                                           const Job &job, int32_t c, uint16_t *lds, int wave, int lane) {
+    constexpr int U = 4 * NT, kPieces = kC * U / 64, kRows = 64 / U;
+    static_assert(kRows * W % 8 == 0, "a wave's pieces are swizzled alike");
+    const u32x4 words = r.words(job.n - c * kC);
 #pragma unroll
     for (int k = 0; k < (kPieces + W - 1) / W; ++k) {
         const int piece = wave + k * W;
         if (kPieces % W != 0 && piece >= kPieces) break;
-        const int tt = piece * kRows + lane / U, u = (lane % U) ^ swz<U>(tt);
         if constexpr (VEC) {
-            if (8 * u < N) to_lds(r, tt * row + 16 * u, lds + piece * 512);
+            to_lds(words, off + k * (kRows * W) * r.row, lds + piece * 512);
         } else {
+            const int tt = piece * kRows + lane / U, u = (lane % U) ^ swz<U>(tt);
             const int32_t at = c * kC + tt;
             const int64_t rr = int64_t(job.t0) + (at < job.n ? at : job.n - 1);
             *reinterpret_cast<u32x4 *>(lds + (piece * 64 + lane) * 8) = load8(base + rr * ts.st, ts.sd, 8 * u, N);
@@ -623,8 +680,10 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                                                                           bool svec) {
     constexpr int U = 4 * NT, kBC = kC * U * 8, kUnits = PAIR ? W / 2 : W;
     constexpr bool kOut = MODE != kStates;
-    __shared__ alignas(16) uint16_t B[2][kBC], C[kOut ? 2 : 1][kOut ? kBC : 8];
-    __shared__ alignas(16) uint16_t xl[W][kC * kPW];
+    // Rows come one chunk ahead; where a chunk takes little time, two.
+    constexpr int kAhead = kOut ? 1 : 2, kBufs = kAhead + 1;
+    __shared__ alignas(16) uint16_t B[kBufs][kBC], C[kOut ? kBufs : 1][kOut ? kBC : 8];
+    __shared__ alignas(16) uint16_t xl[kAhead][W][kC * kPW];
     __shared__ alignas(16) uint16_t scores[kOut && PAIR ? kUnits : 1][kOut && PAIR ? 3 * 2048 : 8];
     __shared__ Factors factors[kUnits][2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -640,7 +699,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     int64_t slot = 0;
     int32_t b = int32_t(place);
     if constexpr (MODE == kWhole) {
-        b = __builtin_amdgcn_readfirstlane(ranked<64 * W>(p, b, reinterpret_cast<int32_t *>(&xl[0][0])));
+        b = __builtin_amdgcn_readfirstlane(ranked<64 * W>(p, b, reinterpret_cast<int32_t *>(&xl[0][0][0])));
         __syncthreads();
     } else {
         slot = place;
@@ -666,72 +725,111 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     }
 
     // columns and rows that a chunk may lack
-    for (int i = threadIdx.x; i < 2 * kBC / 8; i += 64 * W) {
+    for (int i = threadIdx.x; i < kBufs * kBC / 8; i += 64 * W) {
         reinterpret_cast<u32x4 *>(&B[0][0])[i] = u32x4{0, 0, 0, 0};
         if (kOut) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
     }
-    for (int i = threadIdx.x; i < W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0])[i] = u32x4{0, 0, 0, 0};
+    for (int i = threadIdx.x; i < kAhead * W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0][0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
 
     const int half = PAIR ? wave / kUnits : 0, own = PAIR ? wave % kUnits : wave;
     const int32_t unit = block * kUnits + own;
     const bool work = unit < units, first = half == 0, second = !PAIR || half == 1;
     const int32_t h = job.group * p.per_group + (work ? unit / pbs : 0), pb = work ? unit % pbs : 0;
-    Wave<NT, VEC> wv{p, job, lane, h, (PAIR ? 64 : 32) * pb + 32 * half, xl[wave]};
+    Wave<NT, VEC> wv{p, job, lane, h, (PAIR ? 64 : 32) * pb + 32 * half};
     uint16_t *sc = scores[kOut && PAIR ? own : 0];
     float *rows = p.state ? p.state + sp.line * p.s_sl + h * p.s_sh : nullptr;
     const int64_t per_slot = int64_t(p.G) * units * (PAIR ? 2 : 1);
     const int64_t piece = (int64_t(job.group) * units + unit) * (PAIR ? 2 : 1) + half;
     const float A = p.A.p[h * p.A.sh], bias = p.bias.p ? p.bias.p[h * p.bias.sh] : 0.0f;
     const float D = kOut && p.D.p && p.D.sd == 0 ? p.D.p[h * p.D.sh] : 0.0f;
+    const uint16_t *Bg = p.B + job.group * p.bs.sh, *Cg = p.C + job.group * p.cs.sh;
+    const int64_t row0 = int64_t(job.t0) + int64_t(job.c0) * kC;
+    Rows xr(p.x + h * p.xs.sh, p.xs.st, row0), br(Bg, p.bs.st, row0), cr(Cg, p.cs.st, row0);
+    Rows orow(p.out + h * p.os.sh, p.os.st, row0);
+    wv.offsets(xr.row, orow.row);
+    const uint32_t bo = piece_offset<NT, W>(br.row, p.N, wave, lane), co = piece_offset<NT, W>(cr.row, p.N, wave, lane);
+    const bool as_is = !p.z && (!p.D.p || p.D.sd == 0);            // outputs are written as they come
+    // the next chunk that has not been asked for
+    const auto fetch_b = [&](int32_t c, int buf) {
+        fetch_rows<NT, W, VEC>(br, bo, Bg, p.bs, p.N, job, c, B[buf], wave, lane);
+        br.next();
+    };
+    const auto fetch_c = [&](int32_t c, int buf) {
+        if (kOut) fetch_rows<NT, W, VEC>(cr, co, Cg, p.cs, p.N, job, c, C[kOut ? buf : 0], wave, lane);
+        cr.next();
+    };
     typename Wave<NT, VEC>::Step dt = {0, 0};
     wv.zero();
-    fetch_rows<NT, W, VEC>(p.B, p.bs, p.N, job, job.c0, B[0], wave, lane);
-    if (kOut) fetch_rows<NT, W, VEC>(p.C, p.cs, p.N, job, job.c0, C[0], wave, lane);
+    fetch_b(job.c0, 0);
+    fetch_c(job.c0, 0);
     if (work) {
-        wv.fetch_x(job.c0);
+        wv.fetch_x(xr, job.c0, xl[0][wave], 0, 4);
+        xr.next();
+        if (kAhead == 2 && job.c0 + 1 < job.c1) wv.fetch_x(xr, job.c0 + 1, xl[kAhead - 1][wave], 0, 4);
+        if (kAhead == 2) xr.next();
         if (MODE != kStates && job.c0 == 0) {
             if (sp.init) wv.load(rows, svec);
         } else if (MODE == kSegment) {
             wv.load_raw(states + ((slot - 1) * per_slot + piece) * (NT * 1024));
         }
-        if (first) wv.factors(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
+        if (first) {
+            wv.factors(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
+            dt = wv.fetch_dt(job.c0 + 1);
+        }
+    }
+    if (kAhead == 2) {
+        if (job.c0 + 1 < job.c1) fetch_b(job.c0 + 1, 1);
     }
     float total = 0.0f;
-    landed();
+    landed<0>();
     __syncthreads();
+    int cur = 0;                       // the chunk's buffer of B and C
     for (int32_t c = job.c0; c < job.c1; ++c) {
-        const int cur = (c - job.c0) & 1;
-        const bool more = c + 1 < job.c1;
-        const Factors &f = factors[own][cur];
+        const int odd = (c - job.c0) & 1, next = cur + kAhead < kBufs ? cur + kAhead : cur + kAhead - kBufs;
+        const bool more = c + 1 < job.c1, ahead = c + kAhead < job.c1;
+        const Factors &f = factors[own][odd];
+        uint16_t *xw = xl[kAhead == 2 ? odd : 0][wave];
         bf16x8 x[4];
-        if (work) wv.read_x(x);
+        if (work) wv.read_x(xw, x);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // x is in registers: its place is free
-        if (more) {
-            if (work) {
-                if (first) dt = wv.fetch_dt(c + 1);
-                wv.fetch_x(c + 1);
-            }
-            fetch_rows<NT, W, VEC>(p.B, p.bs, p.N, job, c + 1, B[cur ^ 1], wave, lane);
-            if (kOut) fetch_rows<NT, W, VEC>(p.C, p.cs, p.N, job, c + 1, C[kOut ? cur ^ 1 : 0], wave, lane);
-        }
+        typename Wave<NT, VEC>::Step later = dt;
+        if (work && first) later = wv.fetch_dt(c + 2);
+        // What comes for a later chunk is asked for in pieces, all over the chunk: 64 KB at once fill the memory pipeline, and
+        // the waves wait for it.
+        if (ahead) fetch_b(c + kAhead, next);
         if constexpr (kOut) {
             f32x16 y0, y1;
             const uint16_t *Bc = B[cur], *Cc = C[cur];
+            const auto ask = [&](int part) {
+                if (!ahead) return;
+                if (part < 2 && work) wv.fetch_x(xr, c + kAhead, xw, 2 * part, 2 * part + 2);
+                if (part == 1) xr.next();
+                if (part == 2) fetch_c(c + kAhead, next);
+            };
             if constexpr (PAIR) {
                 if (work) {
                     if (first) {
+                        const auto g = wv.template weights<true>(0, f);
+                        const bool plain = __builtin_amdgcn_readfirstlane(f.plain);
                         f32x16 s[1];
                         wv.template score<1>(Bc, Cc, 0, 0, s);
-                        wv.put(wv.template weigh<true>(s[0], 0, f, D), sc, lane);
+                        ask(0);
+                        wv.put(wv.template weigh<true>(s[0], 0, g, plain, f, D), sc, lane);
+                        if (more) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
                     } else {
+                        const auto g = wv.template weights<false>(1, f), g1 = wv.template weights<true>(1, f);
+                        const bool plain = __builtin_amdgcn_readfirstlane(f.plain);
                         f32x16 s[2];
                         wv.template score<2>(Bc, Cc, 0, 1, s);
-                        wv.put(wv.template weigh<false>(s[0], 1, f, D), sc + 2048, lane);
-                        wv.put(wv.template weigh<true>(s[1], 1, f, D), sc + 4096, lane);
+                        ask(0);
+                        wv.put(wv.template weigh<false>(s[0], 1, g, plain, f, D), sc + 2048, lane);
+                        wv.put(wv.template weigh<true>(s[1], 1, g1, plain, f, D), sc + 4096, lane);
                     }
+                    ask(1);
                     wv.from_state(Cc, f, y0, y1);
                 }
+                ask(2);
                 exchange();
                 if (work) {
                     const Scores s00 = wv.get(sc, lane), s01 = wv.get(sc + 2048, lane), s11 = wv.get(sc + 4096, lane);
@@ -740,27 +838,43 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                     wv.add(y1, x[0], x[1], s01);
                     wv.add(y1, x[2], x[3], s11);
                 }
-            } else if (work) {
-                wv.from_state(Cc, f, y0, y1);
-                f32x16 s[1], t[2];
-                wv.template score<1>(Bc, Cc, 0, 0, s);
-                wv.add(y0, x[0], x[1], wv.template weigh<true>(s[0], 0, f, D));
-                wv.template score<2>(Bc, Cc, 0, 1, t);
-                wv.add(y1, x[0], x[1], wv.template weigh<false>(t[0], 1, f, D));
-                wv.add(y1, x[2], x[3], wv.template weigh<true>(t[1], 1, f, D));
+            } else {
+                if (work) {
+                    wv.from_state(Cc, f, y0, y1);
+                    ask(0);
+                    const bool plain = __builtin_amdgcn_readfirstlane(f.plain);
+                    f32x16 s[1], t[2];
+                    wv.template score<1>(Bc, Cc, 0, 0, s);
+                    wv.add(y0, x[0], x[1], wv.template weigh<true>(s[0], 0, wv.template weights<true>(0, f), plain, f, D));
+                    ask(1);
+                    wv.template score<2>(Bc, Cc, 0, 1, t);
+                    wv.add(y1, x[0], x[1], wv.template weigh<false>(t[0], 1, wv.template weights<false>(1, f), plain, f, D));
+                    wv.add(y1, x[2], x[3], wv.template weigh<true>(t[1], 1, wv.template weights<true>(1, f), plain, f, D));
+                    if (more) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+                }
+                ask(2);
             }
             if (work) {
-                wv.store(c, 0, y0);
-                wv.store(c, 1, y1);
+                wv.store(orow, c, 0, y0, as_is);
+                wv.store(orow, c, 1, y1, as_is);
             }
+            orow.next();
+        } else if (work) {
+            if (ahead) wv.fetch_x(xr, c + kAhead, xw, 0, 4);
+            xr.next();
+            if (more && first) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
         }
         if (work) {
-            if (more && first) wv.factors(c + 1, dt, A, bias, factors[own][cur ^ 1]);
             wv.advance(B[cur], x, f);
             if (MODE == kStates) total += f.last;
         }
-        landed();
-        __syncthreads();
+        dt = later;
+        // The next chunk's rows are there.  Behind them a wave has asked for nothing but its 4 writes of this chunk's outputs, or
+        // the rows of the chunk after it: at least a piece of B and 4 of x (waves without work: a piece of B at most).
+        if (!VEC || !work || (kAhead == 2 && !ahead)) landed<0>();
+        else landed<kOut ? 4 : 4 + (kC * U / 64) / W>();
+        exchange();
+        cur = cur + 1 < kBufs ? cur + 1 : 0;
     }
     if (!work) return;
     if constexpr (MODE == kStates) {
