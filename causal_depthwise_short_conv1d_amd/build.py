@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libsconv.so")
 SOURCES = ["sconv_api.hip", "fwd_tokmajor.hip", "fwd_chanlast.hip", "general.hip",
            "update_decode.hip", "paged_fused.hip", "seq_metadata.hip", "gdr_api.hip",
            "gdr_recurrent.hip", "gdr_chunk.hip", "verify_drafts.hip", "ssm_api.hip",
-           "ssm_recurrent.hip", "ssm_chunk.hip", "group_norm.hip"]
+           "ssm_recurrent.hip", "ssm_chunk.hip", "ssm_channel.hip", "group_norm.hip"]
 ARCH = os.environ.get("SCONV_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

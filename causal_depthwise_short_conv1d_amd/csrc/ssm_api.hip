@@ -73,6 +73,14 @@ int check_ssm(const SsmParams &p, int64_t B, int64_t T, Layout *layout) {
     return SCONV_OK;
 }
 
+int check_workspace(const SsmParams &p, int64_t T, const void *workspace, int64_t bytes, int64_t need) {
+    if (!aligned(workspace, 16)) return SCONV_ERR_ALIGN;
+    if (bytes < need) return SCONV_ERR_SHAPE;
+    const Span sw = span_of(workspace, {need}, {1}, 1);
+    return overlap(sw, span_of_out(p, 1, T)) || overlap(sw, span_of_state(p)) || overlaps_input(p, 1, T, sw) ? SCONV_ERR_ALIAS
+                                                                                                          : SCONV_OK;
+}
+
 }  // namespace
 
 namespace sconv {
@@ -93,6 +101,25 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
             plan.seg = int32_t(seg);
             plan.slots = T / (kSsmChunk * seg) + batch + 1;
             plan.bytes = plan.slots * G * waves * (plan.nt * 1024 + 1) * 4;
+        }
+    }
+    return plan;
+}
+
+SsmChannelPlan ssm_channel_plan(int64_t T, int64_t batch, int32_t G, int32_t P, int32_t N, bool workspace) {
+    SsmChannelPlan plan = {};
+    plan.np = N <= 16 ? 16 : (N <= 32 ? 32 : 64);
+    plan.groups = G * ((int64_t(P) + kSsmChannels - 1) / kSsmChannels);
+    // four workgroups a CU hide what each waits for
+    const int64_t mean = T / batch;
+    if (workspace && batch * plan.groups < 512 && mean >= 128) {
+        int64_t seg = (T * plan.groups + 1023) / 1024;
+        seg = (seg < 32 ? 32 : seg) + kSsmTokens - 1;
+        seg -= seg % kSsmTokens;
+        if (seg < mean) {
+            plan.seg = int32_t(seg);
+            plan.slots = T / seg + batch + 1;
+            plan.bytes = plan.slots * plan.groups * (kSsmChannels / 64) * (plan.np + 2) * 64 * 4;
         }
     }
     return plan;
@@ -173,11 +200,8 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
         const int64_t places = (plan.seg ? plan.slots : batch) + 7;
         if (places <= kMaxThreads / (64 * kSsmWaves) / plan.groups && plan.groups <= INT32_MAX) {
             if (plan.bytes) {
-                if (!aligned(workspace, 16)) return SCONV_ERR_ALIGN;
-                if (workspace_bytes < plan.bytes) return SCONV_ERR_SHAPE;
-                const Span sw = span_of(workspace, {plan.bytes}, {1}, 1);
-                if (overlap(sw, span_of_out(p, 1, T)) || overlap(sw, span_of_state(p)) || overlaps_input(p, 1, T, sw))
-                    return SCONV_ERR_ALIAS;
+                const int rc = check_workspace(p, T, workspace, workspace_bytes, plan.bytes);
+                if (rc != SCONV_OK) return rc;
             }
             // rows longer than what is read of them, a chunk's within the 31 bits of a descriptor's offsets
             const auto rows = [&](const void *a, const GdrTensor &t, int32_t heads, int32_t n) {
@@ -190,6 +214,18 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
             return launch_status(launch_ssm_chunk(p, vec, svec, plan, workspace, stream));
         }
     }
+    if (!layout.head && p.H == p.G && p.N <= kSsmMaxChannelN) {
+        const SsmChannelPlan plan = ssm_channel_plan(T, batch, p.G, p.P, p.N, workspace != nullptr);
+        const int64_t places = plan.seg ? plan.slots : batch;
+        if (places <= kMaxThreads / kSsmChannels / plan.groups &&
+            int64_t(batch) * plan.groups <= kMaxThreads / kSsmChannels / plan.np) {
+            if (plan.bytes) {
+                const int rc = check_workspace(p, T, workspace, workspace_bytes, plan.bytes);
+                if (rc != SCONV_OK) return rc;
+            }
+            return launch_status(launch_ssm_channel(p, plan, workspace, stream));
+        }
+    }
     return launch_status(launch_ssm_recurrent(p, layout.head, layout.vec, stream));
 }
 
@@ -198,7 +234,10 @@ int64_t ssm_fwd_workspace_bytes(int32_t batch, int64_t total_tokens, int32_t num
     if (batch < 1 || total_tokens < 1 || num_heads < 1 || num_groups < 1 || num_heads % num_groups || head_dim < 1 ||
         state_dim < 1 || total_tokens > INT32_MAX - 256)
         return 0;
-    if (per_channel || state_dim > kSsmMaxChunkN) return 0;
+    if (per_channel)
+        return num_heads != num_groups || state_dim > kSsmMaxChannelN
+                   ? 0 : ssm_channel_plan(total_tokens, batch, num_groups, head_dim, state_dim, true).bytes;
+    if (state_dim > kSsmMaxChunkN) return 0;
     return ssm_plan(total_tokens, batch, num_heads, num_groups, head_dim, state_dim, true).bytes;
 }
 

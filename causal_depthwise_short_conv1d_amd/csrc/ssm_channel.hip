@@ -1,0 +1,254 @@
+// The selective state space scan of the channel form: prefill with a step size a
+// channel and a decay a channel and state.
+//
+//   S[n] <- e^(d A[n]) S[n] + d x B[n];   y = sum_n S[n] C[n] + D x
+//
+// A thread has a channel, with its states and decays in registers; a workgroup
+// has 256 channels of one group, whose B and C it brings to LDS in fp32, eight
+// tokens at a time, while the eight before are computed.  Nothing is exchanged.
+//
+// A state costs four products or sums and an exponential a token, and a channel
+// the step's softplus: some 100 vector instructions a token for 16 states.  Where a
+// call's channels and sequences do not fill the chip, sequences are cut into
+// segments that are walked twice at once: for the states at their ends, from
+// empty ones, then, once a pass over the segments has joined these, for the outputs.
+#include "ssm_device.h"
+
+namespace sconv {
+
+namespace {
+
+constexpr int kTB = kSsmTokens;        // tokens of a block
+constexpr int kThreads = kSsmChannels; // a workgroup, a channel each
+
+enum Mode { kWhole, kStates, kSegment };
+
+// Segment k of sequence i has slot floor(start_i / seg) + i + k: no two share one, and floor(T / seg) + batch + 1 are enough.
+__device__ __forceinline__ int64_t first_slot(const SsmParams &p, int32_t b, int32_t seg) {
+    int64_t a = p.qsl[b];
+    a = a < 0 ? 0 : (a > p.total_T ? p.total_T : a);
+    return a / seg + b;
+}
+
+// A wave's 64 channels of a slot in the workspace: its states by [n][lane], and the sums of the steps above and below 0.
+template <int NP>
+struct Piece {
+    float S[NP][64];
+    float up[64], down[64];
+};
+
+template <int NP, bool DT32, Mode MODE>
+__global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int32_t blocks, int64_t places, int32_t seg, void *ws) {
+    constexpr bool kOut = MODE != kStates;
+    constexpr int kRow = kOut ? 2 * NP : NP, kStage = (kTB * kRow + kThreads - 1) / kThreads;
+    __shared__ alignas(16) float bc[2][kTB][kRow];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t place = blockIdx.x / uint32_t(p.G * blocks), gb = blockIdx.x - place * uint32_t(p.G * blocks);
+    if (place >= places) return;
+    const int32_t g = int32_t(gb / uint32_t(blocks)), c0 = int32_t(gb % uint32_t(blocks)) * kThreads;
+    SsmSpan sp;
+    int64_t slot = 0, t0 = 0, t1;
+    int32_t b = int32_t(place);
+    if constexpr (MODE != kWhole) {
+        slot = place;
+        int32_t lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int32_t m = (lo + hi + 1) >> 1;
+            if (first_slot(p, m, seg) <= slot) lo = m; else hi = m - 1;
+        }
+        b = lo;
+    }
+    if (!ssm_span(p, b, sp)) return;
+    t1 = sp.n;
+    if constexpr (MODE != kWhole) {
+        const int64_t k = slot - first_slot(p, b, seg);
+        t0 = k * seg;
+        if (k < 0 || t0 >= sp.n) return;
+        if (MODE == kStates && t0 + seg >= sp.n) return;           // the last segment's end is no one's start
+        t1 = t0 + seg < sp.n ? t0 + seg : sp.n;
+    }
+    for (int i = threadIdx.x; i < 2 * kTB * kRow; i += kThreads) (&bc[0][0][0])[i] = 0.0f;
+
+    // one group a head: channel c of group g
+    const int32_t c = c0 + threadIdx.x, cc = c < p.P ? c : 0;
+    const bool live = c < p.P;
+    const int64_t per_slot = int64_t(p.G) * blocks * (kThreads / 64);
+    const int64_t piece = int64_t(gb) * (kThreads / 64) + wave;
+    Piece<NP> *pieces = static_cast<Piece<NP> *>(ws);
+    float S[NP], a[NP];
+    bool up = true;                    // no decay that grows with the step
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        a[n] = n < p.N ? p.A.p[g * p.A.sh + cc * p.A.sd + n * p.A.sn] * kLog2e : 0.0f;
+        up = up && !(a[n] > 0.0f);
+        S[n] = 0.0f;
+    }
+    const bool plain = __builtin_amdgcn_ballot_w64(!up) == 0;
+    float *row = p.state ? p.state + sp.line * p.s_sl + g * p.s_sh + cc * p.s_sp : nullptr;
+    if (kOut && t0 == 0) {
+        if (sp.init) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                if (n < p.N) S[n] = row[n * p.s_sn];
+        }
+    } else if (MODE == kSegment) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) S[n] = pieces[(slot - 1) * per_slot + piece].S[n][lane];
+    }
+    const float bias = p.bias.p ? p.bias.p[g * p.bias.sh + cc * p.bias.sd] : 0.0f;
+    const float D = kOut && p.D.p ? p.D.p[g * p.D.sh + cc * p.D.sd] : 0.0f;
+    const int64_t r0 = sp.t0 + t0;
+    const int32_t left = int32_t(t1 - t0);
+    const uint16_t *xp = p.x + r0 * p.xs.st + g * p.xs.sh + cc * p.xs.sd;
+    const uint16_t *zp = kOut && p.z ? p.z + r0 * p.zs.st + g * p.zs.sh + cc * p.zs.sd : nullptr;
+    uint16_t *op = p.out + r0 * p.os.st + g * p.os.sh + cc * p.os.sd;
+    const int64_t dt0 = r0 * p.ds.st + g * p.ds.sh + cc * p.ds.sd;
+    const uint16_t *Bp = p.B + r0 * p.bs.st + g * p.bs.sh, *Cp = p.C + r0 * p.cs.st + g * p.cs.sh;
+
+    uint32_t xn[kTB], dn[kTB], zn[kTB], sn[kStage];
+    // A block's inputs, past the end of the segment its last token's.
+    const auto fetch = [&](int32_t t) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) {
+            const int at = threadIdx.x + i * kThreads, tt = at / kRow, n = at % kRow;
+            const int64_t r = t + tt < left ? t + tt : left - 1;
+            sn[i] = 0;
+            if (at < kTB * kRow && n % NP < p.N)
+                sn[i] = n < NP ? Bp[r * p.bs.st + n * p.bs.sd] : Cp[r * p.cs.st + (n - NP) * p.cs.sd];
+        }
+#pragma unroll
+        for (int k = 0; k < kTB; ++k) {
+            const int64_t r = t + k < left ? t + k : left - 1;
+            xn[k] = xp[r * p.xs.st];
+            if constexpr (DT32) dn[k] = static_cast<const uint32_t *>(p.dt)[dt0 + r * p.ds.st];
+            else dn[k] = static_cast<const uint16_t *>(p.dt)[dt0 + r * p.ds.st];
+        }
+        if (kOut && zp) {
+#pragma unroll
+            for (int k = 0; k < kTB; ++k) zn[k] = zp[(t + k < left ? t + k : left - 1) * p.zs.st];
+        }
+    };
+    const auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            if (at < kTB * kRow) (&bc[buf][0][0])[at] = __uint_as_float(sn[i] << 16);
+        }
+    };
+    __syncthreads();
+    fetch(0);
+    stage(0);
+    __syncthreads();
+    float sum_up = 0.0f, sum_down = 0.0f;
+    for (int32_t t = 0; t < left; t += kTB) {
+        const int buf = (t / kTB) & 1;
+        uint32_t x[kTB], d[kTB], z[kTB];
+#pragma unroll
+        for (int k = 0; k < kTB; ++k) { x[k] = xn[k]; d[k] = dn[k]; z[k] = zn[k]; }
+        if (t + kTB < left) fetch(t + kTB);
+#pragma unroll
+        for (int k = 0; k < kTB; ++k) {
+            float s = ssm_clamp(p, ssm_softplus(p, __uint_as_float(DT32 ? d[k] : d[k] << 16) + bias));
+            if (t + k >= left) s = 0.0f;               // no step
+            const float xf = __uint_as_float(x[k] << 16), u = t + k < left ? s * xf : 0.0f;
+            const float su = s < 0.0f ? 0.0f : s;      // (NaN stays)
+            if (MODE == kStates) { sum_up += su; sum_down += s - su; }
+            const f32x4 *bv = reinterpret_cast<const f32x4 *>(&bc[buf][k][0]);
+            float y[2] = {0.0f, 0.0f};
+            const auto states = [&](auto decay) {
+#pragma unroll
+                for (int q = 0; q < NP / 4; ++q) {
+                    const f32x4 bb = bv[q], cv = kOut ? bv[(kOut ? NP / 4 : 0) + q] : bb;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int n = 4 * q + e;
+                        S[n] = fmaf(decay(a[n]), S[n], u * bb[e]);
+                        if (kOut) y[e & 1] = fmaf(S[n], cv[e], y[e & 1]);
+                    }
+                }
+            };
+            if (plain) states([&](float an) { return __builtin_amdgcn_exp2f(su * an); });
+            else states([&](float an) { const float v = s * an; return __builtin_amdgcn_exp2f(v > 0.0f ? 0.0f : v); });
+            if constexpr (kOut) {
+                float o = fmaf(D, xf, y[0] + y[1]);
+                if (zp) o = ssm_gate(o, __uint_as_float(z[k] << 16));
+                if (live && t + k < left) op[(t + k) * p.os.st] = to_bf16(o);
+            }
+        }
+        if (t + kTB < left) stage(buf ^ 1);
+        __syncthreads();
+    }
+    if constexpr (MODE == kStates) {
+        Piece<NP> &o = pieces[slot * per_slot + piece];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) o.S[n][lane] = S[n];
+        o.up[lane] = sum_up;
+        o.down[lane] = sum_down;
+    } else {
+        if (p.state && t1 == sp.n && live) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                if (n < p.N) row[n * p.s_sn] = S[n];
+        }
+    }
+}
+
+// From each segment's own states to those that the next one starts from, in place: a thread takes a state of a channel through a
+// sequence's segments.
+template <int NP>
+__global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int32_t blocks, int32_t seg, void *ws) {
+    const int64_t per_slot = int64_t(p.G) * blocks * (kThreads / 64);
+    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x, w = id / (64 * NP);
+    if (w >= int64_t(p.batch) * per_slot) return;
+    const int32_t b = int32_t(w / per_slot), lane = int32_t(id & 63), n = int32_t(id / 64 % NP);
+    const int64_t piece = w - b * per_slot;
+    SsmSpan sp;
+    if (!ssm_span(p, b, sp) || n >= p.N) return;
+    const int64_t ns = (sp.n + seg - 1) / seg;
+    const int32_t g = int32_t(piece / (blocks * (kThreads / 64))), c = int32_t(piece % (blocks * (kThreads / 64))) * 64 + lane;
+    if (c >= p.P) return;
+    const float a = p.A.p[g * p.A.sh + c * p.A.sd + n * p.A.sn] * kLog2e;
+    float S = 0.0f;
+    if (sp.init) S = p.state[sp.line * p.s_sl + g * p.s_sh + c * p.s_sp + n * p.s_sn];
+    Piece<NP> *at = static_cast<Piece<NP> *>(ws) + first_slot(p, b, seg) * per_slot + piece;
+    constexpr int kFew = 4;            // segments read together
+    for (int64_t i = 0; i + 1 < ns; i += kFew) {
+        float own[kFew], sum[kFew];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            const Piece<NP> &q = at[(i + k + 1 < ns ? i + k : ns - 2) * per_slot];
+            own[k] = q.S[n][lane];
+            sum[k] = a > 0.0f ? q.down[lane] : q.up[lane];
+        }
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            if (i + k + 1 >= ns) break;
+            S = fmaf(__builtin_amdgcn_exp2f(a * sum[k]), S, own[k]);
+            at[(i + k) * per_slot].S[n][lane] = S;
+        }
+    }
+}
+
+template <int NP, bool DT32>
+hipError_t launch(const SsmParams &p, const SsmChannelPlan &plan, void *ws, hipStream_t s) {
+    const int32_t blocks = (p.P + kThreads - 1) / kThreads;
+    const int64_t per = int64_t(p.G) * blocks;
+    if (!plan.seg) {
+        ssm_channel_kernel<NP, DT32, kWhole><<<dim3(uint32_t(p.batch * per)), dim3(kThreads), 0, s>>>(p, blocks, p.batch, 0, nullptr);
+        return hipGetLastError();
+    }
+    ssm_channel_kernel<NP, DT32, kStates><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
+    ssm_channel_pass_kernel<NP><<<dim3(uint32_t(p.batch * per * (kThreads / 64) * NP / 4)), dim3(256), 0, s>>>(p, blocks, plan.seg, ws);
+    ssm_channel_kernel<NP, DT32, kSegment><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ssm_channel(const SsmParams &p, const SsmChannelPlan &plan, void *ws, hipStream_t s) {
+    if (plan.np == 16) return p.dt_fp32 ? launch<16, true>(p, plan, ws, s) : launch<16, false>(p, plan, ws, s);
+    if (plan.np == 32) return p.dt_fp32 ? launch<32, true>(p, plan, ws, s) : launch<32, false>(p, plan, ws, s);
+    return p.dt_fp32 ? launch<64, true>(p, plan, ws, s) : launch<64, false>(p, plan, ws, s);
+}
+
+}  // namespace sconv

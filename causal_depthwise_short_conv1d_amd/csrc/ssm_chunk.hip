@@ -336,10 +336,7 @@ struct Wave {
     // The factors of chunk c from its dt.
     __device__ __forceinline__ void factors(int32_t c, const Step &dt, float A, float bias, Factors &f) {
         const int lane = fresh();
-        float d = __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias;
-        if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
-        d = d < p.dt_min ? p.dt_min : d;
-        d = d > p.dt_max ? p.dt_max : d;
+        float d = ssm_clamp(p, ssm_softplus(p, __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias));
         if (c * kC + lane >= job.n) d = 0.0f;
         float g = d * A;
         g = g > 0.0f ? 0.0f : (g < -200.0f ? -200.0f : g);         // e^-200 is 0, as of anything below

@@ -8,13 +8,29 @@ namespace sconv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The step size of head h, channel c at element offset `at` of dt (channel included).
-__device__ __forceinline__ float ssm_step(const SsmParams &p, int64_t at, float bias) {
-    float d = p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
-    d += bias;
-    if (p.softplus) d = d > 20.0f ? d : log1pf(expf(d));
+// softplus(v), or v where the steps come without.  log1p(e) with e = e^-|v| is 2 atanh(q), q = e / (2 + e) <= 1/3: the series'
+// next term is below 2^-26 of it.  Roundings of 2^-24: |v| + 1 in the exponent, 2 each of exp2 and the reciprocal, 1 each of
+// 2 + e, q, the series, the sum.
+__device__ __forceinline__ float ssm_softplus(const SsmParams &p, float v) {
+    if (!p.softplus) return v;
+    const float e = __builtin_amdgcn_exp2f(fabsf(v) * -kLog2e), q = e * __builtin_amdgcn_rcpf(2.0f + e), w = q * q;
+    float s = fmaf(w, 2.0f / 15, 2.0f / 13);
+    s = fmaf(w, s, 2.0f / 11);
+    s = fmaf(w, s, 2.0f / 9);
+    s = fmaf(w, s, 2.0f / 7);
+    s = fmaf(w, s, 2.0f / 5);
+    s = fmaf(w, s, 2.0f / 3);
+    s = fmaf(w, s, 2.0f);
+    return fmaf(q, s, v > 0.0f ? v : 0.0f);
+}
+__device__ __forceinline__ float ssm_clamp(const SsmParams &p, float d) {
     d = d < p.dt_min ? p.dt_min : d;   // (NaN stays)
     return d > p.dt_max ? p.dt_max : d;
+}
+// The step size of head h, channel c at element offset `at` of dt (channel included).
+__device__ __forceinline__ float ssm_step(const SsmParams &p, int64_t at, float bias) {
+    const float d = p.dt_fp32 ? static_cast<const float *>(p.dt)[at] : bf_one(static_cast<const uint16_t *>(p.dt)[at]);
+    return ssm_clamp(p, ssm_softplus(p, d + bias));
 }
 
 // e^(d A), at most 1 (NaN stays).  The argument's rounding moves the result by |d A| e^(d A) 2^-24, which is below 2^-25:

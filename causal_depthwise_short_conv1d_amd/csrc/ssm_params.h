@@ -86,6 +86,20 @@ struct SsmPlan {
 };
 SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int32_t N, bool workspace);
 
+constexpr int kSsmTokens = 8;          // of a block of the channel kernel
+constexpr int kSsmChannels = 256;      // of its workgroups
+constexpr int kSsmMaxChannelN = 64;    // states a channel that it holds in registers
+
+// How the channel kernel takes a call: states rounded up, and whether sequences are cut into segments of `seg` tokens.
+struct SsmChannelPlan {
+    int32_t np;                        // 16, 32 or 64
+    int32_t seg;
+    int64_t slots;
+    int64_t groups;                    // workgroups of a place
+    int64_t bytes;                     // workspace
+};
+SsmChannelPlan ssm_channel_plan(int64_t T, int64_t batch, int32_t G, int32_t P, int32_t N, bool workspace);
+
 // Launchers: each enqueues its kernels and returns hipGetLastError().
 // `head`: one step size and one decay a head.  `vec`: unit strides of B, C and the
 // state, and every base and stride of theirs keeps four elements together.
@@ -93,6 +107,8 @@ hipError_t launch_ssm_recurrent(const SsmParams &p, bool head, bool vec, hipStre
 // `vec`: unit strides of x, B, C, z and out, every base and stride of 8 elements; `svec`: the state's rows in 16-byte
 // pieces.  The head form, up to kSsmMaxChunkN states.
 hipError_t launch_ssm_chunk(const SsmParams &p, bool vec, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s);
+// The channel form with a group a head, up to kSsmMaxChannelN states.
+hipError_t launch_ssm_channel(const SsmParams &p, const SsmChannelPlan &plan, void *workspace, hipStream_t s);
 // `vec`: unit channel strides, every base and stride of 8 elements.
 hipError_t launch_group_norm(const NormParams &p, bool vec, hipStream_t s);
 

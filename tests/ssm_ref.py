@@ -4,8 +4,10 @@ scan a token at a time with a running bound of what fp32 arithmetic may be off.
 Bound.  u = 2^-24.  M carries the state's magnitudes, M <- e M + |d x B|, and E
 its error.  Per token
     E <- e E + u (c_e e M + c_w |d x B| + c_s M')
-where, with k_d roundings in the step size d (4 for the sum, exp and log, and
-|dt + bias|, which a rounding of the softplus' argument costs at most), the
+where, with k_d roundings in the step size d (10 of its softplus: 2 each of an
+exponential and a reciprocal of one ulp, 1 each of dt + bias, the exponent's
+product, the denominator, the quotient, the series and the sum; and 2 |dt +
+bias|, by which the sum's and the product's rounding move the exponent), the
 decay e^(d A) is off by c_e = 4 + |d A| (3 + k_d) (the product with A, with
 log2(e), and d itself reach the exponent; exp2 and what scales it 4 more), a
 written term by c_w = 4 + k_d, and each sum rounds by c_s = 4: chunks sum a
@@ -37,7 +39,7 @@ def steps(d):
     v = d["dt"].to(F64)
     if d["dt_bias"] is not None:
         v = v + d["dt_bias"].to(F64)
-    k = 4 + v.abs().clamp(max=100)
+    k = 10 + 2 * v.abs().clamp(max=100)
     if d["dt_softplus"]:
         v = torch.logaddexp(v, torch.zeros_like(v))
     if d["dt_limit"] is not None:
