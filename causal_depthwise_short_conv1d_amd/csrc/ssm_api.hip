@@ -223,7 +223,11 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
                 const int rc = check_workspace(p, T, workspace, workspace_bytes, plan.bytes);
                 if (rc != SCONV_OK) return rc;
             }
-            return launch_status(launch_ssm_channel(p, plan, workspace, stream));
+            const auto rows = [&](const void *a, const GdrTensor &t) {
+                return !a || (t.sd == 1 && t.st >= p.P && t.st < (1 << 23));
+            };
+            const bool all = rows(p.x, p.xs) && rows(p.z, p.zs) && rows(p.out, p.os) && rows(p.dt, p.ds);
+            return launch_status(launch_ssm_channel(p, all, plan, workspace, stream));
         }
     }
     return launch_status(launch_ssm_recurrent(p, layout.head, layout.vec, stream));

@@ -12,6 +12,8 @@
 // call's channels and sequences do not fill the chip, sequences are cut into
 // segments that are walked twice at once: for the states at their ends, from
 // empty ones, then, once a pass over the segments has joined these, for the outputs.
+#include <type_traits>
+
 #include "ssm_device.h"
 
 namespace sconv {
@@ -30,6 +32,17 @@ __device__ __forceinline__ int64_t first_slot(const SsmParams &p, int32_t b, int
     return a / seg + b;
 }
 
+// The rows of a tensor that a workgroup walks, `left` of them; rows(t): a descriptor of those from t on, a block of them at most.
+struct Block {
+    const void *at;
+    int64_t row;                       // bytes
+    int32_t left;
+    __device__ __forceinline__ Rsrc rows(int32_t t) const {
+        const int32_t n = left - t < kTB ? left - t : kTB;
+        return make_rsrc(static_cast<const char *>(at) + t * row, n * row);
+    }
+};
+
 // A wave's 64 channels of a slot in the workspace: its states by [n][lane], and the sums of the steps above and below 0.
 template <int NP>
 struct Piece {
@@ -37,8 +50,10 @@ struct Piece {
     float up[64], down[64];
 };
 
-template <int NP, bool DT32, Mode MODE>
-__global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int32_t blocks, int64_t places, int32_t seg, void *ws) {
+// ROWS: x, dt, z and out have unit channel strides, and rows longer than a group: they are read and written through descriptors of
+// a block's rows, and what lies behind the last token is not there.
+template <int NP, bool DT32, bool ROWS, Mode MODE>
+__global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel(SsmParams p, int32_t blocks, int64_t places, int32_t seg, void *ws) {
     constexpr bool kOut = MODE != kStates;
     constexpr int kRow = kOut ? 2 * NP : NP, kStage = (kTB * kRow + kThreads - 1) / kThreads;
     __shared__ alignas(16) float bc[2][kTB][kRow];
@@ -105,9 +120,12 @@ __global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int3
     const int64_t dt0 = r0 * p.ds.st + g * p.ds.sh + cc * p.ds.sd;
     const uint16_t *Bp = p.B + r0 * p.bs.st + g * p.bs.sh, *Cp = p.C + r0 * p.cs.st + g * p.cs.sh;
 
+    const Block xb{p.x + r0 * p.xs.st + g * p.xs.sh, p.xs.st * 2, left}, zb{p.z + r0 * p.zs.st + g * p.zs.sh, p.zs.st * 2, left};
+    const Block ob{p.out + r0 * p.os.st + g * p.os.sh, p.os.st * 2, left};
+    const Block db{static_cast<const char *>(p.dt) + (r0 * p.ds.st + g * p.ds.sh) * (DT32 ? 4 : 2), p.ds.st * (DT32 ? 4 : 2), left};
     uint32_t xn[kTB], dn[kTB], zn[kTB], sn[kStage];
-    // A block's inputs, past the end of the segment its last token's.
-    const auto fetch = [&](int32_t t) {
+    // B and C of a block, past the end of the segment its last token's.
+    const auto fetch_bc = [&](int32_t t) {
 #pragma unroll
         for (int i = 0; i < kStage; ++i) {
             const int at = threadIdx.x + i * kThreads, tt = at / kRow, n = at % kRow;
@@ -116,16 +134,27 @@ __global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int3
             if (at < kTB * kRow && n % NP < p.N)
                 sn[i] = n < NP ? Bp[r * p.bs.st + n * p.bs.sd] : Cp[r * p.cs.st + (n - NP) * p.cs.sd];
         }
-#pragma unroll
-        for (int k = 0; k < kTB; ++k) {
+    };
+    // Token k of the block at t of the channel's inputs, in the place of the block's before it.  The lane's offset is kept from
+    // the compiler, which would hold every token's in registers; whole blocks' rows go by the scalar offset.
+    const auto fetch = [&](int32_t t, int k, const Rsrc &xr, const Rsrc &dr, const Rsrc &zr, auto full) {
+        if constexpr (ROWS) {
+            constexpr bool FULL = decltype(full)::value;
+            int32_t at = 2 * cc;
+            asm volatile("" : "+v"(at));
+            const auto load = [&](const Rsrc &r, int32_t row) -> uint32_t {
+                return FULL ? __builtin_amdgcn_raw_buffer_load_b16(r, at, k * row, 0) : __builtin_amdgcn_raw_buffer_load_b16(r, at + k * row, 0, 0);
+            };
+            xn[k] = load(xr, int32_t(xb.row));
+            if constexpr (DT32) dn[k] = __builtin_amdgcn_raw_buffer_load_b32(dr, 2 * at + k * int32_t(db.row), 0, 0);
+            else dn[k] = load(dr, int32_t(db.row));
+            if (kOut && zp) zn[k] = load(zr, int32_t(zb.row));
+        } else {
             const int64_t r = t + k < left ? t + k : left - 1;
             xn[k] = xp[r * p.xs.st];
             if constexpr (DT32) dn[k] = static_cast<const uint32_t *>(p.dt)[dt0 + r * p.ds.st];
             else dn[k] = static_cast<const uint16_t *>(p.dt)[dt0 + r * p.ds.st];
-        }
-        if (kOut && zp) {
-#pragma unroll
-            for (int k = 0; k < kTB; ++k) zn[k] = zp[(t + k < left ? t + k : left - 1) * p.zs.st];
+            if (kOut && zp) zn[k] = zp[r * p.zs.st];
         }
     };
     const auto stage = [&](int buf) {
@@ -136,21 +165,28 @@ __global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int3
         }
     };
     __syncthreads();
-    fetch(0);
+    fetch_bc(0);
+    {
+        const Rsrc xr = xb.rows(0), dr = db.rows(0), zr = zb.rows(zp ? 0 : left);
+#pragma unroll
+        for (int k = 0; k < kTB; ++k) fetch(0, k, xr, dr, zr, std::false_type());
+    }
     stage(0);
     __syncthreads();
     float sum_up = 0.0f, sum_down = 0.0f;
-    for (int32_t t = 0; t < left; t += kTB) {
+    // FULL: all tokens of the block and of the next one exist.
+    const auto block = [&](int32_t t, auto full) {
+        constexpr bool FULL = decltype(full)::value;
         const int buf = (t / kTB) & 1;
-        uint32_t x[kTB], d[kTB], z[kTB];
-#pragma unroll
-        for (int k = 0; k < kTB; ++k) { x[k] = xn[k]; d[k] = dn[k]; z[k] = zn[k]; }
-        if (t + kTB < left) fetch(t + kTB);
+        fetch_bc(t + kTB);
+        const Rsrc xr = xb.rows(t + kTB), dr = db.rows(t + kTB), zr = zb.rows(zp ? t + kTB : left), ow = ob.rows(t);
 #pragma unroll
         for (int k = 0; k < kTB; ++k) {
-            float s = ssm_clamp(p, ssm_softplus(p, __uint_as_float(DT32 ? d[k] : d[k] << 16) + bias));
-            if (t + k >= left) s = 0.0f;               // no step
-            const float xf = __uint_as_float(x[k] << 16), u = t + k < left ? s * xf : 0.0f;
+            float s = ssm_clamp(p, ssm_softplus(p, __uint_as_float(DT32 ? dn[k] : dn[k] << 16) + bias));
+            if (!FULL && t + k >= left) s = 0.0f;      // no step
+            const uint32_t xk = xn[k], zk = kOut ? zn[k] : 0;
+            fetch(t + kTB, k, xr, dr, zr, full);
+            const float xf = __uint_as_float(xk << 16), u = FULL || t + k < left ? s * xf : 0.0f;
             const float su = s < 0.0f ? 0.0f : s;      // (NaN stays)
             if (MODE == kStates) { sum_up += su; sum_down += s - su; }
             const f32x4 *bv = reinterpret_cast<const f32x4 *>(&bc[buf][k][0]);
@@ -171,13 +207,25 @@ __global__ __launch_bounds__(kThreads) void ssm_channel_kernel(SsmParams p, int3
             else states([&](float an) { const float v = s * an; return __builtin_amdgcn_exp2f(v > 0.0f ? 0.0f : v); });
             if constexpr (kOut) {
                 float o = fmaf(D, xf, y[0] + y[1]);
-                if (zp) o = ssm_gate(o, __uint_as_float(z[k] << 16));
-                if (live && t + k < left) op[(t + k) * p.os.st] = to_bf16(o);
+                if (zp) o = ssm_gate(o, __uint_as_float(zk << 16));
+                if constexpr (ROWS) {
+                    uint32_t at = live ? 2 * c : kOob;
+                    asm volatile("" : "+v"(at));
+                    if constexpr (FULL) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(o), ow, at, k * int32_t(ob.row), 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(to_bf16(o), ow, at + k * uint32_t(ob.row), 0, 0);
+                } else if (live && t + k < left) {
+                    op[(t + k) * p.os.st] = to_bf16(o);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);         // (or all tokens' B and C would be read at once)
         }
-        if (t + kTB < left) stage(buf ^ 1);
+        stage(buf ^ 1);
         __syncthreads();
-    }
+    };
+    int32_t t = 0;
+    if constexpr (ROWS)
+        for (; t + 2 * kTB <= left; t += kTB) block(t, std::true_type());
+    for (; t < left; t += kTB) block(t, std::false_type());
     if constexpr (MODE == kStates) {
         Piece<NP> &o = pieces[slot * per_slot + piece];
 #pragma unroll
@@ -229,26 +277,30 @@ __global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int3
     }
 }
 
-template <int NP, bool DT32>
+template <int NP, bool DT32, bool ROWS>
 hipError_t launch(const SsmParams &p, const SsmChannelPlan &plan, void *ws, hipStream_t s) {
     const int32_t blocks = (p.P + kThreads - 1) / kThreads;
     const int64_t per = int64_t(p.G) * blocks;
     if (!plan.seg) {
-        ssm_channel_kernel<NP, DT32, kWhole><<<dim3(uint32_t(p.batch * per)), dim3(kThreads), 0, s>>>(p, blocks, p.batch, 0, nullptr);
+        ssm_channel_kernel<NP, DT32, ROWS, kWhole><<<dim3(uint32_t(p.batch * per)), dim3(kThreads), 0, s>>>(p, blocks, p.batch, 0, nullptr);
         return hipGetLastError();
     }
-    ssm_channel_kernel<NP, DT32, kStates><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
+    ssm_channel_kernel<NP, DT32, ROWS, kStates><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
     ssm_channel_pass_kernel<NP><<<dim3(uint32_t(p.batch * per * (kThreads / 64) * NP / 4)), dim3(256), 0, s>>>(p, blocks, plan.seg, ws);
-    ssm_channel_kernel<NP, DT32, kSegment><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
+    ssm_channel_kernel<NP, DT32, ROWS, kSegment><<<dim3(uint32_t(plan.slots * per)), dim3(kThreads), 0, s>>>(p, blocks, plan.slots, plan.seg, ws);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_ssm_channel(const SsmParams &p, const SsmChannelPlan &plan, void *ws, hipStream_t s) {
-    if (plan.np == 16) return p.dt_fp32 ? launch<16, true>(p, plan, ws, s) : launch<16, false>(p, plan, ws, s);
-    if (plan.np == 32) return p.dt_fp32 ? launch<32, true>(p, plan, ws, s) : launch<32, false>(p, plan, ws, s);
-    return p.dt_fp32 ? launch<64, true>(p, plan, ws, s) : launch<64, false>(p, plan, ws, s);
+hipError_t launch_ssm_channel(const SsmParams &p, bool rows, const SsmChannelPlan &plan, void *ws, hipStream_t s) {
+    const auto as = [&](auto np) {
+        constexpr int NP = decltype(np)::value;
+        if (p.dt_fp32) return rows ? launch<NP, true, true>(p, plan, ws, s) : launch<NP, true, false>(p, plan, ws, s);
+        return rows ? launch<NP, false, true>(p, plan, ws, s) : launch<NP, false, false>(p, plan, ws, s);
+    };
+    if (plan.np == 16) return as(std::integral_constant<int, 16>());
+    return plan.np == 32 ? as(std::integral_constant<int, 32>()) : as(std::integral_constant<int, 64>());
 }
 
 }  // namespace sconv

@@ -107,8 +107,9 @@ hipError_t launch_ssm_recurrent(const SsmParams &p, bool head, bool vec, hipStre
 // `vec`: unit strides of x, B, C, z and out, every base and stride of 8 elements; `svec`: the state's rows in 16-byte
 // pieces.  The head form, up to kSsmMaxChunkN states.
 hipError_t launch_ssm_chunk(const SsmParams &p, bool vec, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s);
-// The channel form with a group a head, up to kSsmMaxChannelN states.
-hipError_t launch_ssm_channel(const SsmParams &p, const SsmChannelPlan &plan, void *workspace, hipStream_t s);
+// The channel form with a group a head, up to kSsmMaxChannelN states.  `rows`: unit channel strides of x, dt, z and out, and
+// rows longer than a group.
+hipError_t launch_ssm_channel(const SsmParams &p, bool rows, const SsmChannelPlan &plan, void *workspace, hipStream_t s);
 // `vec`: unit channel strides, every base and stride of 8 elements.
 hipError_t launch_group_norm(const NormParams &p, bool vec, hipStream_t s);
 
