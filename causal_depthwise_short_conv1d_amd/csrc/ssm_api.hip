@@ -36,7 +36,7 @@ bool overlaps_input(const SsmParams &p, int64_t B, int64_t T, const Span &w) {
 // The layouts that a call's tensors are in.
 struct Layout {
     bool head;      // one step size and decay a head
-    bool vec;       // B, C and the state in groups of four elements
+    bool vec;       // B, C, the state and decays of channels in groups of four elements
 };
 
 // The checks that prefill and decode share; B and T are the sizes of the
@@ -66,7 +66,8 @@ int check_ssm(const SsmParams &p, int64_t B, int64_t T, Layout *layout) {
     layout->vec = p.N % 4 == 0 && p.bs.sd == 1 && p.cs.sd == 1 &&
                   groups_of(p.B, 4, 2, {B, T, p.G}, {p.bs.sb, p.bs.st, p.bs.sh}) &&
                   groups_of(p.C, 4, 2, {B, T, p.G}, {p.cs.sb, p.cs.st, p.cs.sh}) &&
-                  (!p.state || (p.s_sn == 1 && groups_of(p.state, 4, 4, {p.num_lines, p.H, p.P}, {p.s_sl, p.s_sh, p.s_sp})));
+                  (!p.state || (p.s_sn == 1 && groups_of(p.state, 4, 4, {p.num_lines, p.H, p.P}, {p.s_sl, p.s_sh, p.s_sp}))) &&
+                  (layout->head || (p.A.sn == 1 && groups_of(p.A.p, 4, 4, {p.H, p.P}, {p.A.sh, p.A.sd})));
     // the recurrent kernel gives a wave to 8 channels at least, a workgroup to 4 waves
     const int64_t heads = int64_t(p.batch) * p.H;
     if (heads > kMaxThreads / 64 || heads * ((int64_t(p.P) + 7) / 8) > kMaxThreads / 64 - 4) return SCONV_ERR_SHAPE;

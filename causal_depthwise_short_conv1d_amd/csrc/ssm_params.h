@@ -101,8 +101,8 @@ struct SsmChannelPlan {
 SsmChannelPlan ssm_channel_plan(int64_t T, int64_t batch, int32_t G, int32_t P, int32_t N, bool workspace);
 
 // Launchers: each enqueues its kernels and returns hipGetLastError().
-// `head`: one step size and one decay a head.  `vec`: unit strides of B, C and the
-// state, and every base and stride of theirs keeps four elements together.
+// `head`: one step size and one decay a head.  `vec`: unit strides of B, C, the state
+// and, without `head`, A, and every base and stride of theirs keeps four elements together.
 hipError_t launch_ssm_recurrent(const SsmParams &p, bool head, bool vec, hipStream_t s);
 // `vec`: unit strides of x, B, C, z and out, every base and stride of 8 elements; `svec`: the state's rows in 16-byte
 // pieces.  The head form, up to kSsmMaxChunkN states.

@@ -114,9 +114,17 @@ __global__ __launch_bounds__(64 * kRecWaves) void ssm_recurrent_kernel(SsmParams
             bias[i] = p.bias.p ? p.bias.p[h * p.bias.sh + pr[i] * p.bias.sd] : 0.0f;
             const float *a = p.A.p + h * p.A.sh + pr[i] * p.A.sd;
 #pragma unroll
-            for (int c = 0; c < KI * 4; ++c) {
-                const int n = 4 * LN * (c >> 2) + 4 * j + (c & 3);
-                A[i][c] = n < p.N ? a[n * p.A.sn] : 0.0f;
+            for (int k = 0; k < KI; ++k) {
+                const int n = 4 * LN * k + 4 * j;
+                if constexpr (VEC) {
+                    f32x4 w = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (n < p.N) w = *reinterpret_cast<const f32x4 *>(a + n);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) A[i][4 * k + e] = w[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) A[i][4 * k + e] = n + e < p.N ? a[(n + e) * p.A.sn] : 0.0f;
+                }
             }
         }
     }
@@ -190,14 +198,16 @@ template <int LN, int KI, bool HEAD, bool VEC>
 hipError_t launch_n(const SsmParams &p, hipStream_t s) {
     constexpr int kRows = 64 / LN;
     const int64_t heads = int64_t(p.batch) * p.H;
-    // two row groups a wave, one where that leaves fewer than 8 waves a CU
-    const bool few = heads * ((p.P + 2 * kRows - 1) / (2 * kRows)) < 2048;
-    const int rows = few ? kRows : 2 * kRows;
-    const int32_t tiles = (p.P + rows - 1) / rows;
-    const int64_t n = heads * tiles;
+    // two row groups a wave (four of short rows), as long as that leaves 8 waves a CU
+    constexpr int kMost = KI == 1 ? 4 : 2;
+    const auto waves = [&](int r) { return heads * ((p.P + r * kRows - 1) / (r * kRows)); };
+    const int r = waves(kMost) >= 2048 ? kMost : (waves(2) >= 2048 ? 2 : 1);
+    const int64_t n = waves(r);
+    const int32_t tiles = (p.P + r * kRows - 1) / (r * kRows);
     const dim3 grid(uint32_t((n + kRecWaves - 1) / kRecWaves)), block(64 * kRecWaves);
-    if (few) ssm_recurrent_kernel<LN, KI, 1, HEAD, VEC><<<grid, block, 0, s>>>(p, tiles, n);
-    else ssm_recurrent_kernel<LN, KI, 2, HEAD, VEC><<<grid, block, 0, s>>>(p, tiles, n);
+    if (r == 1) ssm_recurrent_kernel<LN, KI, 1, HEAD, VEC><<<grid, block, 0, s>>>(p, tiles, n);
+    else if (r == 2) ssm_recurrent_kernel<LN, KI, 2, HEAD, VEC><<<grid, block, 0, s>>>(p, tiles, n);
+    else ssm_recurrent_kernel<LN, KI, kMost, HEAD, VEC><<<grid, block, 0, s>>>(p, tiles, n);
     return hipGetLastError();
 }
 
