@@ -922,32 +922,48 @@ __global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t unit
     }
 }
 
+template <int NT, bool PAIR, bool VEC>
+hipError_t launch_segments(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, int32_t blocks, int32_t units,
+                           int32_t pbs, hipStream_t s) {
+    constexpr int W = kSsmWaves;
+    const int32_t halves = PAIR ? 2 : 1;
+    const dim3 grid(uint32_t((plan.slots * p.G + 7) / 8 * 8 * blocks));
+    float *states = static_cast<float *>(workspace);
+    const int64_t pieces = int64_t(p.G) * units * halves;
+    float *decays = states + plan.slots * pieces * (NT * 1024);
+    ssm_chunk_kernel<NT, W, PAIR, VEC, kStates>
+        <<<grid, dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
+    ssm_pass_kernel<NT><<<dim3(uint32_t(p.batch * pieces * NT)), dim3(256), 0, s>>>(p, units * halves, pbs * halves, plan.seg, states,
+                                                                                    decays, svec);
+    ssm_chunk_kernel<NT, W, PAIR, VEC, kSegment>
+        <<<grid, dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
+    return hipGetLastError();
+}
+
 template <int NT, int W, bool PAIR, bool VEC>
 hipError_t launch_w(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
     const int32_t pbs = PAIR ? (p.P + 63) / 64 : 1, units = p.per_group * pbs, per = PAIR ? W / 2 : W;
-    const int32_t blocks = (units + per - 1) / per, halves = PAIR ? 2 : 1;
+    const int32_t blocks = (units + per - 1) / per;
     const auto grid = [&](int64_t places) { return dim3(uint32_t((places * p.G + 7) / 8 * 8 * blocks)); };
     if (!plan.seg) {
         ssm_chunk_kernel<NT, W, PAIR, VEC, kWhole>
             <<<grid(p.batch), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, p.batch, 0, nullptr, nullptr, svec);
         return hipGetLastError();
     }
-    float *states = static_cast<float *>(workspace);
-    const int64_t pieces = int64_t(p.G) * units * halves;
-    float *decays = states + plan.slots * pieces * (NT * 1024);
-    ssm_chunk_kernel<NT, W, PAIR, VEC, kStates>
-        <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
-    ssm_pass_kernel<NT><<<dim3(uint32_t(p.batch * pieces * NT)), dim3(256), 0, s>>>(p, units * halves, pbs * halves, plan.seg, states,
-                                                                                    decays, svec);
-    ssm_chunk_kernel<NT, W, PAIR, VEC, kSegment>
-        <<<grid(plan.slots), dim3(64 * W), 0, s>>>(p, blocks, units, pbs, plan.slots, plan.seg, states, decays, svec);
-    return hipGetLastError();
+    if constexpr (W == kSsmWaves) return launch_segments<NT, PAIR, VEC>(p, svec, plan, workspace, blocks, units, pbs, s);
+    return hipErrorInvalidValue;       // (no plan has it)
 }
 
 template <int NT, bool VEC>
 hipError_t launch_nt(const SsmParams &p, bool svec, const SsmPlan &plan, void *workspace, hipStream_t s) {
-    return plan.pair ? launch_w<NT, kSsmWaves, true, VEC>(p, svec, plan, workspace, s)
-                     : launch_w<NT, kSsmWaves, false, VEC>(p, svec, plan, workspace, s);
+    if (!plan.pair) return launch_w<NT, kSsmWaves, false, VEC>(p, svec, plan, workspace, s);
+    if constexpr (VEC) {
+        // a chunk takes a workgroup of two or four waves less time than one of eight, which fills its CU
+        const int64_t heads = int64_t(p.batch) * p.G, units = int64_t(p.per_group) * ((p.P + 63) / 64);
+        if (!plan.seg && heads * units <= kSsmCus) return launch_w<NT, 2, true, VEC>(p, svec, plan, workspace, s);
+        if (!plan.seg && heads * ((units + 1) / 2) <= kSsmCus) return launch_w<NT, 4, true, VEC>(p, svec, plan, workspace, s);
+    }
+    return launch_w<NT, kSsmWaves, true, VEC>(p, svec, plan, workspace, s);
 }
 
 }  // namespace

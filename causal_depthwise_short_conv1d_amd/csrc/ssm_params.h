@@ -71,7 +71,8 @@ inline int norm_threads(int32_t size) {
 }
 
 constexpr int kSsmChunk = 64;          // tokens of a chunk
-constexpr int kSsmWaves = 8;           // a workgroup of the chunked kernel
+constexpr int kSsmWaves = 8;           // a workgroup of the chunked kernel, fewer in small calls
+constexpr int kSsmCus = 256;
 constexpr int kSsmMaxChunkN = 128;     // states a channel of the chunked kernel
 
 // How the chunked kernel takes a call: its shapes, and whether sequences are cut into segments of `seg` chunks (0: they
