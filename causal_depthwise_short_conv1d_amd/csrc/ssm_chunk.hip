@@ -320,8 +320,10 @@ struct Wave {
     __device__ __forceinline__ void fetch_x(const Rows &r, int32_t c, uint16_t *to, int k0, int k1) {
         if constexpr (VEC) {
             const u32x4 words = r.words(job.n - c * kC);
+            uint32_t at = xo;                          // (unknown to the compiler: it would keep every piece's in a register)
+            asm volatile("" : "+v"(at));
 #pragma unroll
-            for (int k = k0; k < k1; ++k) to_lds(words, xo + 16 * k * r.row, to + 512 * k);
+            for (int k = k0; k < k1; ++k) to_lds(words, at + 16 * k * r.row, to + 512 * k);
         } else {
             const int lane = fresh(), t0 = lane >> 2, ch = ch0 + 8 * ((lane & 3) ^ swz<4>(t0));
 #pragma unroll 1
@@ -333,7 +335,8 @@ struct Wave {
         }
     }
 
-    // The factors of chunk c from its dt.
+    // The factors of chunk c from its dt: those of the states, and with OUT of the outputs.
+    template <bool OUT>
     __device__ __forceinline__ void factors(int32_t c, const Step &dt, float A, float bias, Factors &f) {
         const int lane = fresh();
         float d = ssm_clamp(p, ssm_softplus(p, __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias));
@@ -347,22 +350,26 @@ struct Wave {
         G = dpp_add64<0x118, 0xf>(G);
         G = dpp_add64<0x142, 0xa>(G);
         G = dpp_add64<0x143, 0xc>(G);
-        const double last = lane64<63>(G), mid = lane64<31>(G);
-        const double rel = G - (lane < 32 ? 0.0 : mid);
-        const float r = float(rel);
-        f.eG[lane] = __builtin_amdgcn_exp2f(float(G));
+        const double last = lane64<63>(G);
         f.w[lane] = d * __builtin_amdgcn_exp2f(float(last - G));
-        f.u[lane] = __builtin_amdgcn_exp2f(r);
-        f.v[lane] = d * __builtin_amdgcn_exp2f(-r);
-        if (lane < 32) f.vx[lane] = d * __builtin_amdgcn_exp2f(float(mid - G));
-        const bool plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
-        f.relh[lane] = r;
-        f.rell[lane] = float(rel - double(r));
-        f.d[lane] = d;
         if (lane == 0) {
             f.keep = __builtin_amdgcn_exp2f(float(last));
             f.last = float(last);
-            f.plain = plain;
+        }
+        if constexpr (OUT) {
+            const double mid = lane64<31>(G), rel = G - (lane < 32 ? 0.0 : mid);
+            const float r = float(rel);
+            f.eG[lane] = __builtin_amdgcn_exp2f(float(G));
+            f.u[lane] = __builtin_amdgcn_exp2f(r);
+            f.v[lane] = d * __builtin_amdgcn_exp2f(-r);
+            if (lane < 32) f.vx[lane] = d * __builtin_amdgcn_exp2f(float(mid - G));
+            const bool plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
+            if (!plain) {
+                f.relh[lane] = r;
+                f.rell[lane] = float(rel - double(r));
+                f.d[lane] = d;
+            }
+            if (lane == 0) f.plain = plain;
         }
     }
 
@@ -563,13 +570,15 @@ struct Wave {
     // whatever of them exists (landed() counts them).  r: out's rows of the chunk.
     __device__ __forceinline__ void store(const Rows &r, int32_t c, int it, const f32x16 &y, bool plain) {
         const Rsrc to = r.rsrc(job.n - c * kC);
+        uint32_t at[2] = {oo[0], oo[1]};
+        asm volatile("" : "+v"(at[0]), "+v"(at[1]));
         if (VEC && plain) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = y[8 * k + e];
-                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, oo[k] + 32 * it * r.row, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, at[k] + 32 * it * r.row, 0, 0);
             }
             return;
         }
@@ -597,7 +606,7 @@ struct Wave {
                 for (int e = 0; e < 8; ++e) v[e] = ssm_gate(v[e], zf[e]);
             }
             if constexpr (VEC) {
-                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, oo[k] + 32 * it * r.row, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(v), to, at[k] + 32 * it * r.row, 0, 0);
             } else {
                 uint16_t *o = p.out + row * p.os.st + h * p.os.sh;
 #pragma unroll
@@ -622,6 +631,7 @@ __device__ __forceinline__ void fetch_rows(const Rows &r, uint32_t off, const ui
     constexpr int U = 4 * NT, kPieces = kC * U / 64, kRows = 64 / U;
     static_assert(kRows * W % 8 == 0, "a wave's pieces are swizzled alike");
     const u32x4 words = r.words(job.n - c * kC);
+    asm volatile("" : "+v"(off));
 #pragma unroll
     for (int k = 0; k < (kPieces + W - 1) / W; ++k) {
         const int piece = wave + k * W;
@@ -771,7 +781,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
             wv.load_raw(states + ((slot - 1) * per_slot + piece) * (NT * 1024));
         }
         if (first) {
-            wv.factors(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
+            wv.template factors<kOut>(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
             dt = wv.fetch_dt(job.c0 + 1);
         }
     }
@@ -813,7 +823,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                         wv.template score<1>(Bc, Cc, 0, 0, s);
                         ask(0);
                         wv.put(wv.template weigh<true>(s[0], 0, g, plain, f, D), sc, lane);
-                        if (more) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+                        if (more) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
                     } else {
                         const auto g = wv.template weights<false>(1, f), g1 = wv.template weights<true>(1, f);
                         const bool plain = __builtin_amdgcn_readfirstlane(f.plain);
@@ -847,7 +857,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                     wv.template score<2>(Bc, Cc, 0, 1, t);
                     wv.add(y1, x[0], x[1], wv.template weigh<false>(t[0], 1, wv.template weights<false>(1, f), plain, f, D));
                     wv.add(y1, x[2], x[3], wv.template weigh<true>(t[1], 1, wv.template weights<true>(1, f), plain, f, D));
-                    if (more) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+                    if (more) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
                 }
                 ask(2);
             }
@@ -859,7 +869,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
         } else if (work) {
             if (ahead) wv.fetch_x(xr, c + kAhead, xw, 0, 4);
             xr.next();
-            if (more && first) wv.factors(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+            if (more && first) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
         }
         if (work) {
             wv.advance(B[cur], x, f);
