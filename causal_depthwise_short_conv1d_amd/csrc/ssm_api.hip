@@ -93,9 +93,12 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
     const int64_t units = int64_t(H / G) * (plan.pair ? (int64_t(P) + 63) / 64 : 1);       // of a group
     const int64_t waves = units * (plan.pair ? 2 : 1);
     plan.groups = G * ((waves + kSsmWaves - 1) / kSsmWaves);
-    // a place takes a CU a workgroup: segments, until there is one for each of 256
+    // A place takes a CU a workgroup.  Segments walk all of a sequence at once, but walk it twice, and the first walk and the
+    // pass behind it cost some 25 us: with at most 64 workgroups, from ten chunks a sequence on.  us with / without, 128 heads of
+    // 64 x 128 (32 workgroups a sequence): 256 tokens 42 / 28, 512 55 / 48, 1024 59 / 86; 2 sequences of 1024 90 / 94, 3 110 / 97,
+    // 3 of 4096 335 / 337, 5 of 1024 176 / 128; 64 heads: 256 tokens 39 / 27, 512 44 / 47.
     const int64_t chunks = T / kSsmChunk + batch, mean = T / kSsmChunk / batch;
-    if (workspace && batch * plan.groups < 192 && mean >= 4) {
+    if (workspace && batch * plan.groups <= 64 && mean >= 10) {
         int64_t seg = (chunks * plan.groups + 255) / 256;
         if (seg < 2) seg = 2;
         if (seg < mean) {
@@ -111,9 +114,10 @@ SsmChannelPlan ssm_channel_plan(int64_t T, int64_t batch, int32_t G, int32_t P, 
     SsmChannelPlan plan = {};
     plan.np = N <= 16 ? 16 : (N <= 32 ? 32 : 64);
     plan.groups = G * ((int64_t(P) + kSsmChannels - 1) / kSsmChannels);
-    // four workgroups a CU hide what each waits for
+    // Four workgroups a CU hide what each waits for.  us with segments / without, 8192 channels (32 workgroups a sequence): 128
+    // tokens 47 / 66, 1024 103 / 475, 4 sequences of 512 156 / 245, 8 266 / 247, 12 438 / 313; 64 tokens 45 / 38.
     const int64_t mean = T / batch;
-    if (workspace && batch * plan.groups < 512 && mean >= 128) {
+    if (workspace && batch * plan.groups <= 128 && mean >= 128) {
         int64_t seg = (T * plan.groups + 1023) / 1024;
         seg = (seg < 32 ? 32 : seg) + kSsmTokens - 1;
         seg -= seg % kSsmTokens;
@@ -196,7 +200,9 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
     if (rc != SCONV_OK) return rc;
     p.per_group = p.H / p.G;
     const int64_t T = total_tokens;
-    if (layout.head && p.N <= kSsmMaxChunkN) {
+    // A chunk takes as long as five tokens or so, one after the other: 64 sequences of 4 tokens, 128 heads, 129 us a token at a
+    // time and 160 in chunks, of 8 tokens 218 and 163; 16 sequences of 4 tokens 37 and 45.
+    if (layout.head && p.N <= kSsmMaxChunkN && (T > 5 * int64_t(batch) || batch == 1)) {
         const SsmPlan plan = ssm_plan(T, batch, p.H, p.G, p.P, p.N, workspace != nullptr);
         const int64_t places = (plan.seg ? plan.slots : batch) + 7;
         if (places <= kMaxThreads / (64 * kSsmWaves) / plan.groups && plan.groups <= INT32_MAX) {
@@ -215,7 +221,8 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
             return launch_status(launch_ssm_chunk(p, vec, svec, plan, workspace, stream));
         }
     }
-    if (!layout.head && p.H == p.G && p.N <= kSsmMaxChannelN) {
+    // (64 sequences of 4 tokens of 8192 channels: 38 us a token at a time, 68 with a thread a channel; one of 64 tokens 50 and 38)
+    if (!layout.head && p.H == p.G && p.N <= kSsmMaxChannelN && T > 8 * int64_t(batch)) {
         const SsmChannelPlan plan = ssm_channel_plan(T, batch, p.G, p.P, p.N, workspace != nullptr);
         const int64_t places = plan.seg ? plan.slots : batch;
         if (places <= kMaxThreads / kSsmChannels / plan.groups &&

@@ -86,6 +86,31 @@ def test_fwd_alignment_and_overlap(lib):
         assert fwd(lib, st=addr(x)) == EALIAS, x
 
 
+def test_fwd_workspace(lib):
+    f = lib.ssm_fwd_workspace_bytes
+    need = f(2, 2000, 8, 2, 64, 128, 0)
+    assert need > 0
+    assert fwd(lib, T=2000, ws=addr(14), wb=need) == ELAUNCH
+    assert fwd(lib, T=2000, ws=addr(14), wb=need - 1) == ESHAPE
+    assert fwd(lib, T=2000, ws=ctypes.c_void_p(BASE + 14 * GB + 8), wb=need) == EALIGN
+    for x in (*range(1, 10), 13):
+        assert fwd(lib, T=2000, ws=addr(x), wb=need) == EALIAS, x
+    assert f(2, 600, 8, 2, 64, 128, 0) == 0                     # short sequences
+    assert f(100, 1 << 20, 64, 8, 64, 128, 0) == 0              # many of them
+    assert f(1, 2000, 8, 2, 64, 129, 0) == 0                    # more states than the chunked kernel has
+    channels = dict(H=2, G=2, as_=(64 * 16, 16, 1), ds=(128, 64, 1), db=(64, 1), dd=(64, 1), N=16, xs=(128, 64, 1), zs=(128, 64, 1),
+                    os=(128, 64, 1), ss=(2 * 64 * 16, 64 * 16, 16, 1))
+    need = f(2, 2000, 2, 2, 64, 16, 1)
+    assert need > 0
+    assert fwd(lib, T=2000, ws=addr(14), wb=need, **channels) == ELAUNCH
+    assert fwd(lib, T=2000, ws=addr(14), wb=need - 1, **channels) == ESHAPE
+    assert f(2, 2000, 4, 2, 64, 16, 1) == 0                     # heads that share groups
+    assert f(2, 2000, 2, 2, 64, 65, 1) == 0
+    for bad in ((0, 2000, 8, 2, 64, 128, 0), (2, 0, 8, 2, 64, 128, 0), (2, 2000, 0, 2, 64, 128, 0), (2, 2000, 8, 3, 64, 128, 0),
+                (2, 2000, 8, 0, 64, 128, 0), (2, 2000, 8, 2, 0, 128, 0), (2, 2000, 8, 2, 64, 0, 0), (1, 1 << 31, 8, 2, 64, 128, 0)):
+        assert f(*bad) == 0
+
+
 def update(lib, **kw):
     no_gpu()
     a = dict(x=addr(1), xs=(2048, 512, 64, 1), dt=addr(2), ds=(32, 8, 1, 0), f32=0, a=addr(3), as_=(1, 0, 0), b=addr(4),
