@@ -1,9 +1,10 @@
 /*
  * sconv.h -- C ABI of libsconv, a gfx950 (MI355X) library for the causal
  * depthwise short convolution (width 2..5) used by hybrid / linear-attention
- * language models, for the gated delta rule that such a layer feeds with the
- * convolution's output, and for the verification of drafted tokens that
- * yields the convolution's and the delta rule's num_accepted_tokens.
+ * language models, for the two recurrences that such a layer feeds with the
+ * convolution's output (the gated delta rule, the selective state space scan)
+ * and the gated group norm behind them, and for the verification of drafted
+ * tokens that yields their num_accepted_tokens.
  *
  * The operation, in the notation of the pages it comes from:
  *
@@ -610,9 +611,14 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  * num_heads must be a multiple of num_groups and state_dim at most 256 (else
  *   SCONV_ERR_SHAPE), total_tokens at most 2^31 - 257, and a call's rows of
  *   state (entries x num_heads x head_dim) below about 2^29.
- * Layouts and speed (results agree to rounding): unit strides of b, c and the
- *   state, state_dim a multiple of 4 and rows aligned to 16 bytes take the
- *   vector loads; every other layout loads by elements.
+ * Layouts and speed (results agree to rounding).  Decode: unit strides of b, c
+ *   and the state (and of a where channels have decays), state_dim a multiple
+ *   of 4 and every base and stride of four elements take 16-byte pieces.
+ *   Prefill with one decay a head: unit strides of x, b, c, z and out, head_dim
+ *   and state_dim multiples of 8, bases of 16 bytes, strides of 8 elements and
+ *   below 2^23, tokens at least as far apart as what is read of them.  Prefill
+ *   with one a channel: unit channel strides of x, dt, z and out, tokens as
+ *   above.  Every other layout loads by elements.
  * Errors: a NULL tensor -> SCONV_ERR_NULL; bad sizes -> SCONV_ERR_SHAPE; a
  *   negative stride, or out / state with two elements at one address ->
  *   SCONV_ERR_STRIDE; a pointer not aligned to its elements ->
@@ -628,14 +634,25 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  * to its line (a sequence of no tokens writes nothing).  state may be NULL:
  * zero states, none written.  Rows of skipped sequences and rows behind the
  * last sequence are left untouched.
- * Heads with one decay and up to 128 states a channel are processed in chunks of
- * 64 tokens on the matrix cores.  In a chunk an infinity or NaN in a token's x may
- * reach the other tokens of its chunk, sequence and head, earlier ones too.
+ * One decay a head, up to 128 states a channel: chunks of 64 tokens on the
+ * matrix cores.  In a chunk
+ *   - products that feed the state have operands of 24 bits, those that only
+ *     feed out (the state with c, the scores with x) of 17, where out has 8;
+ *   - an infinity or NaN in a token's x may reach the other tokens of its
+ *     chunk, sequence and head, earlier ones too, and an infinite state counts
+ *     as NaN;
+ *   - a decay below e^-200 a token counts as 0.
+ * One decay a channel and state, heads as many as groups, up to 64 states: a
+ * token at a time with a thread a channel.  Everything else, and sequences of a
+ * few tokens, go as in decode.
  * workspace    device memory, 16-byte aligned, in use until the call's work is
  *              done, or NULL.  With ssm_fwd_workspace_bytes() bytes of it, calls
- *              of few heads and long sequences take three kernels that walk all
- *              segments of their sequences at once.  Smaller than asked for ->
- *              SCONV_ERR_SHAPE.
+ *              of few heads (or channels) and long sequences take three kernels
+ *              that walk all segments of their sequences at once; without it
+ *              they take one, several times as long.  Smaller than asked for ->
+ *              SCONV_ERR_SHAPE.  It holds the segments' states, and does not grow
+ *              with the call: 45 MB at most, 80 MB with one decay a channel and
+ *              64 states (19 MB with 16).
  */
 int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,
                    const void *dt, int64_t dt_stride_tok, int64_t dt_stride_head, int64_t dt_stride_dim, int32_t dt_fp32,
