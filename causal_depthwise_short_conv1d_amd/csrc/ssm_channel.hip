@@ -12,6 +12,13 @@
 // call's channels and sequences do not fill the chip, sequences are cut into
 // segments that are walked twice at once: for the states at their ends, from
 // empty ones, then, once a pass over the segments has joined these, for the outputs.
+//
+// Bound by the vector instructions, of which an exponential takes as long as two:
+// 4195 tokens of 8192 channels with 16 states take 119 us for the states, 12 for the
+// pass and 147 for the outputs, of which, by leaving each out in turn, the
+// exponentials are about 30, the softplus 22 and the wait for x, dt and z 36.
+// B and C in scalar registers took as long as from LDS; more waves a SIMD than
+// four spill.
 #include <type_traits>
 
 #include "ssm_device.h"

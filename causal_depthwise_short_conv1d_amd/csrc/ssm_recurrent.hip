@@ -10,6 +10,14 @@
 // other; everything else is a few KiB.  State rows pass the caches
 // (nontemporal): a step reads a line once, and the next step comes after a
 // model's other layers.
+//
+// Bound by the states' bytes: 256 requests of 128 heads of 64 x 128 355 us, 6.0 TB/s;
+// 64 requests of 4 tokens with each token's states saved 240 (writes, 5.6 TB/s).
+// Small calls are bound by the chain of loads: one request of 64 heads 4.9 us; 64
+// requests of 8192 channels x 16 states 19.8 us (26.5 with one row group a wave
+// and decays by elements), two generations of waves for 72 MB.  Workgroups of
+// eight waves were slower (409 against 368 us at 256 requests), and so were
+// states through the caches (21.7 against 20.6 at 64).
 #include "ssm_device.h"
 
 namespace sconv {
