@@ -181,3 +181,9 @@ def test_empty_calls(form):
     d = R.on(R.draw((0, 1), *form, 1), DEV)
     assert call_update(d, st).shape == d["x"].shape
     assert torch.equal(st, before)
+
+
+@pytest.mark.parametrize("lens,form", [([769] * 20, ("head", 2, 64, 1, 64)), ([257] * 40, ("channel", 1, 70, 1, 20))])
+def test_segments_whose_last_one_ends_first(lens, form):
+    """Last segments of one token, which write their lines while the first ones are at work, on lines that hold a state."""
+    prefill(lens, *form, seed=12, init=[True] * len(lens), slow=0.05)
