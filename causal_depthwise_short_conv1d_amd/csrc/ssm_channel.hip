@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
     if (place >= places) return;
     const int32_t g = int32_t(gb / uint32_t(blocks)), c0 = int32_t(gb % uint32_t(blocks)) * kThreads;
     SsmSpan sp;
-    int64_t slot = 0, t0 = 0, t1, before = 0;
+    int64_t slot = 0, t0 = 0, t1;
     int32_t b = int32_t(place);
     if constexpr (MODE != kWhole) {
         slot = place;
@@ -88,7 +88,6 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
         if (k < 0 || t0 >= sp.n) return;
         if (MODE == kStates && t0 + seg >= sp.n) return;           // the last segment's end is no one's start
         t1 = t0 + seg < sp.n ? t0 + seg : sp.n;
-        before = slot + (k > 0 ? -1 : (sp.n - 1) / seg);           // the slot that the segment's first states are in
     }
     for (int i = threadIdx.x; i < 2 * kTB * kRow; i += kThreads) (&bc[0][0][0])[i] = 0.0f;
 
@@ -111,7 +110,7 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
     if (MODE == kSegment && sp.n > seg) {
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-            if (n < p.N) S[n] = pieces[before * per_slot + piece].S[n][lane];
+            if (n < p.N) S[n] = pieces[slot * per_slot + piece].S[n][lane];
     } else if (kOut) {
         if (sp.init) {
 #pragma unroll
@@ -250,9 +249,8 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
     }
 }
 
-// From each segment's own states to those that the next one starts from, in place: a thread takes a state of a channel through a
-// sequence's segments.  What the first one starts from goes to the last one's place, which has no states of its own: in the third
-// kernel the last segment may write the line before the first has begun.
+// From each segment's own states to those that it starts from, in place: a thread takes a state of a channel through a sequence's
+// segments.  The first one's are among them: in the third kernel the last segment may write the line before the first has begun.
 template <int NP>
 __global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int32_t blocks, int32_t seg, void *ws) {
     const int64_t per_slot = int64_t(p.G) * blocks * (kThreads / 64);
@@ -269,7 +267,6 @@ __global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int3
     float S = 0.0f;
     if (sp.init) S = p.state[sp.line * p.s_sl + g * p.s_sh + c * p.s_sp + n * p.s_sn];
     Piece<NP> *at = static_cast<Piece<NP> *>(ws) + first_slot(p, b, seg) * per_slot + piece;
-    if (ns > 1) at[(ns - 1) * per_slot].S[n][lane] = S;
     constexpr int kFew = 4;            // segments read together
     for (int64_t i = 0; i + 1 < ns; i += kFew) {
         float own[kFew], sum[kFew];
@@ -282,10 +279,11 @@ __global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int3
 #pragma unroll
         for (int k = 0; k < kFew; ++k) {
             if (i + k + 1 >= ns) break;
-            S = fmaf(__builtin_amdgcn_exp2f(a * sum[k]), S, own[k]);
             at[(i + k) * per_slot].S[n][lane] = S;
+            S = fmaf(__builtin_amdgcn_exp2f(a * sum[k]), S, own[k]);
         }
     }
+    if (ns > 1) at[(ns - 1) * per_slot].S[n][lane] = S;
 }
 
 template <int NP, bool DT32, bool ROWS>

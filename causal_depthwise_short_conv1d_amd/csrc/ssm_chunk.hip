@@ -736,14 +736,12 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     const int32_t nc = int32_t((sp.n + kC - 1) / kC);
     job.c0 = 0;
     job.c1 = nc;
-    int64_t before = 0;                // the slot that a segment's first states are in
     if constexpr (MODE != kWhole) {
         const int64_t k = slot - first_slot(p, b, seg);
         if (k < 0 || k * seg >= nc) return;
         if (MODE == kStates && (k + 1) * seg >= nc) return;        // the last segment's end is no one's start
         job.c0 = int32_t(k * seg);
         job.c1 = job.c0 + seg < nc ? job.c0 + seg : nc;
-        before = slot + (k > 0 ? -1 : (nc - 1) / seg);
     }
 
     // columns and rows that a chunk may lack
@@ -791,7 +789,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
         if (kAhead == 2 && job.c0 + 1 < job.c1) wv.fetch_x(xr, job.c0 + 1, xl[kAhead - 1][wave], 0, 4);
         if (kAhead == 2) xr.next();
         if (MODE == kSegment && nc > seg) {
-            wv.load_raw(states + (before * per_slot + piece) * (NT * 1024));
+            wv.load_raw(states + (slot * per_slot + piece) * (NT * 1024));
         } else if (MODE != kStates) {
             if (sp.init) wv.load(rows, svec);
         }
@@ -907,9 +905,8 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     }
 }
 
-// From each segment's own states to the states that the next one starts from, in place: a thread takes 4 of them through a
-// sequence's segments.  What the first one starts from goes to the last one's place, which has no states of its own: in the third
-// kernel the last segment may write the line before the first has begun.
+// From each segment's own states to the states that it starts from, in place: a thread takes 4 of them through a sequence's
+// segments.  The first one's are among them: in the third kernel the last segment may write the line before the first has begun.
 template <int NT>
 __global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t units, int32_t pbs, int32_t seg, float *states,
                                                        const float *decays, bool svec) {
@@ -940,13 +937,14 @@ __global__ __launch_bounds__(256) void ssm_pass_kernel(SsmParams p, int32_t unit
         }
     }
     const int64_t first = first_slot(p, b, seg) * per_slot + piece;
-    *reinterpret_cast<f32x4 *>(states + (first + (ns - 1) * per_slot) * (NT * 1024) + quad * 4) = S;
+    const auto place = [&](int32_t i) { return reinterpret_cast<f32x4 *>(states + (first + i * per_slot) * (NT * 1024) + quad * 4); };
     for (int32_t i = 0; i + 1 < ns; ++i) {
-        const int64_t at = first + i * per_slot;
-        f32x4 *s = reinterpret_cast<f32x4 *>(states + at * (NT * 1024) + quad * 4);
-        S = S * decays[at] + *s;
+        f32x4 *s = place(i);
+        const f32x4 end = S * decays[first + i * per_slot] + *s;
         *s = S;
+        S = end;
     }
+    *place(ns - 1) = S;
 }
 
 template <int NT, bool PAIR, bool VEC>
