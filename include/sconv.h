@@ -643,7 +643,8 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  *     as NaN;
  *   - a decay below e^-200 a token counts as 0.
  * One decay a channel and state, heads as many as groups, up to 64 states: a
- * token at a time with a thread a channel.  Everything else, and sequences of a
+ * token at a time with a thread a channel (there and in decode an infinity in a
+ * token's step or x may count as NaN from that token on).  Everything else, and sequences of a
  * few tokens, go as in decode.
  * workspace    device memory, 16-byte aligned, in use until the call's work is
  *              done, or NULL.  With ssm_fwd_workspace_bytes() bytes of it, calls
