@@ -73,11 +73,12 @@ __device__ __forceinline__ int swz(int r) {
 // 16 bytes a lane from byte `at` of r to lds + 16 lane, past the registers.  What lies past r's end may or may not be written
 // as zero: those places hold zeros or an earlier chunk's rows.  Written as an instruction (it has no register to be written
 // late): the builtin makes the compiler wait for it before the next read of the same array, the other buffer's included, which
-// is a trip to memory in every chunk.  landed() waits for it; no other
-// instruction here goes by m0.
+// is a trip to memory in every chunk.  landed() waits for it.  The compiler keeps nothing in m0.  A vector instruction (the
+// v_readlane of a spilled word) may have written r just before: five wait states lie between, which the compiler does not put in
+// front of what it does not know.
 __device__ __forceinline__ void to_lds(const u32x4 &r, uint32_t at, void *lds) {
     const uint32_t to = __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>(lds)));   // (its place in the LDS)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(r), "s"(to) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(r), "s"(to) : "memory");
 }
 // A barrier for what waves exchange through ds_write: what is on its way to LDS past the registers stays on its way.
 __device__ __forceinline__ void exchange() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
