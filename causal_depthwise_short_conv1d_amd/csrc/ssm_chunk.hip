@@ -21,10 +21,9 @@
 // (ds_read_b64_tr_b16).  Rows of S and of y are taken in the order n = r with bits
 // 2 and 3 swapped, so that a lane holds 8 neighbours: 16-byte reads and writes.
 //
-// Precision.  x, B and C are bf16 and enter as they are; every other operand is
-// split into bf16 parts, which have fp32's range: e^(..) d x, which feeds the
-// state, into three (24 bits); S and the scores, which only feed the bf16
-// output, into two (to 2^-17 of each).  All sums are fp32, G is fp64.
+// Precision.  x, B and C are bf16 and enter as they are; every other operand
+// (e^(..) d x, S, the scores) is split into three bf16 parts, which hold all of
+// its 24 bits and have fp32's range.  All sums are fp32, G is fp64.
 //
 // Bound by the issue of instructions: of a chunk's 17 K cycles the two waves of a
 // SIMD have 6.7 K of matrix products (32 cycles each) and 7 K of vector
@@ -51,15 +50,18 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kC = kSsmChunk;          // tokens per chunk
 constexpr int kPW = 32;                // channels a wave
 
-// A head's factors of a chunk, per token, in the LDS of its wave.
+// A head's factors of a chunk, per token, in LDS: those of its states, whose next chunk's come beside them, and those of its
+// outputs, which take the place of the last chunk's once both waves are done with these.
+struct alignas(16) Keeps {
+    float w[kC];                       // e^(G_last - G) d
+    float keep, last;                  // e^G_last, G_last in powers of 2
+};
 struct alignas(16) Factors {
     float eG[kC];                      // e^G
-    float w[kC];                       // e^(G_last - G) d
     float u[kC];                       // e^(G - R), R: G at the start of the token's half
-    float v[kC];                       // e^(R - G) d
+    float v[kC];                       // plain: e^(R - G) d, else d
     float vx[kC / 2];                  // e^(R_1 - G) d of the first half
-    float relh[kC], rell[kC], d[kC];   // G - R in two parts, in powers of 2, and the step
-    float keep, last;                  // e^G_last, G_last in powers of 2
+    float relh[kC], rell[kC];          // G - R in two parts, in powers of 2
     int plain;                         // e^(R - G) does not pass 2^64
 };
 
@@ -140,20 +142,11 @@ __device__ __forceinline__ uint32_t upper(float a, float b) {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 __device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-// x = hi + lo to 2^-17 of it.  (Cut off, not rounded: a conversion takes 6.5 cycles where a logical instruction takes 4, and
-// a dot product with (-1, 0) in place of the two for what is left takes 8 beside another wave's matrix products.)
-__device__ __forceinline__ void split2(const float (&x)[8], bf16x8 &hi, bf16x8 &lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = upper(x[2 * i], x[2 * i + 1]);
-        l[i] = pack_bf16x2(below(x[2 * i]), below(x[2 * i + 1]));
-    }
-    hi = as_bf16(h);
-    lo = as_bf16(l);
-}
-// ... in three parts, to 2^-24.
-__device__ __forceinline__ void split3(const float (&x)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
+// x = hi + mid + lo: each takes the next 8 of its 24 bits.  (Cut off, not rounded: a conversion takes 6.5 cycles where a logical
+// instruction takes 4, and a dot product with (-1, 0) in place of the two for what is left takes 8 beside another wave's matrix
+// products.)
+struct Parts { bf16x8 hi, mid, lo; };
+__device__ __forceinline__ Parts split(const float (&x)[8]) {
     uint32_t h[4], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -162,9 +155,7 @@ __device__ __forceinline__ void split3(const float (&x)[8], bf16x8 &hi, bf16x8 &
         m[i] = upper(a, b);
         l[i] = upper(below(a), below(b));
     }
-    hi = as_bf16(h);
-    mid = as_bf16(m);
-    lo = as_bf16(l);
+    return {as_bf16(h), as_bf16(m), as_bf16(l)};
 }
 
 // x + the value that lane CTRL's pattern moves here (fp64, 0 where it moves none).
@@ -219,8 +210,9 @@ struct Rows {
 
 enum Mode { kWhole, kStates, kSegment };
 
-// A tile of scores as an operand of its product with x: two steps of 16 tokens, high and low parts.
-struct Scores { bf16x8 hi[2], lo[2]; };
+// A tile of scores as an operand of its product with x: two steps of 16 tokens.
+struct Scores { Parts k[2]; };
+constexpr int kTile = 3 * 2 * 64 * 8;  // halves
 
 template <int NT, bool VEC>
 struct Wave {
@@ -349,9 +341,10 @@ struct Wave {
         }
     }
 
-    // The factors of chunk c from its dt: those of the states, and with OUT of the outputs.
+    // The factors of chunk c from its dt: those of the states, and with OUT of the outputs, a token a lane.
+    struct Decays { float eG, u, v, vx, relh, rell; bool plain; };
     template <bool OUT>
-    __device__ __forceinline__ void factors(int32_t c, const Step &dt, float A, float bias, Factors &f) {
+    __device__ __forceinline__ Decays factors(int32_t c, const Step &dt, float A, float bias, Keeps &f) {
         const int lane = fresh();
         float d = ssm_clamp(p, ssm_softplus(p, __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias));
         if (c * kC + lane >= job.n) d = 0.0f;
@@ -370,21 +363,30 @@ struct Wave {
             f.keep = __builtin_amdgcn_exp2f(float(last));
             f.last = float(last);
         }
+        Decays r = {};
         if constexpr (OUT) {
             const double mid = lane64<31>(G), rel = G - (lane < 32 ? 0.0 : mid);
-            const float r = float(rel);
-            f.eG[lane] = __builtin_amdgcn_exp2f(float(G));
-            f.u[lane] = __builtin_amdgcn_exp2f(r);
-            f.v[lane] = d * __builtin_amdgcn_exp2f(-r);
-            if (lane < 32) f.vx[lane] = d * __builtin_amdgcn_exp2f(float(mid - G));
-            const bool plain = __builtin_amdgcn_ballot_w64(!(r > -64.0f)) == 0;
-            if (!plain) {
-                f.relh[lane] = r;
-                f.rell[lane] = float(rel - double(r));
-                f.d[lane] = d;
-            }
-            if (lane == 0) f.plain = plain;
+            r.relh = float(rel);
+            r.rell = float(rel - double(r.relh));
+            r.plain = __builtin_amdgcn_ballot_w64(!(r.relh > -64.0f)) == 0;
+            r.eG = __builtin_amdgcn_exp2f(float(G));
+            r.u = __builtin_amdgcn_exp2f(r.relh);
+            r.v = r.plain ? d * __builtin_amdgcn_exp2f(-r.relh) : d;
+            r.vx = d * __builtin_amdgcn_exp2f(float(mid - G));
         }
+        return r;
+    }
+    __device__ __forceinline__ void put(const Decays &r, Factors &f) const {
+        const int lane = fresh();
+        f.eG[lane] = r.eG;
+        f.u[lane] = r.u;
+        f.v[lane] = r.v;
+        if (lane < 32) f.vx[lane] = r.vx;
+        if (!r.plain) {
+            f.relh[lane] = r.relh;
+            f.rell[lane] = r.rell;
+        }
+        if (lane == 0) f.plain = r.plain;
     }
 
     // x^T: channel chan() a lane, 16 tokens each.
@@ -395,24 +397,25 @@ struct Wave {
     }
 
     // S <- e^G_last S + sum_j w_j x_j B_j^T
-    __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], const Factors &f) {
+    __device__ __forceinline__ void advance(const uint16_t *B, const bf16x8 (&x)[4], const Keeps &f) {
         const int lane = fresh(), hh = lane >> 5;
         const float keep = f.keep;
         f32x4 w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = row4(f.w + 8 * k + 4 * hh);
-        bf16x8 b[2][NT], hi[2], mid[2], lo[2];
+        bf16x8 b[2][NT];
+        Parts xp[2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) b[0][i] = read_cols<U>(B, 0, i, lane);
         issued();
-        const auto split = [&](int k) {
+        const auto weigh_x = [&](int k) {
             float xw[8];
             unpack8(__builtin_bit_cast(u32x4, x[k]), xw);
 #pragma unroll
             for (int e = 0; e < 8; ++e) xw[e] *= w[2 * k + (e >> 2)][e & 3];
-            split3(xw, hi[k & 1], mid[k & 1], lo[k & 1]);
+            xp[k & 1] = split(xw);
         };
-        split(0);
+        weigh_x(0);
 #pragma unroll
         for (int i = 0; i < NT; ++i) S[i] *= keep;
         // The next 16 tokens' operands are read and split between this step's products.
@@ -422,14 +425,14 @@ struct Wave {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) b[(k + 1) & 1][i] = read_cols<U>(B, 16 * k + 16, i, lane);
                 issued();
-                split(k + 1);
+                weigh_x(k + 1);
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], hi[k & 1], S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], xp[k & 1].hi, S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], mid[k & 1], S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], xp[k & 1].mid, S[i]);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], lo[k & 1], S[i]);
+            for (int i = 0; i < NT; ++i) S[i] = mfma(b[k & 1][i], xp[k & 1].lo, S[i]);
             if (k < 3) interleave<3 * NT>();
         }
     }
@@ -486,11 +489,11 @@ struct Wave {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int j = 32 * half + 8 * k + 4 * hh;
-                const f32x4 jh = row4(f.relh + j), jl = row4(f.rell + j), d = row4(f.d + j);
+                const f32x4 jh = row4(f.relh + j), jl = row4(f.rell + j);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = (ih - jh[e]) + (il - jl[e]), g = d[e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a);
-                    v[4 * k + e] = s[4 * k + e] * (8 * k + e <= i ? g : 0.0f);
+                    const float a = (ih - jh[e]) + (il - jl[e]), d = g.v[k][e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a);
+                    v[4 * k + e] = s[4 * k + e] * (8 * k + e <= i ? d : 0.0f);
                 }
             }
         } else {
@@ -510,20 +513,20 @@ struct Wave {
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = v[8 * k + e];
-            split2(t, r.hi[k], r.lo[k]);
+            r.k[k] = split(t);
         }
         return r;
     }
     static __device__ __forceinline__ void put(const Scores &s, uint16_t *at, int lane) {
         bf16x8 *o = reinterpret_cast<bf16x8 *>(at) + lane;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) { o[128 * k] = s.hi[k]; o[128 * k + 64] = s.lo[k]; }
+        for (int k = 0; k < 2; ++k) { o[192 * k] = s.k[k].hi; o[192 * k + 64] = s.k[k].mid; o[192 * k + 128] = s.k[k].lo; }
     }
     static __device__ __forceinline__ Scores get(const uint16_t *at, int lane) {
         const bf16x8 *o = reinterpret_cast<const bf16x8 *>(at) + lane;
         Scores s;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) { s.hi[k] = o[128 * k]; s.lo[k] = o[128 * k + 64]; }
+        for (int k = 0; k < 2; ++k) s.k[k] = {o[192 * k], o[192 * k + 64], o[192 * k + 128]};
         return s;
     }
 
@@ -540,17 +543,17 @@ struct Wave {
         };
         fetch(0);
         issued();
-        bf16x8 hi[2][2], lo[2][2];
-        const auto split = [&](int g) {
+        Parts s[2][2];
+        const auto split_s = [&](int g) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float t[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = S[g][8 * k + e];
-                split2(t, hi[g & 1][k], lo[g & 1][k]);
+                s[g & 1][k] = split(t);
             }
         };
-        split(0);
+        split_s(0);
         y0 = zero16();
         y1 = zero16();
 #pragma unroll
@@ -558,26 +561,30 @@ struct Wave {
             if (g + 1 < NT) {
                 fetch(g + 1);
                 issued();
-                split(g + 1);
+                split_s(g + 1);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                y0 = mfma(hi[g & 1][k], c[g & 1][k][0], y0);
-                y1 = mfma(hi[g & 1][k], c[g & 1][k][1], y1);
-                y0 = mfma(lo[g & 1][k], c[g & 1][k][0], y0);
-                y1 = mfma(lo[g & 1][k], c[g & 1][k][1], y1);
+                y0 = mfma(s[g & 1][k].hi, c[g & 1][k][0], y0);
+                y1 = mfma(s[g & 1][k].hi, c[g & 1][k][1], y1);
+                y0 = mfma(s[g & 1][k].mid, c[g & 1][k][0], y0);
+                y1 = mfma(s[g & 1][k].mid, c[g & 1][k][1], y1);
+                y0 = mfma(s[g & 1][k].lo, c[g & 1][k][0], y0);
+                y1 = mfma(s[g & 1][k].lo, c[g & 1][k][1], y1);
             }
-            if (g + 1 < NT) interleave<8>();
+            if (g + 1 < NT) interleave<12>();
         }
         y0 *= e0;
         y1 *= e1;
     }
     // y += P x of a tile
     static __device__ __forceinline__ void add(f32x16 &y, const bf16x8 &xa, const bf16x8 &xb, const Scores &s) {
-        y = mfma(xa, s.hi[0], y);
-        y = mfma(xb, s.hi[1], y);
-        y = mfma(xa, s.lo[0], y);
-        y = mfma(xb, s.lo[1], y);
+        y = mfma(xa, s.k[0].hi, y);
+        y = mfma(xb, s.k[1].hi, y);
+        y = mfma(xa, s.k[0].mid, y);
+        y = mfma(xb, s.k[1].mid, y);
+        y = mfma(xa, s.k[0].lo, y);
+        y = mfma(xb, s.k[1].lo, y);
     }
 
     // Outputs of the lane's token of half `it`: channels 8 (l / 32) .. and 16 + 8 (l / 32) .. of the wave's.  VEC: two writes,
@@ -703,10 +710,13 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     constexpr bool kOut = MODE != kStates;
     // Rows come one chunk ahead; where a chunk takes little time, two.
     constexpr int kAhead = kOut ? 1 : 2, kBufs = kAhead + 1;
-    __shared__ alignas(16) uint16_t B[kBufs][kBC], C[kOut ? kBufs : 1][kOut ? kBC : 8];
+    // (of C one chunk where the waves meet behind its last read: the next one's comes then)
+    constexpr int kCBufs = kOut && !PAIR ? kBufs : 1;
+    __shared__ alignas(16) uint16_t B[kBufs][kBC], C[kCBufs][kOut ? kBC : 8];
     __shared__ alignas(16) uint16_t xl[kAhead][W][kC * kPW];
-    __shared__ alignas(16) uint16_t scores[kOut && PAIR ? kUnits : 1][kOut && PAIR ? 3 * 2048 : 8];
-    __shared__ Factors factors[kUnits][2];
+    __shared__ alignas(16) uint16_t scores[kOut && PAIR ? kUnits : 1][kOut && PAIR ? 3 * kTile : 8];
+    __shared__ Keeps keeps[kUnits][2];
+    __shared__ Factors factors[kOut ? kUnits : 1];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
 
     // Blocks go to the 8 XCDs in turn: those of one place and group, which read the same B and C, follow each other on one.
@@ -748,7 +758,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     // columns and rows that a chunk may lack
     for (int i = threadIdx.x; i < kBufs * kBC / 8; i += 64 * W) {
         reinterpret_cast<u32x4 *>(&B[0][0])[i] = u32x4{0, 0, 0, 0};
-        if (kOut) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
+        if (kOut && i < kCBufs * kBC / 8) reinterpret_cast<u32x4 *>(&C[0][0])[i] = u32x4{0, 0, 0, 0};
     }
     for (int i = threadIdx.x; i < kAhead * W * kC * kPW / 8; i += 64 * W) reinterpret_cast<u32x4 *>(&xl[0][0][0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
@@ -777,9 +787,10 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
         br.next();
     };
     const auto fetch_c = [&](int32_t c, int buf) {
-        if (kOut) fetch_rows<NT, W, VEC>(cr, co, Cg, p.cs, p.N, job, c, C[kOut ? buf : 0], wave, lane);
+        if (kOut) fetch_rows<NT, W, VEC>(cr, co, Cg, p.cs, p.N, job, c, C[kCBufs > 1 ? buf : 0], wave, lane);
         cr.next();
     };
+    Factors &f = factors[kOut ? own : 0];
     typename Wave<NT, VEC>::Step dt = {0, 0};
     wv.zero();
     fetch_b(job.c0, 0);
@@ -795,7 +806,8 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
             if (sp.init) wv.load(rows, svec);
         }
         if (first) {
-            wv.template factors<kOut>(job.c0, wv.fetch_dt(job.c0), A, bias, factors[own][0]);
+            const auto r = wv.template factors<kOut>(job.c0, wv.fetch_dt(job.c0), A, bias, keeps[own][0]);
+            if (kOut) wv.put(r, f);
             dt = wv.fetch_dt(job.c0 + 1);
         }
     }
@@ -809,7 +821,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
     for (int32_t c = job.c0; c < job.c1; ++c) {
         const int odd = (c - job.c0) & 1, next = cur + kAhead < kBufs ? cur + kAhead : cur + kAhead - kBufs;
         const bool more = c + 1 < job.c1, ahead = c + kAhead < job.c1;
-        const Factors &f = factors[own][odd];
+        const Keeps &keep = keeps[own][odd];
         uint16_t *xw = xl[kAhead == 2 ? odd : 0][wave];
         bf16x8 x[4];
         if (work) wv.read_x(xw, x);
@@ -821,7 +833,8 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
         if (ahead) fetch_b(c + kAhead, next);
         if constexpr (kOut) {
             f32x16 y0, y1;
-            const uint16_t *Bc = B[cur], *Cc = C[cur];
+            const uint16_t *Bc = B[cur], *Cc = C[kCBufs > 1 ? cur : 0];
+            typename Wave<NT, VEC>::Decays later_f = {};
             const auto ask = [&](int part) {
                 if (!ahead) return;
                 if (part < 2 && work) wv.fetch_x(xr, c + kAhead, xw, 2 * part, 2 * part + 2);
@@ -837,23 +850,24 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                         wv.template score<1>(Bc, Cc, 0, 0, s);
                         ask(0);
                         wv.put(wv.template weigh<true>(s[0], 0, g, plain, f, D), sc, lane);
-                        if (more) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+                        if (more) later_f = wv.template factors<kOut>(c + 1, dt, A, bias, keeps[own][odd ^ 1]);
                     } else {
                         const auto g = wv.template weights<false>(1, f), g1 = wv.template weights<true>(1, f);
                         const bool plain = __builtin_amdgcn_readfirstlane(f.plain);
                         f32x16 s[2];
                         wv.template score<2>(Bc, Cc, 0, 1, s);
                         ask(0);
-                        wv.put(wv.template weigh<false>(s[0], 1, g, plain, f, D), sc + 2048, lane);
-                        wv.put(wv.template weigh<true>(s[1], 1, g1, plain, f, D), sc + 4096, lane);
+                        wv.put(wv.template weigh<false>(s[0], 1, g, plain, f, D), sc + kTile, lane);
+                        wv.put(wv.template weigh<true>(s[1], 1, g1, plain, f, D), sc + 2 * kTile, lane);
                     }
                     ask(1);
                     wv.from_state(Cc, f, y0, y1);
                 }
-                ask(2);
                 exchange();
+                ask(2);
                 if (work) {
-                    const Scores s00 = wv.get(sc, lane), s01 = wv.get(sc + 2048, lane), s11 = wv.get(sc + 4096, lane);
+                    if (more && first) wv.put(later_f, f);
+                    const Scores s00 = wv.get(sc, lane), s01 = wv.get(sc + kTile, lane), s11 = wv.get(sc + 2 * kTile, lane);
                     issued();
                     wv.add(y0, x[0], x[1], s00);
                     wv.add(y1, x[0], x[1], s01);
@@ -871,7 +885,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
                     wv.template score<2>(Bc, Cc, 0, 1, t);
                     wv.add(y1, x[0], x[1], wv.template weigh<false>(t[0], 1, wv.template weights<false>(1, f), plain, f, D));
                     wv.add(y1, x[2], x[3], wv.template weigh<true>(t[1], 1, wv.template weights<true>(1, f), plain, f, D));
-                    if (more) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+                    if (more) wv.put(wv.template factors<kOut>(c + 1, dt, A, bias, keeps[own][odd ^ 1]), f);
                 }
                 ask(2);
             }
@@ -883,11 +897,11 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
         } else if (work) {
             if (ahead) wv.fetch_x(xr, c + kAhead, xw, 0, 4);
             xr.next();
-            if (more && first) wv.template factors<kOut>(c + 1, dt, A, bias, factors[own][odd ^ 1]);
+            if (more && first) wv.template factors<kOut>(c + 1, dt, A, bias, keeps[own][odd ^ 1]);
         }
         if (work) {
-            wv.advance(B[cur], x, f);
-            if (MODE == kStates) total += f.last;
+            wv.advance(B[cur], x, keep);
+            if (MODE == kStates) total += keep.last;
         }
         dt = later;
         // The next chunk's rows are there.  Behind them a wave has asked for nothing but its 4 writes of this chunk's outputs, or

@@ -635,9 +635,7 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  * zero states, none written.  Rows of skipped sequences and rows behind the
  * last sequence are left untouched.
  * One decay a head, up to 128 states a channel: chunks of 64 tokens on the
- * matrix cores.  In a chunk
- *   - products that feed the state have operands of 24 bits, those that only
- *     feed out (the state with c, the scores with x) of 17, where out has 8;
+ * matrix cores, whose operands keep fp32's 24 bits.  In a chunk
  *   - an infinity or NaN in a token's x may reach the other tokens of its
  *     chunk, sequence and head, earlier ones too, and an infinite state counts
  *     as NaN;
