@@ -9,11 +9,14 @@ namespace sconv {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // softplus(v), or v where the steps come without.  log1p(e) with e = e^-|v| is 2 atanh(q), q = e / (2 + e) <= 1/3: the series'
-// next term is below 2^-26 of it.  Roundings of 2^-24: |v| + 1 in the exponent, 2 each of exp2 and the reciprocal, 1 each of
-// 2 + e, q, the series, the sum.
+// next term is below 2^-26 of it.  The exponent goes in two parts (its product's rounding alone would move e by |v| 2^-24), up to
+// 128, where e is 0.
+// Roundings of 2^-24: 3 of e, 1 of 2 + e, 2 of its reciprocal, 1 of q, 2 of the series, 1 of the sum.
 __device__ __forceinline__ float ssm_softplus(const SsmParams &p, float v) {
     if (!p.softplus) return v;
-    const float e = __builtin_amdgcn_exp2f(fabsf(v) * -kLog2e), q = e * __builtin_amdgcn_rcpf(2.0f + e), w = q * q;
+    constexpr float kLog2eLow = 1.4426950408889634 - double(kLog2e);
+    const float a = fminf(fabsf(v), 128.0f), h = a * -kLog2e, l = fmaf(a, -kLog2eLow, fmaf(a, -kLog2e, -h)), e0 = __builtin_amdgcn_exp2f(h);
+    const float e = fmaf(e0 * l, 0.6931471805599453f, e0), q = e * __builtin_amdgcn_rcpf(2.0f + e), w = q * q;
     float s = fmaf(w, 2.0f / 15, 2.0f / 13);
     s = fmaf(w, s, 2.0f / 11);
     s = fmaf(w, s, 2.0f / 9);
@@ -21,7 +24,7 @@ __device__ __forceinline__ float ssm_softplus(const SsmParams &p, float v) {
     s = fmaf(w, s, 2.0f / 5);
     s = fmaf(w, s, 2.0f / 3);
     s = fmaf(w, s, 2.0f);
-    return fmaf(q, s, v > 0.0f ? v : 0.0f);
+    return fmaf(q, s, v < 0.0f ? 0.0f : v);            // (NaN stays)
 }
 __device__ __forceinline__ float ssm_clamp(const SsmParams &p, float d) {
     d = d < p.dt_min ? p.dt_min : d;   // (NaN stays)

@@ -1,0 +1,75 @@
+"""The step sizes: how exact the softplus is, and what a step of 0 does."""
+import pytest
+import torch
+
+import causal_depthwise_short_conv1d_amd as S
+from tests import ssm_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+F64 = torch.float64
+U = 2.0 ** -24
+
+
+def scan(form, x, dt, A, B, C, state, T=None, **kw):
+    """ssm_fwd_varlen over sequences of T tokens, or (T None) ssm_update; everything on the CPU, the state too."""
+    st = state.to(DEV)
+    if T is None:
+        out = S.ssm_update(*(t.to(DEV) for t in (x, dt, A, B, C)), st, **kw)
+    else:
+        n = x.shape[0] // T
+        qsl = (torch.arange(n + 1) * T).to(torch.int32).to(DEV)
+        out = S.ssm_fwd_varlen(*(t.to(DEV) for t in (x, dt, A, B, C)), st, qsl, None, torch.ones(n, dtype=torch.bool, device=DEV), **kw)
+    return out.cpu(), st.cpu()
+
+
+# a token at a time (decode, a prompt of one token), in chunks, a thread a channel
+KERNELS = [("head", None), ("head", 1), ("head", 70), ("channel", None), ("channel", 1), ("channel", 24)]
+
+
+def inputs(form, T, n, H, P, N):
+    """x and B of 1 in the last token and of 0 before it, C of 0; (n T, ..), or (n, ..) for decode."""
+    rows = n * (T or 1)
+    last = torch.zeros(n, T or 1, dtype=BF)
+    last[:, -1] = 1
+    last = last.view(rows, 1, 1)
+    if form == "head":
+        return last.expand(rows, H, P).contiguous(), last.expand(rows, 1, N).contiguous(), torch.zeros(rows, 1, N, dtype=BF)
+    return last[:, 0].expand(rows, H * P).contiguous(), last.expand(rows, 1, N).contiguous(), torch.zeros(rows, 1, N, dtype=BF)
+
+
+@pytest.mark.parametrize("form,T", KERNELS)
+def test_softplus(form, T):
+    """The state after one written token of x = B = 1 is the step size itself.
+
+    Roundings of u = 2^-24, relative to log(1 + e^v): 3 of e^-|v| (two of the exponential, one of what its argument's second part
+    adds), 1 of 2 + e, 2 of its reciprocal, 1 of the quotient, 2 of the series, 1 of the sum; what lies below 2^-126 may be 0."""
+    H, P, N, n = (64, 4, 8, 40) if form == "head" else (1, 256, 8, 10)
+    v = torch.linspace(-87, 30, 2560)
+    x, B, C = inputs(form, T, n, H, P, N)
+    k = 2560 // n
+    dt = torch.zeros(n, T or 1, k)
+    dt[:, -1] = v.view(n, k)
+    dt = dt.view(-1, k)
+    A = -torch.ones(H) if form == "head" else -torch.ones(P, N)
+    shape = (n, H, P, N) if form == "head" else (n, P, N)
+    _, st = scan(form, x, dt, A, B, C, torch.zeros(shape), T, dt_softplus=True)
+    want = torch.logaddexp(v.to(F64), torch.zeros(2560, dtype=F64)).view((n, H, 1, 1) if form == "head" else (n, P, 1)).expand(shape)
+    R.check(st, want, 10 * U * want + 2.0 ** -126, "step")
+
+
+@pytest.mark.parametrize("form,T", KERNELS)
+def test_softplus_far_out(form, T):
+    H, P, N, n = (4, 4, 8, 1) if form == "head" else (1, 4, 8, 1)
+    v = torch.tensor([-float("inf"), -1e30, 1e30, 3e38])
+    x, B, C = inputs(form, T, n, H, P, N)
+    dt = torch.zeros(T or 1, 4)
+    dt[-1] = v
+    A = -torch.ones(H) if form == "head" else -torch.ones(P, N)
+    shape = (n, H, P, N) if form == "head" else (n, P, N)
+    _, st = scan(form, x, dt, A, B, C, torch.zeros(shape), T, dt_softplus=True)
+    assert torch.equal(st, v.clamp(min=0).view((n, H, 1, 1) if form == "head" else (n, P, 1)).expand(shape))
+    dt[-1] = float("nan")
+    _, st = scan(form, x, dt, A, B, C, torch.zeros(shape), T, dt_softplus=True)
+    assert torch.isnan(st).all()
