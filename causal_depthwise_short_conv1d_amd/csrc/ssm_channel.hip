@@ -19,6 +19,8 @@
 // exponentials are about 30, the softplus 22 and the wait for x, dt and z 36.
 // B and C in scalar registers took as long as from LDS; more waves a SIMD than
 // four spill.
+#include <float.h>
+
 #include <type_traits>
 
 #include "ssm_device.h"
@@ -98,11 +100,11 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
     const int64_t piece = int64_t(gb) * (kThreads / 64) + wave;
     Piece<NP> *pieces = static_cast<Piece<NP> *>(ws);
     float S[NP], a[NP];
-    bool up = true;                    // no decay that grows with the step
+    bool up = true;                    // no decay that grows with the step, and none that is infinite
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         a[n] = n < p.N ? p.A.p[g * p.A.sh + cc * p.A.sd + n * p.A.sn] * kLog2e : 0.0f;
-        up = up && !(a[n] > 0.0f);
+        up = up && a[n] <= 0.0f && a[n] >= -FLT_MAX;
         S[n] = 0.0f;
     }
     const bool plain = __builtin_amdgcn_ballot_w64(!up) == 0;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(kThreads, NP <= 16 ? 4 : 2) void ssm_channel_kernel
                 }
             };
             if (plain) states([&](float an) { return __builtin_amdgcn_exp2f(su * an); });
-            else states([&](float an) { const float v = s * an; return __builtin_amdgcn_exp2f(v > 0.0f ? 0.0f : v); });
+            else states([&](float an) { const float v = s == 0.0f ? 0.0f : s * an; return __builtin_amdgcn_exp2f(v > 0.0f ? 0.0f : v); });
             if constexpr (kOut) {
                 float o = fmaf(D, xf, y[0] + y[1]);
                 if (zp) o = ssm_gate(o, __uint_as_float(zk << 16));
@@ -280,7 +282,7 @@ __global__ __launch_bounds__(256) void ssm_channel_pass_kernel(SsmParams p, int3
         for (int k = 0; k < kFew; ++k) {
             if (i + k + 1 >= ns) break;
             at[(i + k) * per_slot].S[n][lane] = S;
-            S = fmaf(__builtin_amdgcn_exp2f(a * sum[k]), S, own[k]);
+            S = fmaf(__builtin_amdgcn_exp2f(sum[k] == 0.0f ? 0.0f : a * sum[k]), S, own[k]);
         }
     }
     if (ns > 1) at[(ns - 1) * per_slot].S[n][lane] = S;

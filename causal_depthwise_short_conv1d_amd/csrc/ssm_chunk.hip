@@ -348,7 +348,7 @@ struct Wave {
         const int lane = fresh();
         float d = ssm_clamp(p, ssm_softplus(p, __uint_as_float(dt.hi << 16 | (p.dt_fp32 ? dt.lo : 0u)) + bias));
         if (c * kC + lane >= job.n) d = 0.0f;
-        float g = d * A;
+        float g = d == 0.0f ? 0.0f : d * A;            // (A may be infinite)
         g = g > 0.0f ? 0.0f : (g < -200.0f ? -200.0f : g);         // e^-200 is 0, as of anything below
         double G = double(g) * 1.4426950408889634;
         G = dpp_add64<0x111, 0xf>(G);                  // row_shr 1, 2, 4, 8, then the rows' last values

@@ -36,10 +36,11 @@ __device__ __forceinline__ float ssm_step(const SsmParams &p, int64_t at, float 
     return ssm_clamp(p, ssm_softplus(p, d + bias));
 }
 
-// e^(d A), at most 1 (NaN stays).  The argument's rounding moves the result by |d A| e^(d A) 2^-24, which is below 2^-25:
-// what a state keeps is right to that share of the state.
+// e^(d A), at most 1 (NaN stays), and 1 for a step of 0 whatever A is.  Three roundings reach the argument (the product's with A,
+// log2(e)'s and the product's with it), which move the result by 3 |d A| e^(d A) 2^-24 at most, below 2^-23.8: what a state
+// keeps is right to that share of the state, and to the exponential's own.
 __device__ __forceinline__ float ssm_decay(float d, float A) {
-    const float g = d * A;
+    const float g = d == 0.0f ? 0.0f : d * A;
     return __builtin_amdgcn_exp2f((g > 0.0f ? 0.0f : g) * kLog2e);
 }
 

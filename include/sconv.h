@@ -591,7 +591,8 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  *     d = dt + dt_bias;  d = softplus(d) when dt_softplus is non-zero;
  *     d = min(max(d, dt_min), dt_max)
  *     S <- e^(d A) S + d x B;   y = sum S C + D x;   y <- y silu(z)
- * d A is at most 0; a larger value counts as 0.  Two forms, told apart by
+ * d A is at most 0; a larger value counts as 0, and so does a step of 0 times
+ * any A.  Two forms, told apart by
  * strides: one step size and one decay a head (dt, dt_bias and A of channel
  * stride 0, A of state stride 0), or one step size a channel and one decay a
  * channel and state.  Steps, decays, the state and all sums are in fp32 or

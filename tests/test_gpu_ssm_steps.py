@@ -73,3 +73,39 @@ def test_softplus_far_out(form, T):
     dt[-1] = float("nan")
     _, st = scan(form, x, dt, A, B, C, torch.zeros(shape), T, dt_softplus=True)
     assert torch.isnan(st).all()
+
+
+# (form, lengths or None for decode): a token at a time, chunks of which a part is empty, segments some of which have no step
+# at all, a thread a channel, its segments
+FORGETFUL = [("head", 3, 64, 1, 32, None), ("head", 3, 64, 1, 32, [2, 3, 1]), ("head", 3, 64, 1, 32, [70, 5, 129]), ("head", 2, 32, 1, 64, [90]),
+             ("head", 2, 64, 1, 32, [1300]), ("head", 2, 16, 1, 160, [40]), ("channel", 1, 70, 1, 16, None),
+             ("channel", 2, 20, 2, 20, [2, 1]), ("channel", 1, 70, 1, 16, [70, 5, 129]), ("channel", 1, 70, 1, 5, [1300])]
+
+
+@pytest.mark.parametrize("form,H,P,G,N,lens", FORGETFUL)
+def test_decays_of_minus_infinity(form, H, P, G, N, lens):
+    """A step forgets everything, a step of 0 (and what lies behind a sequence's end) nothing.  In 64 bits e^(-10^6 d) is 0 as well
+    for every other step here, which is 0.01 or more."""
+    rows = (5, 2) if lens is None else (sum(lens),)
+    d = R.draw(rows, form, H, P, G, N, 7, raw=False)
+    g = torch.Generator().manual_seed(8)
+    d["dt"] = torch.where(torch.rand(d["dt"].shape, generator=g) < 0.4, 0.0, d["dt"].clamp(min=0.01))
+    if lens and lens[0] > 500:
+        d["dt"][150:450] = 0
+    d["A"].view(-1)[::3] = -1e6
+    shape = (5 if lens is None else len(lens), H, P, N) if form == "head" else (5 if lens is None else len(lens), H * P, N)
+    state = torch.randn(shape, generator=g)
+    st = state.to(DEV)
+    k = R.on(d, DEV)
+    k["A"].view(-1)[::3] = -float("inf")
+    args = (k["x"], k["dt"], k["A"], k["B"], k["C"], st)
+    if lens is None:
+        o, otol, s, stol, _ = R.update(d, state, None, None, None)
+        out = S.ssm_update(*args, D=k["D"])
+    else:
+        qsl = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32)
+        has = torch.ones(len(lens), dtype=torch.bool)
+        o, otol, s, stol, _ = R.fwd(d, state, qsl, None, has)
+        out = S.ssm_fwd_varlen(*args, qsl.to(DEV), None, has.to(DEV), D=k["D"])
+    R.check(out, o, otol, "out")
+    R.check_state(st, s, stol)
