@@ -478,7 +478,8 @@ struct Wave {
         for (int k = 0; k < 4; ++k) r.v[k] = row4((DIAG ? f.v + 32 * half : f.vx) + 8 * k + 4 * (lane >> 5));
         return r;
     }
-    // The scores times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).
+    // The scores times e^(G_i - G_j) d_j.  DIAG: of one half (masked, D on the diagonal).  What is masked is 0, not a score
+    // times 0: a later token's B may not be finite.
     template <bool DIAG>
     __device__ __forceinline__ Scores weigh(const f32x16 &s, int half, const Weights &g, bool plain, const Factors &f, float D) {
         const int lane = fresh(), n = lane & 31, hh = lane >> 5;
@@ -493,7 +494,7 @@ struct Wave {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float a = (ih - jh[e]) + (il - jl[e]), d = g.v[k][e] * __builtin_amdgcn_exp2f(a > 0.0f ? 0.0f : a);
-                    v[4 * k + e] = s[4 * k + e] * (8 * k + e <= i ? d : 0.0f);
+                    v[4 * k + e] = 8 * k + e <= i ? s[4 * k + e] * d : 0.0f;
                 }
             }
         } else {
@@ -501,7 +502,7 @@ struct Wave {
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    v[4 * k + e] = s[4 * k + e] * g.u * (!DIAG || 8 * k + e <= i ? g.v[k][e] : 0.0f);
+                    v[4 * k + e] = !DIAG || 8 * k + e <= i ? s[4 * k + e] * g.u * g.v[k][e] : 0.0f;
         }
         if constexpr (DIAG) {
 #pragma unroll
