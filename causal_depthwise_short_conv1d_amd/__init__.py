@@ -930,7 +930,7 @@ def ssm_fwd_varlen(x, dt, A, B, C, state, query_start_loc, cache_indices=None, h
     fp32; A, D, dt_bias and state fp32; D, z (like x), dt_bias and state may be None.  dt_limit: (least, largest) step size.
     A decay d A above 0 counts as 0.  query_start_loc int32 (batch+1,), cache_indices int32 (batch,) or None,
     has_initial_state bool (batch,) or None: as for conv1d_fwd_varlen.  state is updated in place.  Returns out, like x;
-    rows of padded sequences are left as they are.  Calls of few heads and long sequences take a workspace of up to 80 MB for
+    rows of padded sequences are left as they are.  Calls of few heads and long sequences take a workspace of up to 87 MB for
     the time of the call; where memory for it is short, a call takes a slower form that needs none."""
     dev = x.device
     index = x.get_device()

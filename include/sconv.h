@@ -651,8 +651,8 @@ int sconv_verify_drafts(const int32_t *draft_tokens, const int32_t *draft_start_
  *              that walk all segments of their sequences at once; without it
  *              they take one, several times as long.  Smaller than asked for ->
  *              SCONV_ERR_SHAPE.  It holds the segments' states, and does not grow
- *              with the call: 45 MB at most, 80 MB with one decay a channel and
- *              64 states (19 MB with 16).
+ *              with the call: 51 MB at most, with one decay a channel and state
+ *              24 MB up to 16 states, 45 MB up to 32, 87 MB up to 64.
  */
 int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, int64_t x_stride_dim,
                    const void *dt, int64_t dt_stride_tok, int64_t dt_stride_head, int64_t dt_stride_dim, int32_t dt_fp32,
