@@ -200,9 +200,12 @@ int ssm_fwd_varlen(const void *x, int64_t x_stride_tok, int64_t x_stride_head, i
     if (rc != SCONV_OK) return rc;
     p.per_group = p.H / p.G;
     const int64_t T = total_tokens;
-    // A chunk takes as long as five tokens or so, one after the other: 64 sequences of 4 tokens, 128 heads, 129 us a token at a
-    // time and 160 in chunks, of 8 tokens 218 and 163; 16 sequences of 4 tokens 37 and 45.
-    if (layout.head && p.N <= kSsmMaxChunkN && (T > 5 * int64_t(batch) || batch == 1)) {
+    // A chunk takes as long as six tokens, one after the other, and where a token's rows do not fill the chip as long as ten or
+    // twelve.  us a token at a time / in chunks, heads of 64 x 128: 128 heads, 64 sequences of 6 tokens 188 / 191, 8 tokens
+    // 234 / 195; 16 sequences of 6 tokens 48 / 50, of 8 57 / 50; 4 sequences of 10 tokens 17.1 / 18.2, of 12 20.0 / 18.2; one of 1
+    // token 4.8 / 15.3, 10 tokens 13.0 / 15.6, 16 18.5 / 15.7; 8 heads, 64 sequences of 10 tokens 17.0 / 19.8, of 16 24.6 / 19.5.
+    const int64_t few = int64_t(batch) * p.H <= 512 ? 10 : 6;
+    if (layout.head && p.N <= kSsmMaxChunkN && T > few * batch) {
         const SsmPlan plan = ssm_plan(T, batch, p.H, p.G, p.P, p.N, workspace != nullptr);
         const int64_t places = (plan.seg ? plan.slots : batch) + 7;
         if (places <= kMaxThreads / (64 * kSsmWaves) / plan.groups && plan.groups <= INT32_MAX) {
