@@ -700,11 +700,10 @@ __device__ __forceinline__ int64_t first_slot(const SsmParams &p, int32_t b, int
     return a / (int64_t(kC) * seg) + b;
 }
 
-struct alignas(16) Raw { float v[4]; };
-
-// PAIR: two waves a block of 64 channels of a head, which share its scores; otherwise a wave for up to 32 channels.
+// PAIR: two waves a block of 64 channels of a head, which share its scores; otherwise a wave for up to 32 channels.  Eight waves
+// fill a CU two to a SIMD; calls that take fewer have a CU or more a workgroup.
 template <int NT, int W, bool PAIR, bool VEC, Mode MODE>
-__global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
+__global__ __launch_bounds__(64 * W, W == kSsmWaves ? 2 : 1) void ssm_chunk_kernel(SsmParams p, int32_t blocks, int32_t units, int32_t pbs,
                                                                           int64_t places, int32_t seg, float *states, float *decays,
                                                                           bool svec) {
     constexpr int U = 4 * NT, kBC = kC * U * 8, kUnits = PAIR ? W / 2 : W;
@@ -766,7 +765,7 @@ __global__ __launch_bounds__(64 * W, 2) void ssm_chunk_kernel(SsmParams p, int32
 
     const int half = PAIR ? wave / kUnits : 0, own = PAIR ? wave % kUnits : wave;
     const int32_t unit = block * kUnits + own;
-    const bool work = unit < units, first = half == 0, second = !PAIR || half == 1;
+    const bool work = unit < units, first = half == 0;
     const int32_t h = job.group * p.per_group + (work ? unit / pbs : 0), pb = work ? unit % pbs : 0;
     Wave<NT, VEC> wv{p, job, lane, h, (PAIR ? 64 : 32) * pb + 32 * half};
     uint16_t *sc = scores[kOut && PAIR ? own : 0];
