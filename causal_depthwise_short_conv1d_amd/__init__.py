@@ -915,7 +915,7 @@ def _limits(dt_limit):
     if dt_limit is None:
         return -_INF, _INF
     lo, hi = dt_limit
-    return float(lo), float(hi)
+    return ctypes.c_float(lo).value, ctypes.c_float(hi).value      # (what fp32 does not hold is no limit)
 
 
 def ssm_fwd_varlen(x, dt, A, B, C, state, query_start_loc, cache_indices=None, has_initial_state=None, D=None, z=None,
