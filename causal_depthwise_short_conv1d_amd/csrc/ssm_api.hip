@@ -95,8 +95,8 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
     plan.groups = G * ((waves + kSsmWaves - 1) / kSsmWaves);
     // A place takes a CU a workgroup.  Segments walk all of a sequence at once, but walk it twice, and the first walk and the
     // pass behind it cost some 25 us: with at most 64 workgroups, from ten chunks a sequence on.  us with / without, 128 heads of
-    // 64 x 128 (32 workgroups a sequence): 256 tokens 42 / 28, 512 55 / 48, 1024 59 / 86; 2 sequences of 1024 90 / 94, 3 110 / 97,
-    // 3 of 4096 335 / 337, 5 of 1024 176 / 128; 64 heads: 256 tokens 39 / 27, 512 44 / 47.
+    // 64 x 128 (32 workgroups a sequence): 256 tokens 45 / 32, 512 53 / 54, 640 54 / 65, 1024 60 / 98; 2 sequences of 1024 85 / 100,
+    // 3 108 / 102, 3 of 4096 343 / 357, 5 of 1024 189 / 129; 64 heads: 256 tokens 40 / 31, 512 45 / 52.
     const int64_t chunks = T / kSsmChunk + batch, mean = T / kSsmChunk / batch;
     if (workspace && batch * plan.groups <= 64 && mean >= 10) {
         int64_t seg = (chunks * plan.groups + 255) / 256;
@@ -115,7 +115,7 @@ SsmChannelPlan ssm_channel_plan(int64_t T, int64_t batch, int32_t G, int32_t P, 
     plan.np = N <= 16 ? 16 : (N <= 32 ? 32 : 64);
     plan.groups = G * ((int64_t(P) + kSsmChannels - 1) / kSsmChannels);
     // Four workgroups a CU hide what each waits for.  us with segments / without, 8192 channels (32 workgroups a sequence): 128
-    // tokens 47 / 66, 1024 103 / 475, 4 sequences of 512 156 / 245, 8 266 / 247, 12 438 / 313; 64 tokens 45 / 38.
+    // tokens 46 / 65, 1024 100 / 467, 4 sequences of 512 154 / 242, 8 265 / 243, 12 438 / 307; 64 tokens 44 / 37.
     const int64_t mean = T / batch;
     if (workspace && batch * plan.groups <= 128 && mean >= 128) {
         int64_t seg = (T * plan.groups + 1023) / 1024;

@@ -8,17 +8,21 @@
 // tokens at a time, while the eight before are computed.  Nothing is exchanged.
 //
 // A state costs four products or sums and an exponential a token, and a channel
-// the step's softplus: some 100 vector instructions a token for 16 states.  Where a
+// the step's softplus: for 16 states 114 vector instructions a token in the walk for
+// the states alone, 138 in the one for the outputs.  Where a
 // call's channels and sequences do not fill the chip, sequences are cut into
 // segments that are walked twice at once: for the states at their ends, from
 // empty ones, then, once a pass over the segments has joined these, for the outputs.
 //
 // Bound by the vector instructions, of which an exponential takes as long as two:
-// 4195 tokens of 8192 channels with 16 states take 119 us for the states, 12 for the
-// pass and 147 for the outputs, of which, by leaving each out in turn, the
-// exponentials are about 30, the softplus 22 and the wait for x, dt and z 36.
+// 4195 tokens of 8192 channels with 16 states take 124 us for the states, 12 for the
+// pass and 151 for the outputs, of which, by leaving each out in turn, the
+// exponentials are about 30, the softplus 26 (4 of them its exponent's second part,
+// by what it added) and the wait for x, dt and z 36.
 // B and C in scalar registers took as long as from LDS; more waves a SIMD than
-// four spill.
+// four spill, and so do 33 to 64 states with two (12 to 90 registers in scratch
+// memory: 4195 tokens of 4096 channels 184 us with 16 states, 318 with 32, 731 with
+// 64, and 4741 a token at a time with 128).
 #include <float.h>
 
 #include <type_traits>

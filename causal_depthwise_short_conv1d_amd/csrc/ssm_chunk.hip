@@ -25,18 +25,20 @@
 // (e^(..) d x, S, the scores) is split into three bf16 parts, which hold all of
 // its 24 bits and have fp32's range.  All sums are fp32, G is fp64.
 //
-// Bound by the issue of instructions: of a chunk's 17 K cycles the two waves of a
-// SIMD have 6.7 K of matrix products (32 cycles each) and 7 K of vector
+// Bound by the issue of instructions: of a chunk's 19.5 K cycles the two waves of a
+// SIMD have 8.1 K of matrix products (32 cycles each) and 8.6 K of vector
 // instructions, mostly splits, scalings and decays (64 sequences of up to 2048
-// tokens, 64 heads of 64 x 128: 36 and 47 % of all cycles, LDS 26 %, 531 us for
-// 1.4 GB).  Hence one wave's scores and decays serve two, parts are cut off by
-// logical instructions (4 cycles, v_cvt_pk_bf16_f32 6.5) and vector instructions
-// are put between the products.  128 x 32 states and what a wave has in flight fill
-// its 256 registers, two waves a SIMD; 64 tokens are the most whose x, B and C
-// lie twice in the LDS beside the scores.  Few long sequences are walked in
-// segments, twice: 14807 tokens of 128 heads 103 us for the states at the segments'
-// ends, 12 to join them, 242 for the outputs (4195 tokens: 39, 12, 82).  128
-// tokens of 64 heads take 17.6 us in workgroups of two waves.
+// tokens, 64 heads of 64 x 128: 38 and 51 % of all cycles, the products' issue
+// among the latter; LDS 25 %, a third of it bank conflicts; 616 us for 1.4 GB).
+// Hence one wave's scores and decays serve two, parts are cut off by logical
+// instructions (4 cycles, v_cvt_pk_bf16_f32 6.5) and vector instructions are put
+// between the products.  128 x 32 states and what a wave has in flight fill its
+// 256 registers, two waves a SIMD; 64 tokens are the most whose x and B come
+// beside the last ones' while C and the scores lie in the LDS.  Few long
+// sequences are walked in segments, twice: 14807 tokens of 128 heads 103 us for the
+// states at the segments' ends, 12 to join them, 286 for the outputs (4195
+// tokens: 40, 12, 96).  128 tokens of 64 heads take 20.0 us in workgroups of two
+// waves.
 #include "ssm_device.h"
 
 namespace sconv {

@@ -89,7 +89,7 @@ SsmPlan ssm_plan(int64_t T, int64_t batch, int32_t H, int32_t G, int32_t P, int3
 
 constexpr int kSsmTokens = 8;          // of a block of the channel kernel
 constexpr int kSsmChannels = 256;      // of its workgroups
-constexpr int kSsmMaxChannelN = 64;    // states a channel that it holds in registers
+constexpr int kSsmMaxChannelN = 64;    // states a channel that it takes: up to 32 in registers, more partly in scratch memory
 
 // How the channel kernel takes a call: states rounded up, and whether sequences are cut into segments of `seg` tokens.
 struct SsmChannelPlan {
